@@ -89,14 +89,15 @@ typedef enum {
   FLCE_OK = 0,
   FLCE_ERR_NULL_POINTER = 1,      /* a required pointer is NULL */
   FLCE_ERR_BAD_SHAPE = 2,         /* N < 0, H < 1, V < 1, or a size beyond the limits below */
-  FLCE_ERR_BAD_REDUCTION = 3,     /* reduction not FLCE_REDUCTION_NONE / _MEAN / _SUM */
+  FLCE_ERR_BAD_REDUCTION = 3,     /* reduction not one that the call takes */
   FLCE_ERR_MISALIGNED = 4,        /* see "Alignment" above */
   FLCE_ERR_WORKSPACE_TOO_SMALL = 5,
   FLCE_ERR_BAD_SOFTCAP = 6,       /* softcap is NaN or infinite */
   FLCE_ERR_HIP = 7,               /* a HIP runtime call or kernel launch failed */
   FLCE_ERR_INVALID_LABEL = 8,     /* reported only by flce_get_status */
   FLCE_ERR_BAD_OPTION = 9,        /* z_loss_scale negative or not finite, unknown grad_dtype,
-                                   * class_weight under NONE, entropy_per_token not 0 or 1 */
+                                   * class_weight under NONE, entropy_per_token not 0 or 1; an
+                                   * embedding, policy or preference option outside its range */
   FLCE_ERR_TOO_LARGE = 10         /* flce_forward_noalloc: the shape needs more scratch than
                                    * FLCE_NOALLOC_SCRATCH_BYTES */
 } flce_status_t;
@@ -377,8 +378,198 @@ flce_status_t flce_forward_backward(const void* hidden, const void* weight, cons
                                     float* reduced, void* grad_hidden, void* grad_weight,
                                     void* workspace, size_t workspace_bytes, void* stream);
 
-/* Reads the status word that the last flce_forward / flce_backward /
- * flce_forward_backward on this workspace left, after synchronising `stream`. *invalid_labels (may be NULL)
+/* ---- Embedding lookup and its gradient ----------------------------------------
+ * The input end of the vocabulary matrix: for token ids x_i
+ *   hidden_i = scale * E[x_i],     dE[v] = scale * sum_{i : x_i = v} grad_hidden_i,
+ * where E[v] is row v of a table [V,H] (FLCE_EMBED_VH) or column v of a weight
+ * [H,V] (FLCE_EMBED_HV: the head's own weight, so that a model with tied
+ * embeddings keeps one matrix; Gemma2-style models scale by sqrt(H)).
+ * A token equal to ignore_index, or outside [0, V_total), gives a zero row and
+ * takes part in no gradient; the latter are counted in the workspace's status
+ * word (flce_get_status). A vocabulary slice [v_begin, v_begin + Vs) of V_total
+ * ids gives zero rows for the ids of other slices, so that the sum of the
+ * slices' outputs is the whole lookup (an all-reduce across GPUs), and the
+ * slice's own gradient; unsharded calls pass Vs = V_total, v_begin = 0.
+ * Every product is formed and every sum accumulated in fp32, in an order that
+ * depends on the inputs only (no atomics), and rounded once to the output type. */
+enum { FLCE_EMBED_VH = 0, FLCE_EMBED_HV = 1 };
+
+typedef struct flce_embedding_options {
+  int64_t ignore_index;  /* token id that marks a skipped position */
+  double scale;          /* finite; used as fp32 */
+  int layout;            /* FLCE_EMBED_VH or FLCE_EMBED_HV */
+  int hidden_dtype;      /* FLCE_GRAD_BF16 or FLCE_GRAD_F32: type of the backward's grad_hidden
+                          * (the forward reads and writes bf16 whatever it says) */
+  int grad_dtype;        /* FLCE_GRAD_BF16 or FLCE_GRAD_F32: type of grad_weight */
+  int accumulate;        /* 0: grad_weight is written whole (zero for unused ids);
+                          * 1: the gradient is added to what grad_weight holds, e.g. the head's
+                          * grad_weight of a tied matrix (only used ids are touched) */
+} flce_embedding_options_t;
+
+/* Workspace bytes of the two calls for Vs ids (host only; either out-pointer
+ * may be NULL). */
+flce_status_t flce_embedding_workspace_size(int64_t N, int64_t H, int64_t Vs,
+                                            const flce_embedding_options_t* opt, size_t* fwd_bytes,
+                                            size_t* bwd_bytes);
+
+/* hidden device bf16 [N,H] from weight device bf16 ([Vs,H] or [H,Vs]) and
+ * tokens device int64 [N]. H must be a multiple of 8; Vs may take any value.
+ * weight, hidden and workspace 16-byte aligned. */
+flce_status_t flce_embedding_forward(const void* weight, const int64_t* tokens, int64_t N,
+                                     int64_t H, int64_t Vs, int64_t v_begin, int64_t V_total,
+                                     const flce_embedding_options_t* opt, void* hidden,
+                                     void* workspace, size_t workspace_bytes, void* stream);
+
+/* grad_weight device ([Vs,H] or [H,Vs], type grad_dtype) from grad_hidden
+ * device [N,H] (type hidden_dtype). grad_hidden, grad_weight and workspace
+ * 16-byte aligned. */
+flce_status_t flce_embedding_backward(const void* grad_hidden, const int64_t* tokens, int64_t N,
+                                      int64_t H, int64_t Vs, int64_t v_begin, int64_t V_total,
+                                      const flce_embedding_options_t* opt, void* grad_weight,
+                                      void* workspace, size_t workspace_bytes, void* stream);
+
+/* ---- Losses on the head's per-token outputs -------------------------------------
+ * The losses that an RL or preference fine-tuning step forms between the head's
+ * forward (per-token logprob and entropy) and its backward (per-token upstream
+ * gradients). All take the packed batch the head takes: N tokens, labels with
+ * ignore_index (and ids outside [0, V)) marking tokens without a loss, and B
+ * sequences given by cu_seqlens, device int64 [B+1]: sequence s is the tokens
+ * [cu_seqlens[s], cu_seqlens[s+1]), which must not decrease and must lie in
+ * [0, N]. Tokens before the first and behind the last sequence take no part
+ * (gradient 0). What the per-token arrays hold at tokens that take no part is
+ * never used (it may be NaN or infinite).
+ * Every per-token term is computed, and every sum accumulated, in float64 in a
+ * fixed order; outputs are rounded once to fp32.
+ * A sequence whose offsets decrease or leave [0, N] makes the reduced loss, the
+ * statistics and every valid token's gradient NaN, and (preference) its pair's
+ * outputs; the results of the other sequences are then unspecified. The status
+ * word counts such sequences and the labels of sequences that are neither
+ * ignore_index nor in [0, V). */
+enum { FLCE_REDUCTION_SEQUENCE_MEAN = 3 };  /* flce_policy_loss_* only */
+enum { FLCE_KL_K1 = 0, FLCE_KL_K2 = 1, FLCE_KL_K3 = 2 };
+enum { FLCE_RATIO_TOKEN = 0, FLCE_RATIO_SEQUENCE = 1 };
+
+/* Clipped policy loss with a KL term. With d = logprob - old_logprob (under
+ * FLCE_RATIO_SEQUENCE its mean over the sequence's valid tokens), r = exp(d) and
+ * the advantage A, a valid token's loss is
+ *   policy = 0 where A = 0, else
+ *   policy = -min(r A, clamp(r, 1 - clip_low, 1 + clip_high) A), and where A < 0
+ *            and dual_clip > 0 at most -dual_clip A,
+ *   loss   = policy + kl_coef kl - entropy_coef entropy,
+ *   kl(x)  = x (K1), x^2 / 2 (K2), exp(-x) + x - 1 (K3),  x = logprob - ref_logprob.
+ * A ratio exactly on a bound is not clipped. The gradient of a clipped policy
+ * term is zero. MEAN averages over the batch's valid tokens, SUM sums,
+ * SEQUENCE_MEAN averages within each sequence and then over the sequences that
+ * have a valid token. No valid token gives 0. */
+typedef struct flce_policy_options {
+  int64_t ignore_index;
+  double clip_low;      /* in [0, 1] */
+  double clip_high;     /* >= 0 */
+  double dual_clip;     /* 0: off, else > 1 */
+  double kl_coef;       /* needs ref_logprob unless 0 */
+  double entropy_coef;  /* needs entropy unless 0 */
+  int kl_estimator;     /* FLCE_KL_* */
+  int level;            /* FLCE_RATIO_*; SEQUENCE needs cu_seqlens and one advantage a sequence */
+  int reduction;        /* FLCE_REDUCTION_MEAN, _SUM or _SEQUENCE_MEAN */
+  int advantages_per_sequence; /* 0: advantages [N], 1: advantages [B] */
+} flce_policy_options_t;
+
+/* Workspace bytes of the two policy-loss calls that take one (host only). */
+flce_status_t flce_policy_workspace_size(int64_t N, int64_t B, size_t* bytes);
+
+/* logprob, old_logprob (and where given entropy, ref_logprob): device fp32 [N];
+ * advantages device fp32 [N] or [B]; labels device int64 [N]; cu_seqlens device
+ * int64 [B+1], or NULL with B = 1: one sequence of all tokens.
+ *   stats      device fp32 [8]: loss, policy, kl, entropy, share of clipped
+ *              tokens, -d (the k1 estimate of KL(old || new)), each reduced like
+ *              the loss; then the number of valid tokens and of sequences that
+ *              have one
+ *   seq_state  device float64 [B+1, 2]: what flce_policy_loss_backward needs */
+flce_status_t flce_policy_loss_forward(const float* logprob, const float* entropy,
+                                       const float* old_logprob, const float* ref_logprob,
+                                       const float* advantages, const int64_t* labels,
+                                       const int64_t* cu_seqlens, int64_t N, int64_t B, int64_t V,
+                                       const flce_policy_options_t* opt, float* stats,
+                                       double* seq_state, void* workspace, size_t workspace_bytes,
+                                       void* stream);
+
+/* grad_logprob, and unless NULL grad_entropy (device fp32 [N]), of
+ * grad_loss[0] * loss (device fp32 [1]; NULL means 1), from the inputs of the
+ * matching forward and its seq_state. */
+flce_status_t flce_policy_loss_backward(const float* logprob, const float* old_logprob,
+                                        const float* ref_logprob, const float* advantages,
+                                        const int64_t* labels, const int64_t* cu_seqlens,
+                                        int64_t N, int64_t B, int64_t V,
+                                        const flce_policy_options_t* opt, const double* seq_state,
+                                        const float* grad_loss, float* grad_logprob,
+                                        float* grad_entropy, void* stream);
+
+/* Both in one call, for an upstream gradient known in advance (one launch for
+ * small batches). The results are those of the
+ * two calls above. */
+flce_status_t flce_policy_loss_forward_backward(
+    const float* logprob, const float* entropy, const float* old_logprob, const float* ref_logprob,
+    const float* advantages, const int64_t* labels, const int64_t* cu_seqlens, int64_t N, int64_t B,
+    int64_t V, const flce_policy_options_t* opt, const float* grad_loss, float* stats,
+    float* grad_logprob, float* grad_entropy, void* workspace, size_t workspace_bytes,
+    void* stream);
+
+/* Preference loss over P pairs of sequences: sequence i < P is the chosen and
+ * sequence P + i the rejected answer of pair i (2 P sequences). With R_s the sum
+ * over the valid tokens of sequence s of logprob - ref_logprob (ref_logprob NULL:
+ * of logprob), divided by their number under length_normalize (an empty sequence
+ * has R = 0), and x = beta (R_chosen - R_rejected) - margin, a pair's loss is
+ *   SIGMOID  -(1 - eps) log sigmoid(x) - eps log sigmoid(-x),  eps = label_smoothing
+ *   HINGE    max(0, 1 - x)   (no gradient at x = 1)
+ *   IPO      (R_chosen - R_rejected - 1 / (2 beta))^2
+ * Every pair counts in the mean. */
+enum { FLCE_PREFERENCE_SIGMOID = 0, FLCE_PREFERENCE_HINGE = 1, FLCE_PREFERENCE_IPO = 2 };
+
+typedef struct flce_preference_options {
+  int64_t ignore_index;
+  double beta;             /* > 0 */
+  double label_smoothing;  /* in [0, 0.5]; SIGMOID only, else 0 */
+  double margin;           /* finite; SIGMOID and HINGE only, else 0 */
+  int kind;                /* FLCE_PREFERENCE_* */
+  int length_normalize;    /* 0 or 1 */
+  int reduction;           /* FLCE_REDUCTION_NONE, _MEAN or _SUM over the pairs */
+} flce_preference_options_t;
+
+/* Workspace bytes of the two preference-loss calls that take one (host only). */
+flce_status_t flce_preference_workspace_size(int64_t N, int64_t P, size_t* bytes);
+
+/* logprob, ref_logprob (may be NULL): device fp32 [N]; labels device int64 [N];
+ * cu_seqlens device int64 [2P+1].
+ *   pair_loss  device fp32 [P], written under every reduction
+ *   loss       device fp32 [1]; required unless reduction is NONE, ignored then
+ *   chosen_reward, rejected_reward  device fp32 [P]: beta R of the two sides
+ *   seq_state  device float64 [2P+1]: what flce_preference_loss_backward needs */
+flce_status_t flce_preference_loss_forward(const float* logprob, const float* ref_logprob,
+                                           const int64_t* labels, const int64_t* cu_seqlens,
+                                           int64_t N, int64_t P, int64_t V,
+                                           const flce_preference_options_t* opt, float* loss,
+                                           float* pair_loss, float* chosen_reward,
+                                           float* rejected_reward, double* seq_state,
+                                           void* workspace, size_t workspace_bytes, void* stream);
+
+/* grad_logprob device fp32 [N] for the upstream gradient grad_loss: device fp32
+ * [P] under NONE (NULL: ones), [1] otherwise (NULL: 1). */
+flce_status_t flce_preference_loss_backward(const int64_t* labels, const int64_t* cu_seqlens,
+                                            int64_t N, int64_t P, int64_t V,
+                                            const flce_preference_options_t* opt,
+                                            const double* seq_state, const float* grad_loss,
+                                            float* grad_logprob, void* stream);
+
+/* Both in one call. The results are those of the
+ * two calls above. */
+flce_status_t flce_preference_loss_forward_backward(
+    const float* logprob, const float* ref_logprob, const int64_t* labels,
+    const int64_t* cu_seqlens, int64_t N, int64_t P, int64_t V,
+    const flce_preference_options_t* opt, const float* grad_loss, float* loss, float* pair_loss,
+    float* chosen_reward, float* rejected_reward, float* grad_logprob, void* workspace,
+    size_t workspace_bytes, void* stream);
+
+/* Reads the status word that the last call with this workspace left, after synchronising `stream`. *invalid_labels (may be NULL)
  * receives the number of labels that were neither ignore_index nor in [0, V);
  * returns FLCE_ERR_INVALID_LABEL if that number is not 0, else FLCE_OK. */
 flce_status_t flce_get_status(const void* workspace, int64_t* invalid_labels, void* stream);

@@ -8,12 +8,16 @@ import subprocess
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
 LIB = os.path.join(PKG, "libflce.so")
-SOURCES = [os.path.join(PKG, "csrc", "flce_api.hip")]
+SOURCES = [os.path.join(PKG, "csrc", "flce_api.hip"), os.path.join(PKG, "csrc", "flce_ops.hip")]
 HEADERS = [os.path.join(ROOT, "include", "flce.h"),
            os.path.join(PKG, "csrc", "flce_layout.hpp"),
            os.path.join(PKG, "csrc", "flce_plan.hpp"),
            os.path.join(PKG, "csrc", "flce_gemm.hpp"),
-           os.path.join(PKG, "csrc", "flce_kernels.hpp")]
+           os.path.join(PKG, "csrc", "flce_kernels.hpp"),
+           os.path.join(PKG, "csrc", "flce_launch.hpp"),
+           os.path.join(PKG, "csrc", "flce_ops_plan.hpp"),
+           os.path.join(PKG, "csrc", "flce_losses.hpp"),
+           os.path.join(PKG, "csrc", "flce_embedding.hpp")]
 
 # Packed fp32 VALU forms are switched off for all device code.
 HIPCC_FLAGS = ["--offload-arch=gfx950", "-O3", "-std=c++17", "-shared", "-fPIC",

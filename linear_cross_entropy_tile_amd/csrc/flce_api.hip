@@ -1,5 +1,5 @@
-// Host side of libflce: argument checks, the launch plan, the workspace
-// layout, kernel launches and the optional per-kernel event timing.
+// Host side of the fused head in libflce: argument checks, the launch plan,
+// the workspace layout and kernel launches.
 // Declarations and their documentation: include/flce.h.
 #include <hip/hip_runtime.h>
 
@@ -7,99 +7,15 @@
 #include <cstdint>
 #include <cstdlib>
 #include <mutex>
-#include <new>
-#include <vector>
 
 #include "flce.h"
 #include "flce_kernels.hpp"
+#include "flce_launch.hpp"
 #include "flce_plan.hpp"
 
 namespace {
 
 using namespace flce;
-
-// ---- kernel timing hooks --------------------------------------------------------
-// flce_profile_read reports per kind in this order. K_PACK_WEIGHT no longer
-// launches (the weight's dH image is written by the logit tiles themselves);
-// its slot stays so that the indices of the later kinds do not move.
-enum Kind {
-  K_FWD_PREP, K_FWD_TILE, K_FWD_COMBINE, K_FWD_REDUCE, K_BWD_PREP, K_BWD_DLOGITS, K_BWD_DX,
-  K_BWD_DW, K_DW_REDUCE, K_FILL, K_PACK_WEIGHT, K_PACK_HIDDEN, K_DX_FINALIZE, K_FUSED_TILE,
-  K_FUSED_DLOGITS, K_BWD_DXDW, K_NUM
-};
-const char* kKindNames[K_NUM] = {"fwd_prep", "fwd_tile", "fwd_combine", "fwd_reduce", "bwd_prep",
-                                 "bwd_dlogits", "bwd_dx", "bwd_dw", "dw_reduce", "fill_zero",
-                                 "pack_weight", "pack_hidden", "dx_finalize", "fused_tile",
-                                 "fused_dlogits", "bwd_dxdw"};
-
-struct Pending {
-  int kind;
-  hipEvent_t a, b;
-};
-struct Profiler {
-  std::mutex mu;
-  bool on = false;
-  std::vector<Pending> pending;
-  std::vector<hipEvent_t> pool;
-  int64_t launches[K_NUM] = {};
-  double ms[K_NUM] = {};
-  hipEvent_t get() {
-    if (!pool.empty()) {
-      hipEvent_t e = pool.back();
-      pool.pop_back();
-      return e;
-    }
-    hipEvent_t e = nullptr;
-    if (hipEventCreate(&e) != hipSuccess) return nullptr;
-    return e;
-  }
-  void drain() {
-    for (auto& p : pending) {
-      float t = 0.f;
-      if (hipEventSynchronize(p.b) == hipSuccess && hipEventElapsedTime(&t, p.a, p.b) == hipSuccess) {
-        launches[p.kind] += 1;
-        ms[p.kind] += t;
-      }
-      pool.push_back(p.a);
-      pool.push_back(p.b);
-    }
-    pending.clear();
-  }
-};
-Profiler& prof() {
-  static Profiler* p = new Profiler();
-  return *p;
-}
-
-// Launches through `fn` on `st`, bracketed by events when timing is on.
-template <class F>
-flce_status_t launch(int kind, hipStream_t st, F fn) {
-  Profiler& P = prof();
-  hipEvent_t a = nullptr, b = nullptr;
-  const bool timed = P.on;
-  if (timed) {
-    std::lock_guard<std::mutex> g(P.mu);
-    a = P.get();
-    b = P.get();
-    if (a != nullptr) (void)hipEventRecord(a, st);
-  }
-  fn();
-  if (hipGetLastError() != hipSuccess) return FLCE_ERR_HIP;
-  if (timed && a != nullptr && b != nullptr) {
-    (void)hipEventRecord(b, st);
-    std::lock_guard<std::mutex> g(P.mu);
-    P.pending.push_back({kind, a, b});
-  }
-  return FLCE_OK;
-}
-
-#define FLCE_TRY(x)                    \
-  do {                                 \
-    const flce_status_t _s = (x);      \
-    if (_s != FLCE_OK) return _s;      \
-  } while (0)
-
-char* wsp(void* ws, size_t off) { return static_cast<char*>(ws) + off; }
 
 flce_status_t zero_fill(void* p, size_t bytes, hipStream_t st) {
   const int64_t n32 = (int64_t)(bytes / 4);
@@ -1118,16 +1034,18 @@ const char* flce_status_string(flce_status_t s) {
     case FLCE_OK: return "ok";
     case FLCE_ERR_NULL_POINTER: return "a required pointer is NULL";
     case FLCE_ERR_BAD_SHAPE: return "bad shape (need N >= 0, H >= 1, V >= 1 within limits)";
-    case FLCE_ERR_BAD_REDUCTION: return "reduction must be NONE (0), MEAN (1) or SUM (2)";
+    case FLCE_ERR_BAD_REDUCTION: return "reduction must be NONE (0), MEAN (1) or SUM (2) (policy loss: MEAN, SUM or SEQUENCE_MEAN (3))";
     case FLCE_ERR_MISALIGNED:
       return "pointers must be 16-byte aligned and H a multiple of 8";
-    case FLCE_ERR_WORKSPACE_TOO_SMALL: return "workspace smaller than flce_workspace_size";
+    case FLCE_ERR_WORKSPACE_TOO_SMALL:
+      return "workspace smaller than the call's workspace-size function returns";
     case FLCE_ERR_BAD_SOFTCAP: return "softcap must be finite";
     case FLCE_ERR_HIP: return "HIP runtime error or failed kernel launch";
     case FLCE_ERR_INVALID_LABEL: return "labels outside [0, V) that are not ignore_index";
     case FLCE_ERR_BAD_OPTION:
       return "z_loss_scale must be finite and >= 0; grad_dtype BF16 or F32; class_weight needs "
-             "MEAN or SUM; entropy_per_token 0 or 1";
+             "MEAN or SUM; entropy_per_token 0 or 1; embedding, policy and preference options "
+             "within the ranges of flce.h";
     case FLCE_ERR_TOO_LARGE:
       return "the call needs more scratch than flce_forward_noalloc's static buffer "
              "(FLCE_NOALLOC_SCRATCH_BYTES) holds; use flce_forward with a workspace";

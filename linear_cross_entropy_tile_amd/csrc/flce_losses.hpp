@@ -1,0 +1,635 @@
+// Kernels of the losses on the head's per-token outputs (gfx950): the clipped
+// policy loss with a KL term and the paired preference loss.
+//
+// Both are sums over ragged sequences of a packed batch, then a small formula a
+// sequence (or pair), then one gradient value a token:
+//   parts      every 64-lane wave takes a tile of 256 consecutive tokens, forms
+//              the per-token terms and sums them over each sequence's share of
+//              the tile. The share of sequence s in tile t goes to parts[s + t]:
+//              walking the batch, either s or t grows by one from a share to the
+//              next, so s + t names it uniquely and B + T slots hold them all,
+//              however the lengths are mixed.
+//   sequences  adds the shares of each sequence, forms its ratio / its pair's
+//              loss and gradient coefficient, and adds up the batch.
+//   gradients  one pass over the tokens with the coefficients.
+// Tiles and trees depend on the sizes alone and no atomics are used, so equal
+// inputs give equal bits. Terms and sums are float64: a difference of two
+// log-probabilities is exact there, a ratio next to a clip bound falls on the
+// side the definition gives (bounds are compared as logarithms), exp(-x) + x - 1
+// keeps its digits at small x, and sums over 2^21 tokens lose nothing. Each
+// output is rounded once, to fp32.
+//
+// What bounds them: below some 10^5 tokens the launches (hence one launch for
+// everything in small batches, three otherwise); at 2^21 tokens the bytes.
+#pragma once
+
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+#include "flce_ops_plan.hpp"
+
+namespace flce {
+
+// ---- sequences ------------------------------------------------------------------
+
+// Number of entries <= x among the n entries of the sorted array a, found by a
+// whole wave: 64 probes a step. For an array that is not sorted the result is
+// meaningless but lies in [0, n], and the loop ends (m shrinks every step).
+__device__ __forceinline__ int64_t wave_count_le(const int64_t* a, int64_t n, int64_t x) {
+  const int lane = threadIdx.x & 63;
+  int64_t lo = 0, m = n;
+  while (m > 0) {
+    const int64_t step = (m + 63) >> 6;
+    const int64_t p = lane * step + step - 1;
+    const bool le = p < m && a[lo + p] <= x;
+    const int64_t c = __popcll(__builtin_amdgcn_ballot_w64(le));
+    lo += c * step;
+    m = m - c * step < step - 1 ? m - c * step : step - 1;
+  }
+  return lo;
+}
+
+// The sequences that the tokens [t0, t1) can belong to: [s0, s1], empty (s1 < s0)
+// when all lie before the first or behind the last sequence.
+struct SeqRange {
+  int64_t s0, s1;
+};
+__device__ __forceinline__ SeqRange tile_sequences(const int64_t* cu, int64_t B, int64_t t0,
+                                                   int64_t t1) {
+  if (cu == nullptr) return {0, 0};
+  const int64_t a = wave_count_le(cu, B + 1, t0) - 1, b = wave_count_le(cu, B + 1, t1 - 1) - 1;
+  return {a < 0 ? 0 : a, b >= B ? B - 1 : b};
+}
+
+// Sequence of token t within [s0, s1], or -1 when it lies in none.
+__device__ __forceinline__ int64_t token_sequence(const int64_t* cu, const SeqRange& r, int64_t t) {
+  if (cu == nullptr) return 0;
+  int64_t lo = r.s0, hi = r.s1;
+  while (lo < hi) {
+    const int64_t mid = (lo + hi + 1) >> 1;
+    if (cu[mid] <= t)
+      lo = mid;
+    else
+      hi = mid - 1;
+  }
+  return lo <= r.s1 && cu[lo] <= t && t < cu[lo + 1] ? lo : -1;
+}
+
+__device__ __forceinline__ int64_t seq_begin(const int64_t* cu, int64_t s) {
+  return cu == nullptr ? 0 : cu[s];
+}
+__device__ __forceinline__ int64_t seq_end(const int64_t* cu, int64_t s, int64_t N) {
+  return cu == nullptr ? N : cu[s + 1];
+}
+
+__device__ __forceinline__ bool label_valid(int64_t y, int64_t ignore_index, int64_t V) {
+  return y != ignore_index && y >= 0 && y < V;
+}
+
+// ---- wave and block sums --------------------------------------------------------
+
+__device__ __forceinline__ double shfl_down_f64(double v, int d) { return __shfl_down(v, d, 64); }
+
+// What a share of a sequence, a sequence, and the batch sum up to: the loss's
+// own terms x[]; n valid tokens; c clipped tokens (of the batch: sequences with
+// a valid token); inv labels outside [0, V); bad offsets.
+template <int K>
+struct LossSum {
+  double x[K];
+  int n, c, inv, bad;
+  __device__ void clear() {
+#pragma unroll
+    for (int k = 0; k < K; ++k) x[k] = 0.0;
+    n = c = inv = bad = 0;
+  }
+  __device__ void add(const LossSum& o) {
+#pragma unroll
+    for (int k = 0; k < K; ++k) x[k] += o.x[k];
+    n += o.n;
+    c += o.c;
+    inv += o.inv;
+    bad += o.bad;
+  }
+  // Sum over each group of g lanes (a power of two), in its first lane.
+  __device__ void group_sum(int g) {
+    for (int d = g >> 1; d > 0; d >>= 1) {
+#pragma unroll
+      for (int k = 0; k < K; ++k) x[k] += __shfl_down(x[k], d, 64);
+      n += __shfl_down(n, d, 64);
+      c += __shfl_down(c, d, 64);
+      inv += __shfl_down(inv, d, 64);
+      bad += __shfl_down(bad, d, 64);
+    }
+  }
+};
+
+// Sum over the block, waves in order; every thread gets it. sh: one entry a wave.
+template <class S>
+__device__ __forceinline__ S block_total(S v, S* sh) {
+  const int nw = blockDim.x >> 6;
+  v.group_sum(64);
+  if ((threadIdx.x & 63) == 0) sh[threadIdx.x >> 6] = v;
+  __syncthreads();
+  S r;
+  r.clear();
+  for (int w = 0; w < nw; ++w) r.add(sh[w]);
+  __syncthreads();
+  return r;
+}
+
+// Orders this wave's LDS writes before its later LDS reads (other lanes').
+__device__ __forceinline__ void wave_lds_fence() {
+  __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+  __builtin_amdgcn_wave_barrier();
+  __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
+}
+
+// Everything the kernels of one call share; Loss is PolicyLoss or PreferenceLoss.
+template <class Loss>
+struct LossArgs {
+  typename Loss::In in;
+  typename Loss::Out out;
+  const int64_t* labels;
+  const int64_t* cu;            // [B+1], or null: one sequence of all tokens
+  int64_t N, B, V, ignore_index;
+  int64_t items;                // sequences, or pairs
+  int64_t tiles;
+  typename Loss::Share* parts;    // [B + tiles]
+  typename Loss::Share* seq_sum;  // [B]
+  typename Loss::Total* totals;   // [blocks of the sequences kernel]
+  int32_t* header;                // [0] invalid labels and offsets
+  double* state;                  // see Loss
+};
+
+// ---- the clipped policy loss --------------------------------------------------------
+
+struct PolicyLoss {
+  struct In {
+    const float *logprob, *old_logprob, *ref_logprob, *entropy, *advantages;
+    double over, under, dual;              // ratio bounds 1 + clip_high, 1 - clip_low, dual_clip
+    double log_over, log_under, log_dual;  // their logarithms (+-infinity where off)
+    double kl_coef, ent_coef;
+    int kl, by_sequence, adv_seq, reduction;
+  };
+  struct Out {
+    float* stats;            // [8]
+    const float* grad_loss;  // [1] or null
+    float* grad_logprob;
+    float* grad_entropy;     // or null
+  };
+  static constexpr bool kGradReads = true;  // the gradient needs the per-token inputs
+  // state[2 s]: token weight of sequence s before the batch's factor;
+  // state[2 s + 1]: derivative of the policy term by the mean of d (sequence
+  // level); state[2 B]: the batch's factor.
+  using Share = LossSum<4>;  // d, policy, kl, entropy
+  using Total = LossSum<5>;  // weighted: d, policy, kl, entropy, clipped
+  static constexpr int kSides = 1;
+
+  struct Raw {
+    float lp, old, ref, ent;
+  };
+  __device__ static Raw load(const LossArgs<PolicyLoss>& a, int64_t t) {
+    const In& in = a.in;
+    return {in.logprob[t], in.old_logprob[t], in.ref_logprob != nullptr ? in.ref_logprob[t] : 0.f,
+            in.entropy != nullptr ? in.entropy[t] : 0.f};
+  }
+  // Policy term f and its derivative df by the log ratio d, for advantage A.
+  __device__ static void clipped(const In& in, double d, double A, double& f, double& df,
+                                 bool& clip) {
+    double bound = 0.0;
+    clip = true;
+    if (A > 0.0 && d > in.log_over)
+      bound = in.over;
+    else if (A < 0.0 && d < in.log_under)
+      bound = in.under;
+    else if (A < 0.0 && d > in.log_dual)
+      bound = in.dual;
+    else
+      clip = false;
+    f = clip ? -bound * A : (A == 0.0 ? 0.0 : -exp(d) * A);  // A = 0: 0 for any ratio
+    df = clip ? 0.0 : f;
+  }
+  __device__ static void kl_term(const In& in, double x, double& f, double& df) {
+    if (in.kl == FLCE_KL_K1) {
+      f = x;
+      df = 1.0;
+    } else if (in.kl == FLCE_KL_K2) {
+      f = 0.5 * x * x;
+      df = x;
+    } else {
+      const double e = expm1(-x);
+      f = e + x;
+      df = -e;
+    }
+  }
+  // The terms of valid token t of sequence s.
+  __device__ static void token(const LossArgs<PolicyLoss>& a, const Raw& r, int64_t t, int64_t s,
+                               Share& v) {
+    const In& in = a.in;
+    const double d = (double)r.lp - (double)r.old;
+    double df;
+    v.n = 1;
+    v.x[0] = d;
+    if (!in.by_sequence) {
+      bool clip;
+      clipped(in, d, in.advantages[in.adv_seq ? s : t], v.x[1], df, clip);
+      v.c = clip ? 1 : 0;
+    }
+    if (in.ref_logprob != nullptr) kl_term(in, (double)r.lp - (double)r.ref, v.x[2], df);
+    v.x[3] = r.ent;
+  }
+  // Sequence s from its sums: its state, and its share of the batch's.
+  __device__ static void item(const LossArgs<PolicyLoss>& a, int64_t s, Total& tot) {
+    const In& in = a.in;
+    Share v = a.seq_sum[s];
+    double df = 0.0;
+    if (in.by_sequence && v.n > 0) {
+      bool clip;
+      double f;
+      clipped(in, v.x[0] / v.n, in.advantages[s], f, df, clip);
+      v.x[1] = f * v.n;
+      v.c = clip ? v.n : 0;
+    }
+    double w = 1.0;
+    if (in.reduction == FLCE_REDUCTION_SEQUENCE_MEAN) w = v.n > 0 ? 1.0 / v.n : 0.0;
+    a.state[2 * s] = w;
+    a.state[2 * s + 1] = df;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) tot.x[k] += w * v.x[k];
+    tot.x[4] += w * v.c;
+    tot.n += v.n;
+    tot.c += v.n > 0 ? 1 : 0;
+    tot.inv += v.inv;
+    tot.bad += v.bad;
+  }
+  __device__ static void finish(const LossArgs<PolicyLoss>& a, const Total& v) {
+    const In& in = a.in;
+    double k = 1.0;
+    if (in.reduction == FLCE_REDUCTION_MEAN) k = v.n > 0 ? 1.0 / v.n : 0.0;
+    if (in.reduction == FLCE_REDUCTION_SEQUENCE_MEAN) k = v.c > 0 ? 1.0 / v.c : 0.0;
+    if (v.bad != 0) k = __builtin_nan("");
+    a.state[2 * a.B] = k;
+    a.state[2 * a.B + 1] = 0.0;
+    float* s = a.out.stats;
+    // A term whose coefficient is 0 is absent, whatever its value.
+    const double kl = in.kl_coef != 0.0 ? in.kl_coef * v.x[2] : 0.0;
+    const double ent = in.ent_coef != 0.0 ? in.ent_coef * v.x[3] : 0.0;
+    s[0] = (float)(k * (v.x[1] + kl - ent));
+    s[1] = (float)(k * v.x[1]);
+    s[2] = (float)(k * v.x[2]);
+    s[3] = (float)(k * v.x[3]);
+    s[4] = (float)(k * v.x[4]);
+    s[5] = (float)(0.0 - k * v.x[0]);
+    s[6] = (float)v.n;
+    s[7] = (float)v.c;
+  }
+  // Upstream gradient times the batch's factor.
+  __device__ static double grad_scale(const LossArgs<PolicyLoss>& a) {
+    const double g = a.out.grad_loss != nullptr ? (double)a.out.grad_loss[0] : 1.0;
+    return g * a.state[2 * a.B];
+  }
+  __device__ static void grad(const LossArgs<PolicyLoss>& a, const Raw& r, double scale, int64_t t,
+                              int64_t s) {
+    const In& in = a.in;
+    float glp = 0.f, gent = 0.f;
+    if (s >= 0) {
+      double df, f;
+      if (in.by_sequence) {
+        df = a.state[2 * s + 1];
+      } else {
+        bool clip;
+        clipped(in, (double)r.lp - (double)r.old, in.advantages[in.adv_seq ? s : t], f, df, clip);
+      }
+      if (in.kl_coef != 0.0) {
+        double dk;
+        kl_term(in, (double)r.lp - (double)r.ref, f, dk);
+        df += in.kl_coef * dk;
+      }
+      const double w = scale * a.state[2 * s];
+      glp = (float)(w * df);
+      gent = (float)(0.0 - w * in.ent_coef);
+    }
+    a.out.grad_logprob[t] = glp;
+    if (a.out.grad_entropy != nullptr) a.out.grad_entropy[t] = gent;
+  }
+};
+
+// ---- the preference loss --------------------------------------------------------------
+
+struct PreferenceLoss {
+  struct In {
+    const float *logprob, *ref_logprob;
+    double beta, eps, margin, half_inv_beta;
+    int kind, normalize, reduction;
+  };
+  struct Out {
+    float *loss, *pair_loss, *chosen, *rejected;
+    const float* grad_loss;  // [P] under NONE, else [1]; or null
+    float* grad_logprob;
+  };
+  static constexpr bool kGradReads = false;
+  // state[s]: gradient of the reduced loss by a valid token's logprob of
+  // sequence s; state[B] = 1, or NaN after bad offsets.
+  using Share = LossSum<1>;  // logprob - ref_logprob
+  using Total = LossSum<1>;  // the pairs' losses
+  static constexpr int kSides = 2;
+
+  struct Raw {
+    float lp, ref;
+  };
+  __device__ static Raw load(const LossArgs<PreferenceLoss>& a, int64_t t) {
+    return {a.in.logprob[t], a.in.ref_logprob != nullptr ? a.in.ref_logprob[t] : 0.f};
+  }
+  __device__ static void token(const LossArgs<PreferenceLoss>&, const Raw& r, int64_t, int64_t,
+                               Share& v) {
+    v.n = 1;
+    v.x[0] = (double)r.lp - (double)r.ref;
+  }
+  __device__ static void item(const LossArgs<PreferenceLoss>& a, int64_t i, Total& tot) {
+    const In& in = a.in;
+    const int64_t P = a.items;
+    const Share c = a.seq_sum[i], r = a.seq_sum[P + i];
+    const double ic = in.normalize && c.n > 0 ? 1.0 / c.n : 1.0;
+    const double ir = in.normalize && r.n > 0 ? 1.0 / r.n : 1.0;
+    const double rc = c.x[0] * ic, rr = r.x[0] * ir;
+    const double diff = rc - rr;
+    double loss, slope;  // slope: derivative by diff
+    if (in.kind == FLCE_PREFERENCE_IPO) {
+      const double u = diff - in.half_inv_beta;
+      loss = u * u;
+      slope = 2.0 * u;
+    } else {
+      const double x = in.beta * diff - in.margin;
+      if (in.kind == FLCE_PREFERENCE_HINGE) {
+        loss = x < 1.0 ? 1.0 - x : (x >= 1.0 ? 0.0 : x);  // the last keeps NaN
+        slope = x < 1.0 ? -in.beta : (x >= 1.0 ? 0.0 : x);
+      } else {
+        // -log sigmoid(x) = log1p(exp(-|x|)) + max(-x, 0); neither it nor the
+        // sigmoids overflow.
+        const double e = exp(-fabs(x)), tail = log1p(e);
+        const double pos = x >= 0.0 ? 1.0 / (1.0 + e) : e / (1.0 + e);  // sigmoid(x)
+        const double neg = x >= 0.0 ? e / (1.0 + e) : 1.0 / (1.0 + e);  // sigmoid(-x)
+        const double lpos = tail + (x < 0.0 ? -x : 0.0), lneg = tail + (x > 0.0 ? x : 0.0);
+        loss = (1.0 - in.eps) * lpos;
+        if (in.eps != 0.0) loss += in.eps * lneg;  // lneg may be infinite
+        slope = in.beta * (in.eps * pos - (1.0 - in.eps) * neg);
+      }
+    }
+    const double k = in.reduction == FLCE_REDUCTION_MEAN ? 1.0 / (double)P : 1.0;
+    a.state[i] = k * slope * ic;
+    a.state[P + i] = -k * slope * ir;
+    a.out.pair_loss[i] = (float)loss;
+    a.out.chosen[i] = (float)(in.beta * rc);
+    a.out.rejected[i] = (float)(in.beta * rr);
+    tot.x[0] += loss;
+    tot.inv += c.inv + r.inv;
+    tot.bad += c.bad + r.bad;
+  }
+  __device__ static void finish(const LossArgs<PreferenceLoss>& a, const Total& v) {
+    a.state[a.B] = v.bad != 0 ? __builtin_nan("") : 1.0;
+    if (a.in.reduction != FLCE_REDUCTION_NONE) {
+      const double k = a.in.reduction == FLCE_REDUCTION_MEAN && a.items > 0
+                           ? 1.0 / (double)a.items : 1.0;
+      a.out.loss[0] = (float)(k * v.x[0]);
+    }
+  }
+  __device__ static double grad_scale(const LossArgs<PreferenceLoss>& a) {
+    const bool one = a.in.reduction != FLCE_REDUCTION_NONE && a.out.grad_loss != nullptr;
+    return (one ? (double)a.out.grad_loss[0] : 1.0) * a.state[a.B];
+  }
+  __device__ static void grad(const LossArgs<PreferenceLoss>& a, const Raw&, double scale,
+                              int64_t t, int64_t s) {
+    double g = 0.0;
+    if (s >= 0) {
+      g = scale * a.state[s];
+      if (a.in.reduction == FLCE_REDUCTION_NONE && a.out.grad_loss != nullptr)
+        g *= (double)a.out.grad_loss[s < a.items ? s : s - a.items];
+    }
+    a.out.grad_logprob[t] = (float)g;
+  }
+};
+
+// ---- the three steps ----------------------------------------------------------------
+
+// Step 1, one wave, one tile: sh holds the wave's 256 token terms. The sums run
+// in groups of lanes, a group a sequence, as many lanes as the tile's sequences
+// leave each (64 for one long sequence, 1 for 64 short ones).
+template <class Loss>
+__device__ __forceinline__ void tile_parts(const LossArgs<Loss>& a, int64_t tile,
+                                           typename Loss::Share* sh) {
+  const int lane = threadIdx.x & 63;
+  const int64_t t0 = tile * kLossTile;
+  const int64_t t1 = a.N - t0 < kLossTile ? a.N : t0 + kLossTile;
+  typename Loss::Raw raw[kLossTile / 64];
+  int64_t y[kLossTile / 64];
+#pragma unroll
+  for (int j = 0; j < kLossTile / 64; ++j) {
+    const int64_t t = t0 + j * 64 + lane;
+    const int64_t tc = t < a.N ? t : a.N - 1;
+    y[j] = a.labels[tc];
+    raw[j] = Loss::load(a, tc);
+  }
+  const SeqRange r = tile_sequences(a.cu, a.B, t0, t1);
+  const int64_t ns = r.s1 - r.s0 + 1;
+  if (ns <= 0) return;
+#pragma unroll
+  for (int j = 0; j < kLossTile / 64; ++j) {
+    const int64_t t = t0 + j * 64 + lane;
+    typename Loss::Share v;
+    v.clear();
+    const int64_t s = t < a.N ? token_sequence(a.cu, r, t) : -1;
+    if (s >= 0) {
+      if (label_valid(y[j], a.ignore_index, a.V))
+        Loss::token(a, raw[j], t, s, v);
+      else if (y[j] != a.ignore_index)
+        v.inv = 1;
+    }
+    sh[j * 64 + lane] = v;
+  }
+  wave_lds_fence();
+  int g = 64;
+  while (g > 1 && 64 / g < ns) g >>= 1;
+  const int per = 64 / g, k = lane & (g - 1);
+  for (int64_t i = 0; i < ns; i += per) {
+    const int64_t s = r.s0 + i + lane / g;
+    int b = 0, e = 0;
+    if (s <= r.s1) {
+      const int64_t sb = seq_begin(a.cu, s), se = seq_end(a.cu, s, a.N);
+      b = (int)((sb < t0 ? t0 : (sb < t1 ? sb : t1)) - t0);
+      e = (int)((se < t0 ? t0 : (se < t1 ? se : t1)) - t0);
+    }
+    typename Loss::Share v;
+    v.clear();
+    for (int q = b + k; q < e; q += g) v.add(sh[q]);
+    v.group_sum(g);
+    if (k == 0 && b < e) a.parts[s + tile] = v;
+  }
+  wave_lds_fence();  // the next tile reuses sh
+}
+
+// Shares of sequence s: tiles [p0, p0 + count); a sequence with bad offsets has
+// none.
+struct SeqParts {
+  int64_t p0, count;
+  bool bad;
+};
+__device__ __forceinline__ SeqParts seq_parts(const int64_t* cu, int64_t N, int64_t s) {
+  const int64_t b = seq_begin(cu, s), e = seq_end(cu, s, N);
+  if (b < 0 || e < b || e > N) return {0, 0, true};
+  if (b == e) return {0, 0, false};
+  return {b / kLossTile, (e - 1) / kLossTile - b / kLossTile + 1, false};
+}
+
+// Step 2, one block, items [i0, i1): adds up the sequences' shares, then the
+// items. Groups of lanes take a sequence each, sized by the average number of
+// shares; a sequence with far more than that is added by the whole block.
+template <class Loss>
+__device__ __forceinline__ typename Loss::Total sum_sequences(const LossArgs<Loss>& a, int64_t i0,
+                                                              int64_t i1) {
+  using Share = typename Loss::Share;
+  using Total = typename Loss::Total;
+  __shared__ Share sh_share[16];
+  __shared__ Total sh_total[16];
+  const int64_t m = i1 - i0, local = m * Loss::kSides;
+  auto seq = [&](int64_t j) { return j < m ? i0 + j : a.items + i0 + (j - m); };
+  int g = 1;
+  while (g < 64 && g * a.B < a.tiles) g <<= 1;
+  const int64_t longest = (int64_t)g * 16;
+  const int groups = (int)blockDim.x / g, k = threadIdx.x & (g - 1);
+  bool any_long = false;
+  for (int64_t jb = 0; jb < local; jb += groups) {
+    const int64_t j = jb + threadIdx.x / g;
+    Share v;
+    v.clear();
+    bool mine = j < local;
+    int64_t s = 0;
+    if (mine) {
+      s = seq(j);
+      const SeqParts p = seq_parts(a.cu, a.N, s);
+      if (p.count > longest) {
+        any_long = true;
+        mine = false;
+      } else {
+        for (int64_t q = k; q < p.count; q += g) v.add(a.parts[s + p.p0 + q]);
+        if (p.bad && k == 0) {
+          v.x[0] = __builtin_nan("");
+          v.bad = 1;
+        }
+      }
+    }
+    v.group_sum(g);
+    if (mine && k == 0) a.seq_sum[s] = v;
+  }
+  if (__syncthreads_or(any_long ? 1 : 0)) {
+    for (int64_t jb = 0; jb < local; jb += 64) {
+      const int64_t jl = jb + (threadIdx.x & 63);
+      const bool lg = jl < local && seq_parts(a.cu, a.N, seq(jl)).count > longest;
+      uint64_t bits = __builtin_amdgcn_ballot_w64(lg);  // the same in every wave
+      while (bits != 0) {
+        const int64_t s = seq(jb + __builtin_ctzll(bits));
+        bits &= bits - 1;
+        const SeqParts p = seq_parts(a.cu, a.N, s);
+        Share v;
+        v.clear();
+        for (int64_t q = threadIdx.x; q < p.count; q += blockDim.x) v.add(a.parts[s + p.p0 + q]);
+        v = block_total(v, sh_share);
+        if (threadIdx.x == 0) a.seq_sum[s] = v;
+      }
+    }
+    __syncthreads();
+  }
+  Total t;
+  t.clear();
+  for (int64_t i = i0 + threadIdx.x; i < i1; i += blockDim.x) Loss::item(a, i, t);
+  return block_total(t, sh_total);
+}
+
+template <class Loss>
+__device__ __forceinline__ void finish_batch(const LossArgs<Loss>& a,
+                                             const typename Loss::Total& t) {
+  if (threadIdx.x == 0) {
+    a.header[0] = t.inv + t.bad;
+    a.header[1] = t.n;
+    Loss::finish(a, t);
+  }
+}
+
+// Step 3, one wave, one tile.
+template <class Loss>
+__device__ __forceinline__ void tile_grads(const LossArgs<Loss>& a, int64_t tile) {
+  const int lane = threadIdx.x & 63;
+  const int64_t t0 = tile * kLossTile;
+  const int64_t t1 = a.N - t0 < kLossTile ? a.N : t0 + kLossTile;
+  typename Loss::Raw raw[kLossTile / 64];
+  int64_t y[kLossTile / 64];
+#pragma unroll
+  for (int j = 0; j < kLossTile / 64; ++j) {
+    const int64_t t = t0 + j * 64 + lane;
+    const int64_t tc = t < a.N ? t : a.N - 1;
+    y[j] = a.labels[tc];
+    if constexpr (Loss::kGradReads) raw[j] = Loss::load(a, tc);
+  }
+  const SeqRange r = tile_sequences(a.cu, a.B, t0, t1);
+  const double scale = Loss::grad_scale(a);
+#pragma unroll
+  for (int j = 0; j < kLossTile / 64; ++j) {
+    const int64_t t = t0 + j * 64 + lane;
+    if (t >= a.N) continue;
+    int64_t s = -1;
+    if (label_valid(y[j], a.ignore_index, a.V) && r.s0 <= r.s1) s = token_sequence(a.cu, r, t);
+    Loss::grad(a, raw[j], scale, t, s);
+  }
+}
+
+template <class Loss>
+__global__ void __launch_bounds__(64 * kLossWaves) loss_parts_kernel(LossArgs<Loss> a) {
+  __shared__ typename Loss::Share sh[kLossWaves][kLossTile];
+  const int w = threadIdx.x >> 6;
+  const int64_t tile = (int64_t)blockIdx.x * kLossWaves + w;
+  if (tile < a.tiles) tile_parts(a, tile, sh[w]);
+}
+
+template <class Loss>
+__global__ void __launch_bounds__(kSeqThreads) loss_sequences_kernel(LossArgs<Loss> a) {
+  const int64_t i0 = (int64_t)blockIdx.x * kSeqItems;
+  const int64_t i1 = a.items - i0 < kSeqItems ? a.items : i0 + kSeqItems;
+  const typename Loss::Total t = sum_sequences(a, i0, i1);
+  if (gridDim.x == 1)
+    finish_batch(a, t);
+  else if (threadIdx.x == 0)
+    a.totals[blockIdx.x] = t;
+}
+
+// Adds up the blocks of loss_sequences_kernel when there are several.
+template <class Loss>
+__global__ void __launch_bounds__(256) loss_finish_kernel(LossArgs<Loss> a, int blocks) {
+  __shared__ typename Loss::Total sh[16];
+  typename Loss::Total t;
+  t.clear();
+  for (int b = threadIdx.x; b < blocks; b += 256) t.add(a.totals[b]);
+  t = block_total(t, sh);
+  finish_batch(a, t);
+}
+
+template <class Loss>
+__global__ void __launch_bounds__(64 * kLossWaves) loss_grads_kernel(LossArgs<Loss> a) {
+  const int64_t tile = (int64_t)blockIdx.x * kLossWaves + (threadIdx.x >> 6);
+  if (tile < a.tiles) tile_grads(a, tile);
+}
+
+// All three steps in one block, for small batches: the steps exchange their
+// sums through the workspace as the separate kernels do, ordered by barriers.
+template <class Loss, bool GRADS>
+__global__ void __launch_bounds__(64 * kSmallWaves) loss_small_kernel(LossArgs<Loss> a) {
+  __shared__ typename Loss::Share sh[kSmallWaves][kLossTile];
+  const int w = threadIdx.x >> 6;
+  for (int64_t tile = w; tile < a.tiles; tile += kSmallWaves) tile_parts(a, tile, sh[w]);
+  __syncthreads();
+  finish_batch(a, sum_sequences(a, 0, a.items));
+  if constexpr (GRADS) {
+    __syncthreads();
+    for (int64_t tile = w; tile < a.tiles; tile += kSmallWaves) tile_grads(a, tile);
+  }
+}
+
+}  // namespace flce

@@ -1,0 +1,189 @@
+// Host planner of the embedding and loss operators: limits, argument checks
+// and workspace layouts. Host-only C++ without HIP, so that it also builds on
+// its own for sanitizer checks of the layout arithmetic.
+#pragma once
+
+#include <cmath>
+#include <cstddef>
+#include <cstdint>
+
+#include "flce.h"
+#include "flce_plan.hpp"
+
+namespace flce {
+
+// ---- losses ----------------------------------------------------------------------
+
+constexpr int kLossTile = 256;        // tokens a wave takes
+constexpr int kLossWaves = 4;         // waves a block, parts and gradients kernels
+constexpr int kSmallWaves = 8;        // waves of the one-block kernel
+constexpr int kSeqThreads = 1024;     // threads a block, sequences kernel
+constexpr int64_t kSeqItems = 4096;   // sequences (or pairs) a block of it
+// Batches up to these sizes take the one-block kernel.
+constexpr int64_t kSmallTokens = 8192;
+constexpr int64_t kSmallItems = 1024;
+constexpr int64_t kMaxSequences = (int64_t)1 << 21;
+
+// Workspace: header, shares [B + tiles], sequence sums [B], block totals, and
+// the state of the calls that return gradients at once.
+struct LossPlan {
+  int64_t tiles;
+  int seq_blocks;
+  bool small;
+  size_t parts, seq_sum, totals, state, total;
+};
+
+inline LossPlan make_loss_plan(int64_t N, int64_t B, int64_t items, size_t share_bytes,
+                               size_t total_bytes, int64_t state_doubles) {
+  LossPlan p{};
+  p.tiles = ceil_div(N, kLossTile);
+  p.seq_blocks = (int)ceil_div(items > 0 ? items : 1, kSeqItems);
+  p.small = N <= kSmallTokens && items <= kSmallItems;
+  size_t off = kHeaderBytes;
+  auto take = [&](size_t& field, size_t bytes) {
+    field = off;
+    off = align_up(off + bytes);
+  };
+  take(p.parts, share_bytes * (size_t)(B + p.tiles));
+  take(p.seq_sum, share_bytes * (size_t)B);
+  take(p.totals, total_bytes * (size_t)p.seq_blocks);
+  take(p.state, 8 * (size_t)state_doubles);
+  p.total = off;
+  return p;
+}
+
+// Bytes of the kernels' sums: K doubles and four counts (checked where the
+// kernels' types are known).
+constexpr size_t sum_bytes(int k) { return 8 * (size_t)k + 16; }
+
+inline LossPlan policy_plan(int64_t N, int64_t B) {
+  return make_loss_plan(N, B, B, sum_bytes(4), sum_bytes(5), 2 * (B + 1));
+}
+inline LossPlan preference_plan(int64_t N, int64_t P) {
+  return make_loss_plan(N, 2 * P, P, sum_bytes(1), sum_bytes(1), 2 * P + 1);
+}
+
+inline flce_status_t check_policy(int64_t N, int64_t B, int64_t V, bool has_cu,
+                                  const flce_policy_options_t* o) {
+  if (N < 0 || N > kMaxN || B < 1 || B > kMaxSequences || V < 1 || V > kMaxV)
+    return FLCE_ERR_BAD_SHAPE;
+  if (!has_cu && B != 1) return FLCE_ERR_BAD_SHAPE;
+  if (o == nullptr) return FLCE_ERR_NULL_POINTER;
+  if (o->reduction != FLCE_REDUCTION_MEAN && o->reduction != FLCE_REDUCTION_SUM &&
+      o->reduction != FLCE_REDUCTION_SEQUENCE_MEAN)
+    return FLCE_ERR_BAD_REDUCTION;
+  if (!(o->clip_low >= 0.0 && o->clip_low <= 1.0)) return FLCE_ERR_BAD_OPTION;
+  if (!(o->clip_high >= 0.0 && std::isfinite(o->clip_high))) return FLCE_ERR_BAD_OPTION;
+  if (!(o->dual_clip == 0.0 || (o->dual_clip > 1.0 && std::isfinite(o->dual_clip))))
+    return FLCE_ERR_BAD_OPTION;
+  if (!std::isfinite(o->kl_coef) || !std::isfinite(o->entropy_coef)) return FLCE_ERR_BAD_OPTION;
+  if (o->kl_estimator < FLCE_KL_K1 || o->kl_estimator > FLCE_KL_K3) return FLCE_ERR_BAD_OPTION;
+  if (o->level != FLCE_RATIO_TOKEN && o->level != FLCE_RATIO_SEQUENCE) return FLCE_ERR_BAD_OPTION;
+  if (o->advantages_per_sequence != 0 && o->advantages_per_sequence != 1)
+    return FLCE_ERR_BAD_OPTION;
+  if (o->level == FLCE_RATIO_SEQUENCE && (!has_cu || o->advantages_per_sequence != 1))
+    return FLCE_ERR_BAD_OPTION;
+  return FLCE_OK;
+}
+
+inline flce_status_t check_preference(int64_t N, int64_t P, int64_t V,
+                                      const flce_preference_options_t* o) {
+  if (N < 0 || N > kMaxN || P < 1 || P > kMaxSequences / 2 || V < 1 || V > kMaxV)
+    return FLCE_ERR_BAD_SHAPE;
+  if (o == nullptr) return FLCE_ERR_NULL_POINTER;
+  if (!valid_reduction(o->reduction)) return FLCE_ERR_BAD_REDUCTION;
+  if (!(o->beta > 0.0 && std::isfinite(o->beta)) || !std::isfinite(o->margin))
+    return FLCE_ERR_BAD_OPTION;
+  if (!(o->label_smoothing >= 0.0 && o->label_smoothing <= 0.5)) return FLCE_ERR_BAD_OPTION;
+  if (o->kind < FLCE_PREFERENCE_SIGMOID || o->kind > FLCE_PREFERENCE_IPO)
+    return FLCE_ERR_BAD_OPTION;
+  if (o->kind != FLCE_PREFERENCE_SIGMOID && o->label_smoothing != 0.0) return FLCE_ERR_BAD_OPTION;
+  if (o->kind == FLCE_PREFERENCE_IPO && o->margin != 0.0) return FLCE_ERR_BAD_OPTION;
+  if (o->length_normalize != 0 && o->length_normalize != 1) return FLCE_ERR_BAD_OPTION;
+  return FLCE_OK;
+}
+
+inline bool aligned_to(const void* p, size_t a) { return ((uintptr_t)p & (a - 1)) == 0; }
+
+// ---- embedding --------------------------------------------------------------------
+
+constexpr int kPiece = 32;                    // sorted positions a piece; longer runs are split
+constexpr int64_t kSortOneBlock = 16384;      // tokens that one block sorts in LDS
+constexpr int kSortTile = 4096;               // tokens a block of the larger sort takes
+constexpr int kMaxDigitBits = 11;
+
+// The sort: keys are the token's row in the slice, or Vs for a token that takes
+// no part, so that these come last.
+struct SortPlan {
+  int passes, bits;     // digit passes of `bits` bits each
+  int64_t tiles;        // blocks of the larger sort
+  bool one_block;
+};
+inline SortPlan make_sort_plan(int64_t N, int64_t Vs) {
+  SortPlan s{};
+  int total = 1;
+  while (((int64_t)1 << total) <= Vs) ++total;  // the keys 0 .. Vs
+  s.one_block = N <= kSortOneBlock;
+  const int digit = s.one_block ? 9 : kMaxDigitBits;
+  s.passes = (total + digit - 1) / digit;
+  s.bits = (total + s.passes - 1) / s.passes;
+  s.tiles = ceil_div(N, kSortTile);
+  return s;
+}
+
+struct EmbedPlan {
+  SortPlan sort;
+  bool sorted;          // the forward gathers in sorted order
+  size_t key, perm, key2, perm2, counts, totals;  // sort
+  size_t starts;        // backward: first sorted position of every row, [Vs + 1]
+  size_t part;          // backward: sums of split runs, [2 * pieces, H] fp32
+  size_t f_total, b_total;
+};
+
+// Lookups of up to this many tokens from a table count them in one block.
+constexpr int64_t kCountBlockTokens = 8192;
+// Lookups of fewer tokens from an [H,V] weight gather in token order.
+constexpr int64_t kGatherSorted = 512;
+
+inline EmbedPlan make_embed_plan(int64_t N, int64_t H, int64_t Vs, int layout) {
+  EmbedPlan p{};
+  p.sort = make_sort_plan(N, Vs);
+  p.sorted = layout == FLCE_EMBED_HV && N >= kGatherSorted;
+  size_t off = kHeaderBytes;
+  auto take = [&](size_t& field, size_t bytes) {
+    field = off;
+    off = align_up(off + bytes);
+  };
+  take(p.key, 4 * (size_t)N);
+  take(p.perm, 4 * (size_t)N);
+  if (!p.sort.one_block) {
+    take(p.key2, 4 * (size_t)N);
+    take(p.perm2, 4 * (size_t)N);
+    take(p.counts, 4 * ((size_t)p.sort.tiles << p.sort.bits));
+    take(p.totals, (size_t)4 << p.sort.bits);
+  }
+  p.f_total = p.sorted ? off : kHeaderBytes;
+  take(p.starts, 4 * ((size_t)Vs + 1));
+  take(p.part, 4 * 2 * (size_t)ceil_div(N, kPiece) * (size_t)H);
+  p.b_total = off;
+  return p;
+}
+
+inline flce_status_t check_embedding(int64_t N, int64_t H, int64_t Vs, int64_t v_begin,
+                                     int64_t V_total, const flce_embedding_options_t* o) {
+  const flce_status_t s = check_shape(N, H, Vs);
+  if (s != FLCE_OK) return s;
+  if (V_total < 1 || V_total > kMaxV || v_begin < 0 || v_begin + Vs > V_total)
+    return FLCE_ERR_BAD_SHAPE;
+  if (o == nullptr) return FLCE_ERR_NULL_POINTER;
+  if (!std::isfinite(o->scale) || !std::isfinite((float)o->scale)) return FLCE_ERR_BAD_OPTION;
+  if (o->layout != FLCE_EMBED_VH && o->layout != FLCE_EMBED_HV) return FLCE_ERR_BAD_OPTION;
+  if (o->hidden_dtype != FLCE_GRAD_BF16 && o->hidden_dtype != FLCE_GRAD_F32)
+    return FLCE_ERR_BAD_OPTION;
+  if (o->grad_dtype != FLCE_GRAD_BF16 && o->grad_dtype != FLCE_GRAD_F32)
+    return FLCE_ERR_BAD_OPTION;
+  if (o->accumulate != 0 && o->accumulate != 1) return FLCE_ERR_BAD_OPTION;
+  return FLCE_OK;
+}
+
+}  // namespace flce

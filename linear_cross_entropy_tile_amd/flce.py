@@ -8,10 +8,13 @@ Two layers, both argument marshalling only:
   pointers and streams as integers, the options as ``FlceOptions``). A non-OK
   status raises ``FlceError``.
 * ``forward`` / ``backward`` / ``forward_backward`` (the fused call, for
-  upstream gradients known before the forward): take torch CUDA tensors,
-  check dtypes and layouts, allocate outputs and the workspace with torch (so
+  upstream gradients known before the forward), the embedding
+  (``embedding``, ``embedding_backward``) and the losses between the head's
+  forward and its backward (``policy_loss``, ``preference_loss``, each with
+  ``_backward`` and ``_forward_backward``): take torch CUDA tensors, check
+  dtypes and layouts, allocate outputs and the workspace with torch (so
   torch's caching allocator owns all memory), and call the C entry points on
-  torch's current stream. No arithmetic of the head happens here.
+  torch's current stream. No arithmetic of the operators happens here.
 
 The library is loaded on first use. There is no fallback: if libflce.so is
 missing or the device is not a GPU, calls raise.
@@ -31,6 +34,15 @@ __all__ = [
     "flce_status_string", "flce_version", "flce_profile_enable", "flce_profile_reset",
     "flce_profile_kinds", "flce_profile_read", "profile_table", "flce_probe_mfma_rate",
     "forward", "backward", "forward_backward", "workspace_bytes", "check_shapes",
+    "FLCE_REDUCTION_SEQUENCE_MEAN", "FLCE_EMBED_VH", "FLCE_EMBED_HV",
+    "FlceEmbeddingOptions", "FlcePolicyOptions", "FlcePreferenceOptions",
+    "flce_embedding_workspace_size", "flce_embedding_forward", "flce_embedding_backward",
+    "flce_policy_workspace_size", "flce_policy_loss_forward", "flce_policy_loss_backward",
+    "flce_policy_loss_forward_backward", "flce_preference_workspace_size",
+    "flce_preference_loss_forward", "flce_preference_loss_backward",
+    "flce_preference_loss_forward_backward", "embedding", "embedding_backward", "policy_loss",
+    "policy_loss_backward", "policy_loss_forward_backward", "preference_loss",
+    "preference_loss_backward", "preference_loss_forward_backward",
 ]
 
 LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "libflce.so")
@@ -43,6 +55,16 @@ _REDUCTIONS = {"none": FLCE_REDUCTION_NONE, "mean": FLCE_REDUCTION_MEAN,
 FLCE_GRAD_BF16 = 0
 FLCE_GRAD_F32 = 1
 _GRAD_DTYPES = {"bf16": FLCE_GRAD_BF16, "f32": FLCE_GRAD_F32}
+FLCE_REDUCTION_SEQUENCE_MEAN = 3
+_POLICY_REDUCTIONS = {"mean": FLCE_REDUCTION_MEAN, "sum": FLCE_REDUCTION_SUM,
+                      "sequence_mean": FLCE_REDUCTION_SEQUENCE_MEAN}
+FLCE_EMBED_VH = 0
+FLCE_EMBED_HV = 1
+_EMBED_LAYOUTS = {"vh": FLCE_EMBED_VH, "hv": FLCE_EMBED_HV}
+_KL_ESTIMATORS = {"k1": 0, "k2": 1, "k3": 2}
+_RATIO_LEVELS = {"token": 0, "sequence": 1}
+_PREFERENCE_KINDS = {"sigmoid": 0, "hinge": 1, "ipo": 2}
+MAX_VOCAB = (1 << 22) - 256
 
 STATUS_NAMES = {
     0: "FLCE_OK", 1: "FLCE_ERR_NULL_POINTER", 2: "FLCE_ERR_BAD_SHAPE",
@@ -59,6 +81,30 @@ class FlceOptions(ctypes.Structure):
                 ("reduction", ctypes.c_int), ("z_loss_scale", ctypes.c_float),
                 ("grad_dtype", ctypes.c_int), ("class_weight", ctypes.c_void_p),
                 ("entropy_per_token", ctypes.c_int)]
+
+
+class FlceEmbeddingOptions(ctypes.Structure):
+    """flce_embedding_options_t."""
+    _fields_ = [("ignore_index", ctypes.c_int64), ("scale", ctypes.c_double),
+                ("layout", ctypes.c_int), ("hidden_dtype", ctypes.c_int),
+                ("grad_dtype", ctypes.c_int), ("accumulate", ctypes.c_int)]
+
+
+class FlcePolicyOptions(ctypes.Structure):
+    """flce_policy_options_t."""
+    _fields_ = [("ignore_index", ctypes.c_int64), ("clip_low", ctypes.c_double),
+                ("clip_high", ctypes.c_double), ("dual_clip", ctypes.c_double),
+                ("kl_coef", ctypes.c_double), ("entropy_coef", ctypes.c_double),
+                ("kl_estimator", ctypes.c_int), ("level", ctypes.c_int),
+                ("reduction", ctypes.c_int), ("advantages_per_sequence", ctypes.c_int)]
+
+
+class FlcePreferenceOptions(ctypes.Structure):
+    """flce_preference_options_t."""
+    _fields_ = [("ignore_index", ctypes.c_int64), ("beta", ctypes.c_double),
+                ("label_smoothing", ctypes.c_double), ("margin", ctypes.c_double),
+                ("kind", ctypes.c_int), ("length_normalize", ctypes.c_int),
+                ("reduction", ctypes.c_int)]
 
 # Every exported symbol with its (restype, argtypes).
 _P = ctypes.c_void_p
@@ -93,6 +139,35 @@ _SIG = {
     "flce_backward_shard": (ctypes.c_int, [_P, _P, _P, _I64, _I64, _I64, _I64, _I64,
                                            ctypes.POINTER(FlceOptions), _P, _P, _P, _P, _P, _P,
                                            _P, _P, _P, ctypes.c_size_t, _P]),
+    "flce_embedding_workspace_size": (ctypes.c_int, [_I64, _I64, _I64,
+                                                     ctypes.POINTER(FlceEmbeddingOptions),
+                                                     ctypes.POINTER(ctypes.c_size_t),
+                                                     ctypes.POINTER(ctypes.c_size_t)]),
+    "flce_embedding_forward": (ctypes.c_int, [_P, _P, _I64, _I64, _I64, _I64, _I64,
+                                              ctypes.POINTER(FlceEmbeddingOptions), _P, _P,
+                                              ctypes.c_size_t, _P]),
+    "flce_embedding_backward": (ctypes.c_int, [_P, _P, _I64, _I64, _I64, _I64, _I64,
+                                               ctypes.POINTER(FlceEmbeddingOptions), _P, _P,
+                                               ctypes.c_size_t, _P]),
+    "flce_policy_workspace_size": (ctypes.c_int, [_I64, _I64, ctypes.POINTER(ctypes.c_size_t)]),
+    "flce_policy_loss_forward": (ctypes.c_int, [_P] * 7 + [_I64] * 3
+                                 + [ctypes.POINTER(FlcePolicyOptions), _P, _P, _P, ctypes.c_size_t,
+                                    _P]),
+    "flce_policy_loss_backward": (ctypes.c_int, [_P] * 6 + [_I64] * 3
+                                  + [ctypes.POINTER(FlcePolicyOptions), _P, _P, _P, _P, _P]),
+    "flce_policy_loss_forward_backward": (ctypes.c_int, [_P] * 7 + [_I64] * 3
+                                          + [ctypes.POINTER(FlcePolicyOptions), _P, _P, _P, _P, _P,
+                                             ctypes.c_size_t, _P]),
+    "flce_preference_workspace_size": (ctypes.c_int, [_I64, _I64,
+                                                      ctypes.POINTER(ctypes.c_size_t)]),
+    "flce_preference_loss_forward": (ctypes.c_int, [_P] * 4 + [_I64] * 3
+                                     + [ctypes.POINTER(FlcePreferenceOptions), _P, _P, _P, _P, _P,
+                                        _P, ctypes.c_size_t, _P]),
+    "flce_preference_loss_backward": (ctypes.c_int, [_P] * 2 + [_I64] * 3
+                                      + [ctypes.POINTER(FlcePreferenceOptions), _P, _P, _P, _P]),
+    "flce_preference_loss_forward_backward": (ctypes.c_int, [_P] * 4 + [_I64] * 3
+                                              + [ctypes.POINTER(FlcePreferenceOptions), _P, _P, _P,
+                                                 _P, _P, _P, _P, ctypes.c_size_t, _P]),
     "flce_get_status": (ctypes.c_int, [_P, ctypes.POINTER(_I64), _P]),
     "flce_status_string": (ctypes.c_char_p, [ctypes.c_int]),
     "flce_version": (ctypes.c_int, []),
@@ -240,8 +315,102 @@ def flce_backward_shard(hidden, weight_shard, labels, N, H, Vs, v_begin, V_total
            "flce_backward_shard")
 
 
+def flce_embedding_workspace_size(N: int, H: int, Vs: int, opt):
+    f = ctypes.c_size_t(0)
+    b = ctypes.c_size_t(0)
+    _check(lib().flce_embedding_workspace_size(N, H, Vs, ctypes.byref(opt), ctypes.byref(f),
+                                               ctypes.byref(b)), "flce_embedding_workspace_size")
+    return f.value, b.value
+
+
+def flce_embedding_forward(weight, tokens, N, H, Vs, v_begin, V_total, opt, hidden, workspace,
+                           workspace_bytes, stream):
+    _check(lib().flce_embedding_forward(weight, tokens, N, H, Vs, v_begin, V_total,
+                                        ctypes.byref(opt), hidden, workspace, workspace_bytes,
+                                        stream), "flce_embedding_forward")
+
+
+def flce_embedding_backward(grad_hidden, tokens, N, H, Vs, v_begin, V_total, opt, grad_weight,
+                            workspace, workspace_bytes, stream):
+    _check(lib().flce_embedding_backward(grad_hidden, tokens, N, H, Vs, v_begin, V_total,
+                                         ctypes.byref(opt), grad_weight, workspace,
+                                         workspace_bytes, stream), "flce_embedding_backward")
+
+
+def flce_policy_workspace_size(N: int, B: int) -> int:
+    b = ctypes.c_size_t(0)
+    _check(lib().flce_policy_workspace_size(N, B, ctypes.byref(b)), "flce_policy_workspace_size")
+    return b.value
+
+
+def flce_policy_loss_forward(logprob, entropy, old_logprob, ref_logprob, advantages, labels,
+                             cu_seqlens, N, B, V, opt, stats, seq_state, workspace,
+                             workspace_bytes, stream):
+    _check(lib().flce_policy_loss_forward(logprob, entropy, old_logprob, ref_logprob, advantages,
+                                          labels, cu_seqlens, N, B, V, ctypes.byref(opt), stats,
+                                          seq_state, workspace, workspace_bytes, stream),
+           "flce_policy_loss_forward")
+
+
+def flce_policy_loss_backward(logprob, old_logprob, ref_logprob, advantages, labels, cu_seqlens,
+                              N, B, V, opt, seq_state, grad_loss, grad_logprob, grad_entropy,
+                              stream):
+    _check(lib().flce_policy_loss_backward(logprob, old_logprob, ref_logprob, advantages, labels,
+                                           cu_seqlens, N, B, V, ctypes.byref(opt), seq_state,
+                                           grad_loss, grad_logprob, grad_entropy, stream),
+           "flce_policy_loss_backward")
+
+
+def flce_policy_loss_forward_backward(logprob, entropy, old_logprob, ref_logprob, advantages,
+                                      labels, cu_seqlens, N, B, V, opt, grad_loss, stats,
+                                      grad_logprob, grad_entropy, workspace, workspace_bytes,
+                                      stream):
+    _check(lib().flce_policy_loss_forward_backward(logprob, entropy, old_logprob, ref_logprob,
+                                                   advantages, labels, cu_seqlens, N, B, V,
+                                                   ctypes.byref(opt), grad_loss, stats,
+                                                   grad_logprob, grad_entropy, workspace,
+                                                   workspace_bytes, stream),
+           "flce_policy_loss_forward_backward")
+
+
+def flce_preference_workspace_size(N: int, P: int) -> int:
+    b = ctypes.c_size_t(0)
+    _check(lib().flce_preference_workspace_size(N, P, ctypes.byref(b)),
+           "flce_preference_workspace_size")
+    return b.value
+
+
+def flce_preference_loss_forward(logprob, ref_logprob, labels, cu_seqlens, N, P, V, opt, loss,
+                                 pair_loss, chosen_reward, rejected_reward, seq_state, workspace,
+                                 workspace_bytes, stream):
+    _check(lib().flce_preference_loss_forward(logprob, ref_logprob, labels, cu_seqlens, N, P, V,
+                                              ctypes.byref(opt), loss, pair_loss, chosen_reward,
+                                              rejected_reward, seq_state, workspace,
+                                              workspace_bytes, stream),
+           "flce_preference_loss_forward")
+
+
+def flce_preference_loss_backward(labels, cu_seqlens, N, P, V, opt, seq_state, grad_loss,
+                                  grad_logprob, stream):
+    _check(lib().flce_preference_loss_backward(labels, cu_seqlens, N, P, V, ctypes.byref(opt),
+                                               seq_state, grad_loss, grad_logprob, stream),
+           "flce_preference_loss_backward")
+
+
+def flce_preference_loss_forward_backward(logprob, ref_logprob, labels, cu_seqlens, N, P, V, opt,
+                                          grad_loss, loss, pair_loss, chosen_reward,
+                                          rejected_reward, grad_logprob, workspace,
+                                          workspace_bytes, stream):
+    _check(lib().flce_preference_loss_forward_backward(logprob, ref_logprob, labels, cu_seqlens,
+                                                       N, P, V, ctypes.byref(opt), grad_loss,
+                                                       loss, pair_loss, chosen_reward,
+                                                       rejected_reward, grad_logprob, workspace,
+                                                       workspace_bytes, stream),
+           "flce_preference_loss_forward_backward")
+
+
 def flce_get_status(workspace, stream) -> int:
-    """Number of invalid labels the last call on this workspace saw (syncs)."""
+    """Number of invalid labels (or tokens) the last call on this workspace saw (syncs)."""
     n = _I64(0)
     st = lib().flce_get_status(workspace, ctypes.byref(n), stream)
     if st not in (0, 8):
@@ -538,4 +707,377 @@ def forward_backward(hidden, weight, labels, grad_logprob=None, grad_entropy=Non
     if reduced is not None:
         for k, name in enumerate(_OUT_NAMES):
             out[f"{name}_{reduction}"] = reduced[k:k + 1]
+    return out
+
+
+# ---- beside the head: embedding, policy loss, preference loss
+
+def _call(dev, fn, *args) -> None:
+    """fn(*args, stream) on torch's current stream of ``dev``, with it current."""
+    cuda = _torch().cuda
+    if cuda.current_device() == dev.index:
+        fn(*args, cuda.current_stream().cuda_stream)
+        return
+    with cuda.device(dev):
+        fn(*args, cuda.current_stream().cuda_stream)
+
+
+def _check_devices(dev, *named) -> None:
+    for name, t in named:
+        if t is not None and t.device != dev:
+            raise ValueError(f"{name} must be on {dev}, got {t.device}")
+
+
+def _choice(table, value, name):
+    if value not in table:
+        raise ValueError(f"{name} must be one of {sorted(table)}, got {value!r}")
+    return table[value]
+
+
+def _workspace(workspace, nbytes, dev):
+    """``workspace`` when it is large enough, else a new one."""
+    torch = _torch()
+    if workspace is not None:
+        _require(workspace, torch.uint8, 1, "workspace")
+        _check_devices(dev, ("workspace", workspace))
+        if workspace.numel() >= nbytes:
+            return workspace
+    return torch.empty(max(nbytes, 256), dtype=torch.uint8, device=dev)
+
+
+def _require_grad_dtype(t, name):
+    torch = _torch()
+    if not isinstance(t, torch.Tensor) or t.dtype not in (torch.bfloat16, torch.float32):
+        raise ValueError(f"{name} must be a bf16 or fp32 tensor")
+    _require(t, t.dtype, 2, name)
+    return FLCE_GRAD_F32 if t.dtype == torch.float32 else FLCE_GRAD_BF16
+
+
+def embedding(weight, tokens, layout: str = "hv", scale: float = 1.0, ignore_index: int = -100,
+              v_begin: int = 0, v_total=None, workspace=None) -> dict:
+    """{"hidden": bf16 [N,H], "workspace"}: hidden_i = scale * E[tokens_i].
+
+    weight: bf16, the head's [H,V] under layout "hv" (tied embeddings) or a
+    table [V,H] under "vh"; tokens: int64 [N]. Tokens equal to ignore_index or
+    outside the vocabulary give zero rows; the latter are counted
+    (flce_get_status on the workspace). With a vocabulary slice [v_begin,
+    v_begin + V) of v_total ids, tokens of other slices give zero rows.
+    """
+    torch = _torch()
+    _require(weight, torch.bfloat16, 2, "weight")
+    _require(tokens, torch.int64, 1, "tokens")
+    dev = weight.device
+    _check_devices(dev, ("tokens", tokens))
+    lay = _choice(_EMBED_LAYOUTS, layout, "layout")
+    H, V = weight.shape if lay == FLCE_EMBED_HV else (weight.shape[1], weight.shape[0])
+    N = tokens.shape[0]
+    opt = FlceEmbeddingOptions(int(ignore_index), float(scale), lay, FLCE_GRAD_BF16,
+                               FLCE_GRAD_BF16, 0)
+    nbytes, _ = flce_embedding_workspace_size(N, H, V, opt)
+    workspace = _workspace(workspace, nbytes, dev)
+    hidden = torch.empty((N, H), dtype=torch.bfloat16, device=dev)
+    _call(dev, flce_embedding_forward, weight.data_ptr(), tokens.data_ptr(), N, H, V,
+          int(v_begin), V if v_total is None else int(v_total), opt, hidden.data_ptr(),
+          workspace.data_ptr(), workspace.numel())
+    return {"hidden": hidden, "workspace": workspace}
+
+
+def embedding_backward(grad_hidden, tokens, vocab_size: int, layout: str = "hv",
+                       scale: float = 1.0, ignore_index: int = -100, v_begin: int = 0,
+                       v_total=None, grad_dtype: str = "bf16", grad_weight=None, workspace=None):
+    """grad_weight [H,V] ("hv") or [V,H] ("vh"), V = vocab_size (the slice's ids).
+
+    grad_hidden: bf16 or fp32 [N,H]; tokens and the options as for
+    ``embedding``. Without grad_weight a new tensor of ``grad_dtype`` is
+    returned, zero for ids that do not occur. With grad_weight (bf16 or fp32,
+    e.g. the head's gradient of a tied weight, from ``backward``) the gradient
+    is added to it in place and it is returned.
+    """
+    torch = _torch()
+    hdt = _require_grad_dtype(grad_hidden, "grad_hidden")
+    _require(tokens, torch.int64, 1, "tokens")
+    N, H = grad_hidden.shape
+    if tokens.shape[0] != N:
+        raise ValueError(f"tokens must have N = {N} elements")
+    dev = grad_hidden.device
+    _check_devices(dev, ("tokens", tokens), ("grad_weight", grad_weight))
+    lay = _choice(_EMBED_LAYOUTS, layout, "layout")
+    gdt = _choice(_GRAD_DTYPES, grad_dtype, "grad_dtype")
+    V = int(vocab_size)
+    shape = (H, V) if lay == FLCE_EMBED_HV else (V, H)
+    accumulate = grad_weight is not None
+    if accumulate:
+        gdt = _require_grad_dtype(grad_weight, "grad_weight")
+        if tuple(grad_weight.shape) != shape:
+            raise ValueError(f"grad_weight must be {list(shape)}")
+    opt = FlceEmbeddingOptions(int(ignore_index), float(scale), lay, hdt, gdt,
+                               1 if accumulate else 0)
+    _, nbytes = flce_embedding_workspace_size(N, H, V, opt)
+    workspace = _workspace(workspace, nbytes, dev)
+    if not accumulate:
+        grad_weight = torch.empty(shape, device=dev, dtype=torch.float32 if gdt == FLCE_GRAD_F32
+                                  else torch.bfloat16)
+    _call(dev, flce_embedding_backward, grad_hidden.data_ptr(), tokens.data_ptr(), N, H, V,
+          int(v_begin), V if v_total is None else int(v_total), opt, grad_weight.data_ptr(),
+          workspace.data_ptr(), workspace.numel())
+    return grad_weight
+
+
+def _token_arrays(labels, cu_seqlens, arrays):
+    """Checks int64 [N] labels, int64 cu_seqlens (or None) and the fp32 arrays
+    ((name, tensor, size); None tensors skipped); returns the device."""
+    torch = _torch()
+    dev = labels.device
+    if cu_seqlens is not None:
+        _check_devices(dev, ("cu_seqlens", cu_seqlens))
+    for name, t, size in arrays:
+        if t is None:
+            continue
+        _require(t, torch.float32, 1, name)
+        if t.shape[0] != size:
+            raise ValueError(f"{name} must have {size} element(s)")
+        _check_devices(dev, (name, t))
+    return dev
+
+
+def _sequences(labels, cu_seqlens):
+    """(N, number of sequences) after checking both tensors."""
+    torch = _torch()
+    _require(labels, torch.int64, 1, "labels")
+    if cu_seqlens is None:
+        return labels.shape[0], 1
+    _require(cu_seqlens, torch.int64, 1, "cu_seqlens")
+    if cu_seqlens.shape[0] < 2:
+        raise ValueError("cu_seqlens must have one element more than there are sequences")
+    return labels.shape[0], cu_seqlens.shape[0] - 1
+
+
+def _policy_options(clip_low=0.2, clip_high=0.2, dual_clip=0.0, kl_coef=0.0, kl_estimator="k3",
+                    entropy_coef=0.0, level="token", reduction="mean", ignore_index=-100,
+                    vocab_size=None, advantages_per_sequence=False):
+    return (FlcePolicyOptions(int(ignore_index), float(clip_low), float(clip_high),
+                              float(dual_clip), float(kl_coef), float(entropy_coef),
+                              _choice(_KL_ESTIMATORS, kl_estimator, "kl_estimator"),
+                              _choice(_RATIO_LEVELS, level, "level"),
+                              _choice(_POLICY_REDUCTIONS, reduction, "reduction"),
+                              1 if advantages_per_sequence else 0),
+            MAX_VOCAB if vocab_size is None else int(vocab_size))
+
+
+def _policy_check(opt, logprob, labels, old_logprob, advantages, entropy, ref_logprob, cu_seqlens,
+                  grad_loss):
+    """(device, N, B) of a policy call, after checking its tensors."""
+    N, B = _sequences(labels, cu_seqlens)
+    for name, t in (("logprob", logprob), ("old_logprob", old_logprob),
+                    ("advantages", advantages)):
+        if t is None:
+            raise ValueError(f"{name} is required")
+    if opt.kl_coef != 0.0 and ref_logprob is None:
+        raise ValueError("kl_coef needs ref_logprob")
+    if opt.level == 1 and (cu_seqlens is None or not opt.advantages_per_sequence):
+        raise ValueError("level 'sequence' needs cu_seqlens and advantages_per_sequence")
+    dev = _token_arrays(labels, cu_seqlens, (
+        ("logprob", logprob, N), ("old_logprob", old_logprob, N),
+        ("advantages", advantages, B if opt.advantages_per_sequence else N),
+        ("ref_logprob", ref_logprob, N), ("entropy", entropy, N), ("grad_loss", grad_loss, 1)))
+    return dev, N, B
+
+
+def policy_loss(logprob, labels, old_logprob, advantages, entropy=None, ref_logprob=None,
+                cu_seqlens=None, workspace=None, **options) -> dict:
+    """The clipped policy loss with a KL term (flce_policy_loss_forward), from
+    the head's per-token logprob (and entropy).
+
+    logprob, old_logprob, ref_logprob, entropy: fp32 [N]; labels: int64 [N];
+    cu_seqlens: int64 [B+1] sequence offsets, None for one sequence of all
+    tokens; advantages: fp32 [N], or [B] with advantages_per_sequence.
+
+    Options: clip_low = clip_high = 0.2, dual_clip = 0 (off), kl_coef = 0 (needs
+    ref_logprob otherwise), kl_estimator = "k1" | "k2" | "k3" (default),
+    entropy_coef = 0 (needs entropy otherwise), level = "token" (default) or
+    "sequence" ratios, reduction = "mean" over the valid tokens (default),
+    "sum" or "sequence_mean" (the mean over sequences of their token means),
+    ignore_index = -100 and vocab_size (None: the library's limit; labels
+    outside [0, vocab_size) mark tokens without a loss, as ignore_index does),
+    advantages_per_sequence = False.
+
+    Returns loss (fp32 [1]), stats (fp32 [8]: loss, policy term, kl, entropy,
+    share of clipped tokens, estimate of KL(old || new), valid tokens,
+    sequences with a valid token), seq_state (for ``policy_loss_backward``) and
+    workspace.
+    """
+    torch = _torch()
+    opt, V = _policy_options(**options)
+    dev, N, B = _policy_check(opt, logprob, labels, old_logprob, advantages, entropy, ref_logprob,
+                              cu_seqlens, None)
+    if opt.entropy_coef != 0.0 and entropy is None:
+        raise ValueError("entropy_coef needs entropy")
+    workspace = _workspace(workspace, flce_policy_workspace_size(N, B), dev)
+    stats = torch.empty(8, dtype=torch.float32, device=dev)
+    state = torch.empty((B + 1, 2), dtype=torch.float64, device=dev)
+    _call(dev, flce_policy_loss_forward, logprob.data_ptr(), _ptr(entropy),
+          old_logprob.data_ptr(), _ptr(ref_logprob), advantages.data_ptr(), labels.data_ptr(),
+          _ptr(cu_seqlens), N, B, V, opt, stats.data_ptr(), state.data_ptr(),
+          workspace.data_ptr(), workspace.numel())
+    return {"loss": stats[0:1], "stats": stats, "seq_state": state, "workspace": workspace}
+
+
+def policy_loss_backward(logprob, labels, old_logprob, advantages, seq_state, grad_loss=None,
+                         ref_logprob=None, cu_seqlens=None, want_entropy: bool = True,
+                         **options):
+    """(grad_logprob, grad_entropy), fp32 [N] each (grad_entropy None unless
+    want_entropy), of grad_loss (fp32 [1], None for 1) times the loss; inputs,
+    options and seq_state of the matching ``policy_loss``."""
+    torch = _torch()
+    opt, V = _policy_options(**options)
+    dev, N, B = _policy_check(opt, logprob, labels, old_logprob, advantages, None, ref_logprob,
+                              cu_seqlens, grad_loss)
+    _require(seq_state, torch.float64, 2, "seq_state")
+    if tuple(seq_state.shape) != (B + 1, 2):
+        raise ValueError(f"seq_state must be [{B + 1}, 2]")
+    _check_devices(dev, ("seq_state", seq_state))
+    glp = torch.empty(N, dtype=torch.float32, device=dev)
+    gent = torch.empty(N, dtype=torch.float32, device=dev) if want_entropy else None
+    _call(dev, flce_policy_loss_backward, logprob.data_ptr(), old_logprob.data_ptr(),
+          _ptr(ref_logprob), advantages.data_ptr(), labels.data_ptr(), _ptr(cu_seqlens), N, B, V,
+          opt, seq_state.data_ptr(), _ptr(grad_loss), glp.data_ptr(), _ptr(gent))
+    return glp, gent
+
+
+def policy_loss_forward_backward(logprob, labels, old_logprob, advantages, grad_loss=None,
+                                 entropy=None, ref_logprob=None, cu_seqlens=None, workspace=None,
+                                 **options) -> dict:
+    """``policy_loss`` (same inputs and options) and its gradients in one call,
+    for an upstream gradient known before it (grad_loss fp32 [1], None for 1):
+    loss, stats, workspace, grad_logprob (fp32 [N]) and, with entropy,
+    grad_entropy (fp32 [N]), ready for the head's ``backward`` under reduction
+    "none"."""
+    torch = _torch()
+    opt, V = _policy_options(**options)
+    dev, N, B = _policy_check(opt, logprob, labels, old_logprob, advantages, entropy, ref_logprob,
+                              cu_seqlens, grad_loss)
+    if opt.entropy_coef != 0.0 and entropy is None:
+        raise ValueError("entropy_coef needs entropy")
+    workspace = _workspace(workspace, flce_policy_workspace_size(N, B), dev)
+    stats = torch.empty(8, dtype=torch.float32, device=dev)
+    glp = torch.empty(N, dtype=torch.float32, device=dev)
+    out = {"loss": stats[0:1], "stats": stats, "workspace": workspace, "grad_logprob": glp}
+    gent = None
+    if entropy is not None:
+        gent = out["grad_entropy"] = torch.empty(N, dtype=torch.float32, device=dev)
+    _call(dev, flce_policy_loss_forward_backward, logprob.data_ptr(), _ptr(entropy),
+          old_logprob.data_ptr(), _ptr(ref_logprob), advantages.data_ptr(), labels.data_ptr(),
+          _ptr(cu_seqlens), N, B, V, opt, _ptr(grad_loss), stats.data_ptr(), glp.data_ptr(),
+          _ptr(gent), workspace.data_ptr(), workspace.numel())
+    return out
+
+
+def _preference_options(kind="sigmoid", beta=0.1, label_smoothing=0.0, margin=0.0,
+                        length_normalize=False, reduction="mean", ignore_index=-100,
+                        vocab_size=None):
+    return (FlcePreferenceOptions(int(ignore_index), float(beta), float(label_smoothing),
+                                  float(margin), _choice(_PREFERENCE_KINDS, kind, "kind"),
+                                  1 if length_normalize else 0,
+                                  _choice(_REDUCTIONS, reduction, "reduction")),
+            MAX_VOCAB if vocab_size is None else int(vocab_size))
+
+
+def _preference_check(opt, labels, cu_seqlens, grad_loss, arrays):
+    """(device, N, P) of a preference call, after checking its tensors (arrays:
+    (name, fp32 [N] tensor or None))."""
+    if cu_seqlens is None:
+        raise ValueError("cu_seqlens is required")
+    N, B = _sequences(labels, cu_seqlens)
+    if B % 2 != 0:
+        raise ValueError("cu_seqlens must hold an even number of sequences: the chosen ones, "
+                         "then the rejected ones")
+    P = B // 2
+    want = P if opt.reduction == FLCE_REDUCTION_NONE else 1
+    dev = _token_arrays(labels, cu_seqlens, [(name, t, N) for name, t in arrays]
+                        + [("grad_loss", grad_loss, want)])
+    return dev, N, P
+
+
+def _pair_outputs(P, dev, reduction):
+    """The outputs of a preference call: (loss pointer, dict)."""
+    torch = _torch()
+    pair, chosen, rejected = torch.empty((3, P), dtype=torch.float32, device=dev).unbind(0)
+    loss = (None if reduction == FLCE_REDUCTION_NONE
+            else torch.empty(1, dtype=torch.float32, device=dev))
+    return _ptr(loss), {"loss": pair if loss is None else loss, "pair_loss": pair,
+                        "chosen_reward": chosen, "rejected_reward": rejected}
+
+
+def preference_loss(logprob, labels, cu_seqlens, ref_logprob=None, workspace=None,
+                    **options) -> dict:
+    """The preference loss over P pairs (flce_preference_loss_forward), from
+    the head's per-token logprob.
+
+    logprob, ref_logprob (None: no reference): fp32 [N]; labels: int64 [N];
+    cu_seqlens: int64 [2P+1] offsets of the P chosen and then the P rejected
+    sequences; pair i is the sequences i and P + i.
+
+    Options: kind = "sigmoid" (default), "hinge" or "ipo", beta = 0.1,
+    label_smoothing = 0 (sigmoid only), margin = 0 (not for ipo),
+    length_normalize = False, reduction = "mean" over the pairs (default),
+    "sum" or "none", ignore_index = -100 and vocab_size as for ``policy_loss``.
+
+    Returns loss (fp32 [1], or [P] under "none"), pair_loss [P], chosen_reward
+    [P], rejected_reward [P], seq_state (for ``preference_loss_backward``) and
+    workspace.
+    """
+    torch = _torch()
+    opt, V = _preference_options(**options)
+    _require(logprob, torch.float32, 1, "logprob")
+    dev, N, P = _preference_check(opt, labels, cu_seqlens, None,
+                                  (("logprob", logprob), ("ref_logprob", ref_logprob)))
+    workspace = _workspace(workspace, flce_preference_workspace_size(N, P), dev)
+    loss, out = _pair_outputs(P, dev, opt.reduction)
+    state = torch.empty(2 * P + 1, dtype=torch.float64, device=dev)
+    _call(dev, flce_preference_loss_forward, logprob.data_ptr(), _ptr(ref_logprob),
+          labels.data_ptr(), cu_seqlens.data_ptr(), N, P, V, opt, loss,
+          out["pair_loss"].data_ptr(), out["chosen_reward"].data_ptr(),
+          out["rejected_reward"].data_ptr(), state.data_ptr(), workspace.data_ptr(),
+          workspace.numel())
+    out.update(seq_state=state, workspace=workspace)
+    return out
+
+
+def preference_loss_backward(labels, cu_seqlens, seq_state, grad_loss=None, **options):
+    """grad_logprob (fp32 [N]) of grad_loss (fp32 [1], or [P] under reduction
+    "none"; None for ones) times the loss; inputs, options and seq_state of the
+    matching ``preference_loss``."""
+    torch = _torch()
+    opt, V = _preference_options(**options)
+    dev, N, P = _preference_check(opt, labels, cu_seqlens, grad_loss, ())
+    _require(seq_state, torch.float64, 1, "seq_state")
+    if seq_state.shape[0] != 2 * P + 1:
+        raise ValueError(f"seq_state must have {2 * P + 1} elements")
+    _check_devices(dev, ("seq_state", seq_state))
+    glp = torch.empty(N, dtype=torch.float32, device=dev)
+    _call(dev, flce_preference_loss_backward, labels.data_ptr(), cu_seqlens.data_ptr(), N, P, V,
+          opt, seq_state.data_ptr(), _ptr(grad_loss), glp.data_ptr())
+    return glp
+
+
+def preference_loss_forward_backward(logprob, labels, cu_seqlens, grad_loss=None,
+                                     ref_logprob=None, workspace=None, **options) -> dict:
+    """``preference_loss`` (same inputs and options) and its gradient in one
+    call, for an upstream gradient known before it (grad_loss as for
+    ``preference_loss_backward``): loss, pair_loss, chosen_reward,
+    rejected_reward, grad_logprob (fp32 [N]) and workspace."""
+    torch = _torch()
+    opt, V = _preference_options(**options)
+    _require(logprob, torch.float32, 1, "logprob")
+    dev, N, P = _preference_check(opt, labels, cu_seqlens, grad_loss,
+                                  (("logprob", logprob), ("ref_logprob", ref_logprob)))
+    workspace = _workspace(workspace, flce_preference_workspace_size(N, P), dev)
+    loss, out = _pair_outputs(P, dev, opt.reduction)
+    glp = torch.empty(N, dtype=torch.float32, device=dev)
+    _call(dev, flce_preference_loss_forward_backward, logprob.data_ptr(), _ptr(ref_logprob),
+          labels.data_ptr(), cu_seqlens.data_ptr(), N, P, V, opt, _ptr(grad_loss), loss,
+          out["pair_loss"].data_ptr(), out["chosen_reward"].data_ptr(),
+          out["rejected_reward"].data_ptr(), glp.data_ptr(), workspace.data_ptr(),
+          workspace.numel())
+    out.update(grad_logprob=glp, workspace=workspace)
     return out

@@ -5,6 +5,10 @@ outputs, the label log-probability and the entropy. Following that page's
 "Equivalent compute logic", the first output is the log-probability of the
 label (minus the cross-entropy), not the cross-entropy itself.
 
+``embedding``, ``policy_loss`` and ``preference_loss`` are the operators
+beside the head in the same manner: the tied (or separate) embedding lookup,
+and the losses of RL and preference tuning on the head's per-token outputs.
+
 Marshalling only: the forward calls flce_forward through ``flce.forward``
 and keeps the per-token lse and entropy; the backward hands the upstream
 gradients of the two outputs to flce_backward through ``flce.backward``.
@@ -13,9 +17,12 @@ from __future__ import annotations
 
 import torch
 
+from torch.autograd.function import once_differentiable
+
 from . import flce
 
-__all__ = ["LinearCrossEntropy", "linear_cross_entropy"]
+__all__ = ["LinearCrossEntropy", "linear_cross_entropy", "Embedding", "embedding",
+           "PolicyLoss", "policy_loss", "PreferenceLoss", "preference_loss"]
 
 
 class LinearCrossEntropy(torch.autograd.Function):
@@ -68,3 +75,104 @@ def linear_cross_entropy(hidden, weight, labels, reduction="mean", ignore_index=
     hidden and weight (gradients in bf16)."""
     return LinearCrossEntropy.apply(hidden, weight, labels, reduction, ignore_index, softcap,
                                     class_weight, entropy_reduction)
+
+
+class Embedding(torch.autograd.Function):
+    """The scaled lookup; see ``embedding``."""
+
+    @staticmethod
+    def forward(ctx, weight, tokens, layout, scale, ignore_index):
+        hidden = flce.embedding(weight, tokens, layout=layout, scale=scale,
+                                ignore_index=ignore_index)["hidden"]
+        ctx.save_for_backward(tokens)
+        ctx.vocab_size = weight.shape[1 if layout == "hv" else 0]
+        ctx.layout, ctx.scale, ctx.ignore_index = layout, scale, ignore_index
+        return hidden
+
+    @staticmethod
+    @once_differentiable
+    def backward(ctx, grad_hidden):
+        tokens, = ctx.saved_tensors
+        gw = flce.embedding_backward(grad_hidden.contiguous(), tokens, ctx.vocab_size,
+                                     layout=ctx.layout, scale=ctx.scale,
+                                     ignore_index=ctx.ignore_index)
+        return gw, None, None, None, None
+
+
+def embedding(weight, tokens, layout="hv", scale=1.0, ignore_index=-100):
+    """hidden bf16 [N,H] = scale * E[tokens] for tokens int64 [N] and weight
+    bf16: the head's [H,V] (layout "hv", tied embeddings) or a table [V,H]
+    ("vh"). Zero rows at ignore_index and at ids outside the vocabulary.
+    Differentiable with respect to weight (gradient in bf16)."""
+    return Embedding.apply(weight, tokens, layout, scale, ignore_index)
+
+
+class PolicyLoss(torch.autograd.Function):
+    """(loss, stats) of the clipped policy loss; see ``policy_loss``."""
+
+    @staticmethod
+    def forward(ctx, logprob, entropy, labels, old_logprob, advantages, ref_logprob, cu_seqlens,
+                options):
+        out = flce.policy_loss(logprob, labels, old_logprob, advantages, entropy=entropy,
+                               ref_logprob=ref_logprob, cu_seqlens=cu_seqlens, **options)
+        ctx.save_for_backward(logprob, labels, old_logprob, advantages, ref_logprob, cu_seqlens,
+                              out["seq_state"])
+        ctx.options = options
+        ctx.mark_non_differentiable(out["stats"])
+        return out["loss"].reshape(()).clone(), out["stats"]
+
+    @staticmethod
+    @once_differentiable
+    def backward(ctx, grad_loss, _grad_stats):
+        logprob, labels, old_logprob, advantages, ref_logprob, cu_seqlens, state = \
+            ctx.saved_tensors
+        glp, gent = flce.policy_loss_backward(
+            logprob, labels, old_logprob, advantages, state,
+            grad_loss=grad_loss.float().reshape(1).contiguous(), ref_logprob=ref_logprob,
+            cu_seqlens=cu_seqlens, want_entropy=ctx.needs_input_grad[1], **ctx.options)
+        return glp, gent, None, None, None, None, None, None
+
+
+def policy_loss(logprob, labels, old_logprob, advantages, entropy=None, ref_logprob=None,
+                cu_seqlens=None, **options):
+    """(loss, stats): the clipped policy loss of ``flce.policy_loss`` (same
+    arguments and options) as a 0-d fp32 tensor, and its statistics (fp32 [8],
+    not differentiable). Differentiable with respect to logprob and entropy,
+    e.g. the outputs of ``linear_cross_entropy(..., reduction="none")``;
+    old_logprob, ref_logprob and advantages are constants."""
+    return PolicyLoss.apply(logprob, entropy, labels, old_logprob, advantages, ref_logprob,
+                            cu_seqlens, options)
+
+
+class PreferenceLoss(torch.autograd.Function):
+    """(loss, chosen_reward, rejected_reward); see ``preference_loss``."""
+
+    @staticmethod
+    def forward(ctx, logprob, labels, cu_seqlens, ref_logprob, options):
+        out = flce.preference_loss(logprob, labels, cu_seqlens, ref_logprob=ref_logprob,
+                                   **options)
+        ctx.save_for_backward(labels, cu_seqlens, out["seq_state"])
+        ctx.options = options
+        ctx.mark_non_differentiable(out["chosen_reward"], out["rejected_reward"])
+        loss = out["loss"].clone()
+        if options.get("reduction", "mean") != "none":
+            loss = loss.reshape(())
+        return loss, out["chosen_reward"], out["rejected_reward"]
+
+    @staticmethod
+    @once_differentiable
+    def backward(ctx, grad_loss, _grad_chosen, _grad_rejected):
+        labels, cu_seqlens, state = ctx.saved_tensors
+        glp = flce.preference_loss_backward(
+            labels, cu_seqlens, state, grad_loss=grad_loss.float().reshape(-1).contiguous(),
+            **ctx.options)
+        return glp, None, None, None, None
+
+
+def preference_loss(logprob, labels, cu_seqlens, ref_logprob=None, **options):
+    """(loss, chosen_reward, rejected_reward): the preference loss of
+    ``flce.preference_loss`` (same arguments and options), 0-d or [P] under
+    reduction "none", and the rewards [P] of the two sides (not
+    differentiable). Differentiable with respect to logprob; ref_logprob is a
+    constant."""
+    return PreferenceLoss.apply(logprob, labels, cu_seqlens, ref_logprob, options)
