@@ -480,6 +480,7 @@ flce_status_t flce_policy_workspace_size(int64_t N, int64_t B, size_t* bytes);
 /* logprob, old_logprob (and where given entropy, ref_logprob): device fp32 [N];
  * advantages device fp32 [N] or [B]; labels device int64 [N]; cu_seqlens device
  * int64 [B+1], or NULL with B = 1: one sequence of all tokens.
+ *   loss       device fp32 [1], or NULL
  *   stats      device fp32 [8]: loss, policy, kl, entropy, share of clipped
  *              tokens, -d (the k1 estimate of KL(old || new)), each reduced like
  *              the loss; then the number of valid tokens and of sequences that
@@ -489,8 +490,8 @@ flce_status_t flce_policy_loss_forward(const float* logprob, const float* entrop
                                        const float* old_logprob, const float* ref_logprob,
                                        const float* advantages, const int64_t* labels,
                                        const int64_t* cu_seqlens, int64_t N, int64_t B, int64_t V,
-                                       const flce_policy_options_t* opt, float* stats,
-                                       double* seq_state, void* workspace, size_t workspace_bytes,
+                                       const flce_policy_options_t* opt, float* loss,
+                                       float* stats, double* seq_state, void* workspace, size_t workspace_bytes,
                                        void* stream);
 
 /* grad_logprob, and unless NULL grad_entropy (device fp32 [N]), of
@@ -510,8 +511,8 @@ flce_status_t flce_policy_loss_backward(const float* logprob, const float* old_l
 flce_status_t flce_policy_loss_forward_backward(
     const float* logprob, const float* entropy, const float* old_logprob, const float* ref_logprob,
     const float* advantages, const int64_t* labels, const int64_t* cu_seqlens, int64_t N, int64_t B,
-    int64_t V, const flce_policy_options_t* opt, const float* grad_loss, float* stats,
-    float* grad_logprob, float* grad_entropy, void* workspace, size_t workspace_bytes,
+    int64_t V, const flce_policy_options_t* opt, const float* grad_loss, float* loss,
+    float* stats, float* grad_logprob, float* grad_entropy, void* workspace, size_t workspace_bytes,
     void* stream);
 
 /* Preference loss over P pairs of sequences: sequence i < P is the chosen and

@@ -3,7 +3,7 @@
 //
 // Both are sums over ragged sequences of a packed batch, then a small formula a
 // sequence (or pair), then one gradient value a token:
-//   parts      every 64-lane wave takes a tile of 256 consecutive tokens, forms
+//   parts      every 64-lane wave takes a tile of consecutive tokens, forms
 //              the per-token terms and sums them over each sequence's share of
 //              the tile. The share of sequence s in tile t goes to parts[s + t]:
 //              walking the batch, either s or t grows by one from a share to the
@@ -49,30 +49,72 @@ __device__ __forceinline__ int64_t wave_count_le(const int64_t* a, int64_t n, in
   return lo;
 }
 
-// The sequences that the tokens [t0, t1) can belong to: [s0, s1], empty (s1 < s0)
-// when all lie before the first or behind the last sequence.
-struct SeqRange {
-  int64_t s0, s1;
+// The sequences that a tile of tokens [t0, t1) can belong to: ns of them from s0
+// (none when all the tokens lie before the first or behind the last sequence).
+// Lane k has off, where sequence s0 + k begins, counted from t0 and clamped to
+// [0, kLossTile]; lane ns has the last one's end. Tiles of up to kOffSeqs sequences
+// need no other load of the offsets.
+constexpr int kOffSeqs = 62;
+struct TileSeqs {
+  int64_t s0, ns;
+  int off;
 };
-__device__ __forceinline__ SeqRange tile_sequences(const int64_t* cu, int64_t B, int64_t t0,
+__device__ __forceinline__ TileSeqs tile_sequences(const int64_t* cu, int64_t B, int64_t t0,
                                                    int64_t t1) {
-  if (cu == nullptr) return {0, 0};
-  const int64_t a = wave_count_le(cu, B + 1, t0) - 1, b = wave_count_le(cu, B + 1, t1 - 1) - 1;
-  return {a < 0 ? 0 : a, b >= B ? B - 1 : b};
+  const int lane = threadIdx.x & 63;
+  if (cu == nullptr) return {0, 1, lane == 0 ? 0 : kLossTile};
+  const int64_t n = B + 1;
+  int64_t s0, c1, v;
+  if (n <= 64) {  // one load has everything
+    const int64_t x = cu[lane < n ? lane : n - 1];
+    const int c0 = __popcll(__builtin_amdgcn_ballot_w64(lane < n && x <= t0));
+    c1 = __popcll(__builtin_amdgcn_ballot_w64(lane < n && x <= t1 - 1));
+    s0 = c0 > 0 ? c0 - 1 : 0;
+    const int from = s0 + lane < n ? (int)s0 + lane : (int)n - 1;
+    v = (int64_t)__shfl((long long)x, from, 64);
+  } else {
+    const int64_t c0 = wave_count_le(cu, n, t0);
+    s0 = c0 > 0 ? c0 - 1 : 0;
+    v = cu[s0 + lane < n ? s0 + lane : n - 1];
+    const int c = __popcll(__builtin_amdgcn_ballot_w64(s0 + lane < n && v <= t1 - 1));
+    c1 = c < 64 ? s0 + c : wave_count_le(cu, n, t1 - 1);
+  }
+  const int64_t s1 = c1 - 1 < B - 1 ? c1 - 1 : B - 1;
+  const int64_t d = v < t0 ? 0 : (v < t1 ? v - t0 : kLossTile);
+  return {s0, s1 - s0 + 1, (int)d};
 }
 
-// Sequence of token t within [s0, s1], or -1 when it lies in none.
-__device__ __forceinline__ int64_t token_sequence(const int64_t* cu, const SeqRange& r, int64_t t) {
-  if (cu == nullptr) return 0;
-  int64_t lo = r.s0, hi = r.s1;
-  while (lo < hi) {
-    const int64_t mid = (lo + hi + 1) >> 1;
-    if (cu[mid] <= t)
-      lo = mid;
-    else
-      hi = mid - 1;
+// Rank (sequence - s0) of the tile's token tl, or -1 when it lies in none. All
+// lanes of the wave take part.
+__device__ __forceinline__ int token_rank(const int64_t* cu, const TileSeqs& r, int64_t t0,
+                                          int tl) {
+  if (r.ns <= 0) return -1;
+  int lo = 0;
+  bool in;
+  if (r.ns <= kOffSeqs) {
+    const int ns = (int)r.ns;
+    for (int k = 1; k < ns; ++k) lo += __builtin_amdgcn_readlane(r.off, k) <= tl ? 1 : 0;
+    in = __builtin_amdgcn_readlane(r.off, 0) <= tl && tl < __builtin_amdgcn_readlane(r.off, ns);
+  } else {
+    const int64_t* c = cu + r.s0;
+    int hi = (int)r.ns - 1;
+    while (lo < hi) {
+      const int mid = (lo + hi + 1) >> 1;
+      if (c[mid] <= t0 + tl)
+        lo = mid;
+      else
+        hi = mid - 1;
+    }
+    in = c[lo] <= t0 + tl && t0 + tl < c[lo + 1];
   }
-  return lo <= r.s1 && cu[lo] <= t && t < cu[lo + 1] ? lo : -1;
+  return in ? lo : -1;
+}
+
+// Whether the tile's token tl, of rank k >= 0, is the last of its sequence.
+__device__ __forceinline__ bool ends_sequence(const int64_t* cu, const TileSeqs& r, int64_t t0,
+                                              int tl, int k) {
+  if (r.ns <= kOffSeqs) return __shfl(r.off, k + 1, 64) == tl + 1;
+  return cu[r.s0 + k + 1] == t0 + tl + 1;
 }
 
 __device__ __forceinline__ int64_t seq_begin(const int64_t* cu, int64_t s) {
@@ -89,6 +131,30 @@ __device__ __forceinline__ bool label_valid(int64_t y, int64_t ignore_index, int
 // ---- wave and block sums --------------------------------------------------------
 
 __device__ __forceinline__ double shfl_down_f64(double v, int d) { return __shfl_down(v, d, 64); }
+
+// Sums over the wave in lane 63: within rows of 16 lanes by shifts of 1, 2, 4 and
+// 8, then row 0 into 1 and 2 into 3, then 1 into 3.
+template <int CTRL, int ROWS>
+__device__ __forceinline__ int dpp_or_0(int v) {
+  return __builtin_amdgcn_update_dpp(0, v, CTRL, ROWS, 0xf, false);
+}
+template <int CTRL, int ROWS>
+__device__ __forceinline__ double dpp_or_0(double v) {
+  const uint64_t u = __builtin_bit_cast(uint64_t, v);
+  const uint32_t lo = (uint32_t)dpp_or_0<CTRL, ROWS>((int)(uint32_t)u);
+  const uint32_t hi = (uint32_t)dpp_or_0<CTRL, ROWS>((int)(uint32_t)(u >> 32));
+  return __builtin_bit_cast(double, ((uint64_t)hi << 32) | lo);
+}
+template <class T>
+__device__ __forceinline__ T wave_sum_dpp(T v) {
+  v += dpp_or_0<0x111, 0xf>(v);  // row_shr:1
+  v += dpp_or_0<0x112, 0xf>(v);  // row_shr:2
+  v += dpp_or_0<0x114, 0xf>(v);  // row_shr:4
+  v += dpp_or_0<0x118, 0xf>(v);  // row_shr:8
+  v += dpp_or_0<0x142, 0xa>(v);  // row_bcast:15 into rows 1 and 3
+  v += dpp_or_0<0x143, 0xc>(v);  // row_bcast:31 into rows 2 and 3
+  return v;
+}
 
 // What a share of a sequence, a sequence, and the batch sum up to: the loss's
 // own terms x[]; n valid tokens; c clipped tokens (of the batch: sequences with
@@ -110,8 +176,38 @@ struct LossSum {
     inv += o.inv;
     bad += o.bad;
   }
+  __device__ LossSum up(int d) const {
+    LossSum o;
+#pragma unroll
+    for (int k = 0; k < K; ++k) o.x[k] = __shfl_up(x[k], d, 64);
+    o.n = __shfl_up(n, d, 64);
+    o.c = __shfl_up(c, d, 64);
+    o.inv = __shfl_up(inv, d, 64);
+    o.bad = 0;
+    return o;
+  }
+  __device__ LossSum from(int l) const {
+    LossSum o;
+#pragma unroll
+    for (int k = 0; k < K; ++k) o.x[k] = __shfl(x[k], l, 64);
+    o.n = __shfl(n, l, 64);
+    o.c = __shfl(c, l, 64);
+    o.inv = __shfl(inv, l, 64);
+    o.bad = 0;
+    return o;
+  }
+  // Sum over the wave, in lane 63.
+  __device__ void wave_sum() {
+#pragma unroll
+    for (int k = 0; k < K; ++k) x[k] = wave_sum_dpp(x[k]);
+    n = wave_sum_dpp(n);
+    c = wave_sum_dpp(c);
+    inv = wave_sum_dpp(inv);
+    bad = wave_sum_dpp(bad);
+  }
   // Sum over each group of g lanes (a power of two), in its first lane.
   __device__ void group_sum(int g) {
+#pragma unroll 1
     for (int d = g >> 1; d > 0; d >>= 1) {
 #pragma unroll
       for (int k = 0; k < K; ++k) x[k] += __shfl_down(x[k], d, 64);
@@ -123,25 +219,22 @@ struct LossSum {
   }
 };
 
-// Sum over the block, waves in order; every thread gets it. sh: one entry a wave.
+// Sum of the first `used` waves over the block, waves in order, in thread 0. sh:
+// one entry a wave.
 template <class S>
-__device__ __forceinline__ S block_total(S v, S* sh) {
-  const int nw = blockDim.x >> 6;
-  v.group_sum(64);
-  if ((threadIdx.x & 63) == 0) sh[threadIdx.x >> 6] = v;
+__device__ __forceinline__ S block_total(S v, int used, S* sh) {
+  const int lane = threadIdx.x & 63, w = threadIdx.x >> 6;
+  if (w < used) {
+    v.wave_sum();
+    if (lane == 63) sh[w] = v;
+  }
   __syncthreads();
   S r;
   r.clear();
-  for (int w = 0; w < nw; ++w) r.add(sh[w]);
+  if (threadIdx.x == 0)
+    for (int k = 0; k < used; ++k) r.add(sh[k]);
   __syncthreads();
   return r;
-}
-
-// Orders this wave's LDS writes before its later LDS reads (other lanes').
-__device__ __forceinline__ void wave_lds_fence() {
-  __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
-  __builtin_amdgcn_wave_barrier();
-  __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
 }
 
 // Everything the kernels of one call share; Loss is PolicyLoss or PreferenceLoss.
@@ -154,10 +247,11 @@ struct LossArgs {
   int64_t N, B, V, ignore_index;
   int64_t items;                // sequences, or pairs
   int64_t tiles;
+  int rows;                     // of 64 tokens a tile: 1, 2 or 4
   typename Loss::Share* parts;    // [B + tiles]
   typename Loss::Share* seq_sum;  // [B]
   typename Loss::Total* totals;   // [blocks of the sequences kernel]
-  int32_t* header;                // [0] invalid labels and offsets
+  int32_t* header;                // [0] invalid labels and offsets, [2] blocks that are done
   double* state;                  // see Loss
 };
 
@@ -172,11 +266,13 @@ struct PolicyLoss {
     int kl, by_sequence, adv_seq, reduction;
   };
   struct Out {
+    float* loss;             // [1] or null
     float* stats;            // [8]
     const float* grad_loss;  // [1] or null
     float* grad_logprob;
     float* grad_entropy;     // or null
   };
+  static __host__ __device__ constexpr int state_size(int B) { return 2 * (B + 1); }
   static constexpr bool kGradReads = true;  // the gradient needs the per-token inputs
   // state[2 s]: token weight of sequence s before the batch's factor;
   // state[2 s + 1]: derivative of the policy term by the mean of d (sequence
@@ -275,6 +371,7 @@ struct PolicyLoss {
     const double kl = in.kl_coef != 0.0 ? in.kl_coef * v.x[2] : 0.0;
     const double ent = in.ent_coef != 0.0 ? in.ent_coef * v.x[3] : 0.0;
     s[0] = (float)(k * (v.x[1] + kl - ent));
+    if (a.out.loss != nullptr) a.out.loss[0] = s[0];
     s[1] = (float)(k * v.x[1]);
     s[2] = (float)(k * v.x[2]);
     s[3] = (float)(k * v.x[3]);
@@ -327,6 +424,7 @@ struct PreferenceLoss {
     const float* grad_loss;  // [P] under NONE, else [1]; or null
     float* grad_logprob;
   };
+  static __host__ __device__ constexpr int state_size(int B) { return B + 1; }
   static constexpr bool kGradReads = false;
   // state[s]: gradient of the reduced loss by a valid token's logprob of
   // sequence s; state[B] = 1, or NaN after bad offsets.
@@ -411,60 +509,102 @@ struct PreferenceLoss {
 
 // ---- the three steps ----------------------------------------------------------------
 
-// Step 1, one wave, one tile: sh holds the wave's 256 token terms. The sums run
-// in groups of lanes, a group a sequence, as many lanes as the tile's sequences
-// leave each (64 for one long sequence, 1 for 64 short ones).
-template <class Loss>
-__device__ __forceinline__ void tile_parts(const LossArgs<Loss>& a, int64_t tile,
-                                           typename Loss::Share* sh) {
-  const int lane = threadIdx.x & 63;
-  const int64_t t0 = tile * kLossTile;
-  const int64_t t1 = a.N - t0 < kLossTile ? a.N : t0 + kLossTile;
-  typename Loss::Raw raw[kLossTile / 64];
-  int64_t y[kLossTile / 64];
+// A tile's inputs, lane l having the tokens t0 + 64 j + l: all loads are issued at
+// once, and the rows are then taken one after another by a loop that is not
+// unrolled (next() moves the rows up), which keeps the float64 exponentials to
+// one copy.
+template <class Loss, bool READ>
+struct TileRows {
+  typename Loss::Raw raw[kLossRows];
+  int64_t y[kLossRows];
+  __device__ __forceinline__ void load(const LossArgs<Loss>& a, int64_t t0) {
 #pragma unroll
-  for (int j = 0; j < kLossTile / 64; ++j) {
-    const int64_t t = t0 + j * 64 + lane;
-    const int64_t tc = t < a.N ? t : a.N - 1;
-    y[j] = a.labels[tc];
-    raw[j] = Loss::load(a, tc);
+    for (int j = 0; j < kLossRows; ++j) {
+      if (j >= a.rows) break;
+      const int64_t t = t0 + j * 64 + (threadIdx.x & 63);
+      const int64_t tc = t < a.N ? t : a.N - 1;
+      y[j] = a.labels[tc];
+      if constexpr (READ) raw[j] = Loss::load(a, tc);
+    }
   }
-  const SeqRange r = tile_sequences(a.cu, a.B, t0, t1);
-  const int64_t ns = r.s1 - r.s0 + 1;
-  if (ns <= 0) return;
+  __device__ __forceinline__ void next() {
 #pragma unroll
-  for (int j = 0; j < kLossTile / 64; ++j) {
-    const int64_t t = t0 + j * 64 + lane;
-    typename Loss::Share v;
+    for (int j = 0; j + 1 < kLossRows; ++j) {
+      y[j] = y[j + 1];
+      raw[j] = raw[j + 1];
+    }
+  }
+};
+
+// Step 1, one wave, one tile. A tile in one or two sequences, the usual case,
+// adds each lane's tokens and reduces them over the wave once a sequence. With
+// more, each row of 64 tokens is scanned with the sequences as segments, the open
+// segment carried to the next row, and the lane with a sequence's last token in
+// the tile has its share. No LDS either way, so the occupancy is the registers'.
+template <class Loss>
+__device__ __forceinline__ void tile_parts(const LossArgs<Loss>& a, int64_t tile) {
+  using Share = typename Loss::Share;
+  const int lane = threadIdx.x & 63;
+  const int64_t t0 = tile * a.rows * 64;
+  const int64_t t1 = a.N - t0 < a.rows * 64 ? a.N : t0 + a.rows * 64;
+  TileRows<Loss, true> in;
+  in.load(a, t0);
+  const TileSeqs r = tile_sequences(a.cu, a.B, t0, t1);
+  if (r.ns <= 0) return;
+  Share v0, v1;  // up to two sequences: their sums; more: v0 is the carried segment's
+  v0.clear();
+  v1.clear();
+  int rank0 = -1;        // the carried segment
+  bool any0 = false, any1 = false;
+#pragma unroll 1
+  for (int j = 0; j < a.rows; ++j, in.next()) {
+    const int tl = j * 64 + lane;
+    const int64_t t = t0 + tl;
+    int rank = token_rank(a.cu, r, t0, tl);
+    if (t >= a.N) rank = -1;
+    Share v;
     v.clear();
-    const int64_t s = t < a.N ? token_sequence(a.cu, r, t) : -1;
-    if (s >= 0) {
-      if (label_valid(y[j], a.ignore_index, a.V))
-        Loss::token(a, raw[j], t, s, v);
-      else if (y[j] != a.ignore_index)
+    if (rank >= 0) {
+      if (label_valid(in.y[0], a.ignore_index, a.V))
+        Loss::token(a, in.raw[0], t, r.s0 + rank, v);
+      else if (in.y[0] != a.ignore_index)
         v.inv = 1;
     }
-    sh[j * 64 + lane] = v;
-  }
-  wave_lds_fence();
-  int g = 64;
-  while (g > 1 && 64 / g < ns) g >>= 1;
-  const int per = 64 / g, k = lane & (g - 1);
-  for (int64_t i = 0; i < ns; i += per) {
-    const int64_t s = r.s0 + i + lane / g;
-    int b = 0, e = 0;
-    if (s <= r.s1) {
-      const int64_t sb = seq_begin(a.cu, s), se = seq_end(a.cu, s, a.N);
-      b = (int)((sb < t0 ? t0 : (sb < t1 ? sb : t1)) - t0);
-      e = (int)((se < t0 ? t0 : (se < t1 ? se : t1)) - t0);
+    if (r.ns <= 2) {
+      if (rank == 0) {
+        v0.add(v);
+        any0 = true;
+      } else if (rank == 1) {
+        v1.add(v);
+        any1 = true;
+      }
+      continue;
     }
-    typename Loss::Share v;
-    v.clear();
-    for (int q = b + k; q < e; q += g) v.add(sh[q]);
-    v.group_sum(g);
-    if (k == 0 && b < e) a.parts[s + tile] = v;
+    const int before = __shfl_up(rank, 1, 64);
+    const uint64_t heads = __builtin_amdgcn_ballot_w64(lane == 0 || before != rank);
+    // This lane's segment starts at the last head at or below it.
+    const int head = 63 - __builtin_clzll(heads & (~(uint64_t)0 >> (63 - lane)));
+#pragma unroll 1
+    for (int d = 1; d < 64; d <<= 1) {
+      const Share o = v.up(d);
+      if (lane - d >= head) v.add(o);
+    }
+    if (rank == rank0 && rank >= 0) v.add(v0);  // only the first segment can match
+    const bool ends = ends_sequence(a.cu, r, t0, tl, rank < 0 ? 0 : rank);
+    if (rank >= 0 && (ends || t + 1 == t1)) a.parts[r.s0 + rank + tile] = v;
+    v0 = v.from(63);
+    rank0 = __shfl(rank, 63, 64);
   }
-  wave_lds_fence();  // the next tile reuses sh
+  if (r.ns > 2) return;
+#pragma unroll 1
+  for (int i = 0; i < 2; ++i) {
+    if (__builtin_amdgcn_ballot_w64(any0) != 0) {
+      v0.wave_sum();
+      if (lane == 63) a.parts[r.s0 + i + tile] = v0;
+    }
+    v0 = v1;
+    any0 = any1;
+  }
 }
 
 // Shares of sequence s: tiles [p0, p0 + count); a sequence with bad offsets has
@@ -473,11 +613,12 @@ struct SeqParts {
   int64_t p0, count;
   bool bad;
 };
-__device__ __forceinline__ SeqParts seq_parts(const int64_t* cu, int64_t N, int64_t s) {
+__device__ __forceinline__ SeqParts seq_parts(const int64_t* cu, int64_t N, int rows, int64_t s) {
   const int64_t b = seq_begin(cu, s), e = seq_end(cu, s, N);
   if (b < 0 || e < b || e > N) return {0, 0, true};
   if (b == e) return {0, 0, false};
-  return {b / kLossTile, (e - 1) / kLossTile - b / kLossTile + 1, false};
+  const int sh = 5 + __builtin_ffs(rows);  // log2 of the tile: rows is 1, 2 or 4
+  return {b >> sh, ((e - 1) >> sh) - (b >> sh) + 1, false};
 }
 
 // Step 2, one block, items [i0, i1): adds up the sequences' shares, then the
@@ -492,8 +633,7 @@ __device__ __forceinline__ typename Loss::Total sum_sequences(const LossArgs<Los
   __shared__ Total sh_total[16];
   const int64_t m = i1 - i0, local = m * Loss::kSides;
   auto seq = [&](int64_t j) { return j < m ? i0 + j : a.items + i0 + (j - m); };
-  int g = 1;
-  while (g < 64 && g * a.B < a.tiles) g <<= 1;
+  const int g = lanes_per_sequence(a.B, a.tiles);
   const int64_t longest = (int64_t)g * 16;
   const int groups = (int)blockDim.x / g, k = threadIdx.x & (g - 1);
   bool any_long = false;
@@ -505,7 +645,7 @@ __device__ __forceinline__ typename Loss::Total sum_sequences(const LossArgs<Los
     int64_t s = 0;
     if (mine) {
       s = seq(j);
-      const SeqParts p = seq_parts(a.cu, a.N, s);
+      const SeqParts p = seq_parts(a.cu, a.N, a.rows, s);
       if (p.count > longest) {
         any_long = true;
         mine = false;
@@ -523,16 +663,16 @@ __device__ __forceinline__ typename Loss::Total sum_sequences(const LossArgs<Los
   if (__syncthreads_or(any_long ? 1 : 0)) {
     for (int64_t jb = 0; jb < local; jb += 64) {
       const int64_t jl = jb + (threadIdx.x & 63);
-      const bool lg = jl < local && seq_parts(a.cu, a.N, seq(jl)).count > longest;
+      const bool lg = jl < local && seq_parts(a.cu, a.N, a.rows, seq(jl)).count > longest;
       uint64_t bits = __builtin_amdgcn_ballot_w64(lg);  // the same in every wave
       while (bits != 0) {
         const int64_t s = seq(jb + __builtin_ctzll(bits));
         bits &= bits - 1;
-        const SeqParts p = seq_parts(a.cu, a.N, s);
+        const SeqParts p = seq_parts(a.cu, a.N, a.rows, s);
         Share v;
         v.clear();
         for (int64_t q = threadIdx.x; q < p.count; q += blockDim.x) v.add(a.parts[s + p.p0 + q]);
-        v = block_total(v, sh_share);
+        v = block_total(v, (int)(blockDim.x >> 6), sh_share);
         if (threadIdx.x == 0) a.seq_sum[s] = v;
       }
     }
@@ -541,7 +681,8 @@ __device__ __forceinline__ typename Loss::Total sum_sequences(const LossArgs<Los
   Total t;
   t.clear();
   for (int64_t i = i0 + threadIdx.x; i < i1; i += blockDim.x) Loss::item(a, i, t);
-  return block_total(t, sh_total);
+  const int64_t waves = (m + 63) >> 6, nw = blockDim.x >> 6;
+  return block_total(t, (int)(waves < nw ? waves : nw), sh_total);
 }
 
 template <class Loss>
@@ -557,57 +698,56 @@ __device__ __forceinline__ void finish_batch(const LossArgs<Loss>& a,
 // Step 3, one wave, one tile.
 template <class Loss>
 __device__ __forceinline__ void tile_grads(const LossArgs<Loss>& a, int64_t tile) {
-  const int lane = threadIdx.x & 63;
-  const int64_t t0 = tile * kLossTile;
-  const int64_t t1 = a.N - t0 < kLossTile ? a.N : t0 + kLossTile;
-  typename Loss::Raw raw[kLossTile / 64];
-  int64_t y[kLossTile / 64];
-#pragma unroll
-  for (int j = 0; j < kLossTile / 64; ++j) {
-    const int64_t t = t0 + j * 64 + lane;
-    const int64_t tc = t < a.N ? t : a.N - 1;
-    y[j] = a.labels[tc];
-    if constexpr (Loss::kGradReads) raw[j] = Loss::load(a, tc);
-  }
-  const SeqRange r = tile_sequences(a.cu, a.B, t0, t1);
+  const int64_t t0 = tile * a.rows * 64;
+  const int64_t t1 = a.N - t0 < a.rows * 64 ? a.N : t0 + a.rows * 64;
+  TileRows<Loss, Loss::kGradReads> in;
+  in.load(a, t0);
+  const TileSeqs r = tile_sequences(a.cu, a.B, t0, t1);
   const double scale = Loss::grad_scale(a);
-#pragma unroll
-  for (int j = 0; j < kLossTile / 64; ++j) {
-    const int64_t t = t0 + j * 64 + lane;
+#pragma unroll 1
+  for (int j = 0; j < a.rows; ++j, in.next()) {
+    const int tl = j * 64 + (threadIdx.x & 63);
+    const int rank = token_rank(a.cu, r, t0, tl);
+    const int64_t t = t0 + tl;
     if (t >= a.N) continue;
-    int64_t s = -1;
-    if (label_valid(y[j], a.ignore_index, a.V) && r.s0 <= r.s1) s = token_sequence(a.cu, r, t);
-    Loss::grad(a, raw[j], scale, t, s);
+    const bool valid = rank >= 0 && label_valid(in.y[0], a.ignore_index, a.V);
+    Loss::grad(a, in.raw[0], scale, t, valid ? r.s0 + rank : -1);
   }
 }
 
 template <class Loss>
 __global__ void __launch_bounds__(64 * kLossWaves) loss_parts_kernel(LossArgs<Loss> a) {
-  __shared__ typename Loss::Share sh[kLossWaves][kLossTile];
-  const int w = threadIdx.x >> 6;
-  const int64_t tile = (int64_t)blockIdx.x * kLossWaves + w;
-  if (tile < a.tiles) tile_parts(a, tile, sh[w]);
+  if (blockIdx.x == 0 && threadIdx.x == 0) a.header[2] = 0;  // for the next kernel's count
+  const int64_t tile = (int64_t)blockIdx.x * kLossWaves + (threadIdx.x >> 6);
+  if (tile < a.tiles) tile_parts(a, tile);
 }
 
+// A block takes `per` items; the block that is done last adds up the blocks'
+// totals, in block order, and finishes the batch.
 template <class Loss>
-__global__ void __launch_bounds__(kSeqThreads) loss_sequences_kernel(LossArgs<Loss> a) {
-  const int64_t i0 = (int64_t)blockIdx.x * kSeqItems;
-  const int64_t i1 = a.items - i0 < kSeqItems ? a.items : i0 + kSeqItems;
-  const typename Loss::Total t = sum_sequences(a, i0, i1);
-  if (gridDim.x == 1)
-    finish_batch(a, t);
-  else if (threadIdx.x == 0)
-    a.totals[blockIdx.x] = t;
-}
-
-// Adds up the blocks of loss_sequences_kernel when there are several.
-template <class Loss>
-__global__ void __launch_bounds__(256) loss_finish_kernel(LossArgs<Loss> a, int blocks) {
-  __shared__ typename Loss::Total sh[16];
-  typename Loss::Total t;
-  t.clear();
-  for (int b = threadIdx.x; b < blocks; b += 256) t.add(a.totals[b]);
-  t = block_total(t, sh);
+__global__ void __launch_bounds__(kSeqThreads) loss_sequences_kernel(LossArgs<Loss> a,
+                                                                     int64_t per) {
+  using Total = typename Loss::Total;
+  __shared__ Total sh[kSeqThreads / 64];
+  __shared__ int last;
+  const int64_t i0 = (int64_t)blockIdx.x * per;
+  const int64_t i1 = a.items - i0 < per ? a.items : i0 + per;
+  Total t = sum_sequences(a, i0, i1);
+  if (gridDim.x > 1) {
+    if (threadIdx.x == 0) {
+      a.totals[blockIdx.x] = t;
+      __threadfence();
+      const int done = __hip_atomic_fetch_add(&a.header[2], 1, __ATOMIC_ACQ_REL,
+                                              __HIP_MEMORY_SCOPE_AGENT);
+      last = done == (int)gridDim.x - 1 ? 1 : 0;
+    }
+    __syncthreads();
+    if (last == 0) return;
+    __threadfence();
+    t.clear();
+    for (int b = threadIdx.x; b < (int)gridDim.x; b += blockDim.x) t.add(a.totals[b]);
+    t = block_total(t, (int)(blockDim.x >> 6), sh);
+  }
   finish_batch(a, t);
 }
 
@@ -617,19 +757,27 @@ __global__ void __launch_bounds__(64 * kLossWaves) loss_grads_kernel(LossArgs<Lo
   if (tile < a.tiles) tile_grads(a, tile);
 }
 
-// All three steps in one block, for small batches: the steps exchange their
-// sums through the workspace as the separate kernels do, ordered by barriers.
+// All three steps in one block, for small batches; the steps exchange their sums
+// through LDS.
 template <class Loss, bool GRADS>
 __global__ void __launch_bounds__(64 * kSmallWaves) loss_small_kernel(LossArgs<Loss> a) {
-  __shared__ typename Loss::Share sh[kSmallWaves][kLossTile];
+  __shared__ typename Loss::Share parts[kSmallSequences + kSmallTiles];
+  __shared__ typename Loss::Share seq_sum[kSmallSequences];
+  __shared__ double state[2 * kSmallSequences + 2];
+  double* const out_state = a.state;  // the caller's, or null
+  a.parts = parts;
+  a.seq_sum = seq_sum;
+  a.state = state;
   const int w = threadIdx.x >> 6;
-  for (int64_t tile = w; tile < a.tiles; tile += kSmallWaves) tile_parts(a, tile, sh[w]);
+  for (int64_t tile = w; tile < a.tiles; tile += kSmallWaves) tile_parts(a, tile);
   __syncthreads();
   finish_batch(a, sum_sequences(a, 0, a.items));
-  if constexpr (GRADS) {
-    __syncthreads();
+  __syncthreads();
+  if (out_state != nullptr)
+    for (int i = threadIdx.x; i < Loss::state_size((int)a.B); i += blockDim.x)
+      out_state[i] = state[i];
+  if constexpr (GRADS)
     for (int64_t tile = w; tile < a.tiles; tile += kSmallWaves) tile_grads(a, tile);
-  }
 }
 
 }  // namespace flce

@@ -17,6 +17,7 @@ namespace {
 
 using namespace flce;
 
+static_assert(kSmallTiles * 64 >= kSmallTokens, "a small batch's tiles have 64 tokens or more");
 static_assert(sizeof(PolicyLoss::Share) == sum_bytes(4) && sizeof(PolicyLoss::Total) == sum_bytes(5) &&
                   sizeof(PreferenceLoss::Share) == sum_bytes(1) &&
                   sizeof(PreferenceLoss::Total) == sum_bytes(1),
@@ -34,16 +35,16 @@ flce_status_t run_grads(const LossArgs<Loss>& a, hipStream_t st) {
 }
 
 // Forward (parts, sequences) and, with `grads`, the gradients. The workspace
-// regions of `a` are set here; a.state too unless it is the caller's.
+// regions of `a` are set here; a.state is the caller's, or null.
 template <class Loss>
 flce_status_t run_loss(LossArgs<Loss>& a, const LossPlan& p, bool grads, void* workspace,
                        hipStream_t st) {
   a.tiles = p.tiles;
+  a.rows = p.rows;
   a.parts = reinterpret_cast<typename Loss::Share*>(wsp(workspace, p.parts));
   a.seq_sum = reinterpret_cast<typename Loss::Share*>(wsp(workspace, p.seq_sum));
   a.totals = reinterpret_cast<typename Loss::Total*>(wsp(workspace, p.totals));
   a.header = reinterpret_cast<int32_t*>(workspace);
-  if (a.state == nullptr) a.state = reinterpret_cast<double*>(wsp(workspace, p.state));
   if (p.small) {
     return launch(K_LOSS_SMALL, st, [&] {
       if (grads)
@@ -52,19 +53,15 @@ flce_status_t run_loss(LossArgs<Loss>& a, const LossPlan& p, bool grads, void* w
         loss_small_kernel<Loss, false><<<1, 64 * kSmallWaves, 0, st>>>(a);
     });
   }
-  if (a.tiles > 0) {
-    const int grid = (int)ceil_div(a.tiles, kLossWaves);
-    FLCE_TRY(launch(K_LOSS_PARTS, st, [&] {
-      loss_parts_kernel<Loss><<<grid, 64 * kLossWaves, 0, st>>>(a);
-    }));
-  }
-  FLCE_TRY(launch(K_LOSS_SEQUENCES, st, [&] {
-    loss_sequences_kernel<Loss><<<p.seq_blocks, kSeqThreads, 0, st>>>(a);
+  if (a.state == nullptr) a.state = reinterpret_cast<double*>(wsp(workspace, p.state));
+  // At least one block, which readies the header for the next kernel.
+  const int grid = (int)ceil_div(a.tiles > 0 ? a.tiles : 1, kLossWaves);
+  FLCE_TRY(launch(K_LOSS_PARTS, st, [&] {
+    loss_parts_kernel<Loss><<<grid, 64 * kLossWaves, 0, st>>>(a);
   }));
-  if (p.seq_blocks > 1)
-    FLCE_TRY(launch(K_LOSS_SEQUENCES, st, [&] {
-      loss_finish_kernel<Loss><<<1, 256, 0, st>>>(a, p.seq_blocks);
-    }));
+  FLCE_TRY(launch(K_LOSS_SEQUENCES, st, [&] {
+    loss_sequences_kernel<Loss><<<p.seq_blocks, kSeqThreads, 0, st>>>(a, p.seq_items);
+  }));
   return grads ? run_grads(a, st) : FLCE_OK;
 }
 
@@ -99,7 +96,6 @@ LossArgs<PolicyLoss> policy_args(const float* logprob, const float* entropy,
   a.V = V;
   a.ignore_index = o.ignore_index;
   a.items = B;
-  a.tiles = ceil_div(N, kLossTile);
   return a;
 }
 
@@ -124,7 +120,7 @@ flce_status_t policy_impl(const float* logprob, const float* entropy, const floa
                           const float* ref_logprob, const float* advantages,
                           const int64_t* labels, const int64_t* cu, int64_t N, int64_t B,
                           int64_t V, const flce_policy_options_t* opt, const float* grad_loss,
-                          float* stats, double* state, bool grads, float* grad_logprob,
+                          float* loss, float* stats, double* state, bool grads, float* grad_logprob,
                           float* grad_entropy, void* workspace, size_t workspace_bytes,
                           void* stream) {
   FLCE_TRY(check_policy(N, B, V, cu != nullptr, opt));
@@ -132,7 +128,7 @@ flce_status_t policy_impl(const float* logprob, const float* entropy, const floa
   if (stats == nullptr || workspace == nullptr) return FLCE_ERR_NULL_POINTER;
   if (opt->entropy_coef != 0.0 && N > 0 && entropy == nullptr) return FLCE_ERR_NULL_POINTER;
   if (grads && N > 0 && grad_logprob == nullptr) return FLCE_ERR_NULL_POINTER;
-  if (!aligned_to(entropy, 4) || !aligned_to(stats, 4) || !aligned_to(state, 8) ||
+  if (!aligned_to(entropy, 4) || !aligned_to(loss, 4) || !aligned_to(stats, 4) || !aligned_to(state, 8) ||
       !aligned_to(grad_loss, 4) || !aligned_to(grad_logprob, 4) || !aligned_to(grad_entropy, 4) ||
       !aligned16(workspace))
     return FLCE_ERR_MISALIGNED;
@@ -140,6 +136,7 @@ flce_status_t policy_impl(const float* logprob, const float* entropy, const floa
   if (workspace_bytes < p.total) return FLCE_ERR_WORKSPACE_TOO_SMALL;
   LossArgs<PolicyLoss> a = policy_args(logprob, entropy, old_logprob, ref_logprob, advantages,
                                        labels, cu, N, B, V, *opt);
+  a.out.loss = loss;
   a.out.stats = stats;
   a.out.grad_loss = grad_loss;
   a.out.grad_logprob = grad_logprob;
@@ -169,7 +166,6 @@ LossArgs<PreferenceLoss> preference_args(const float* logprob, const float* ref_
   a.V = V;
   a.ignore_index = o.ignore_index;
   a.items = P;
-  a.tiles = ceil_div(N, kLossTile);
   return a;
 }
 
@@ -424,12 +420,12 @@ flce_status_t flce_policy_loss_forward(const float* logprob, const float* entrop
                                        const float* old_logprob, const float* ref_logprob,
                                        const float* advantages, const int64_t* labels,
                                        const int64_t* cu_seqlens, int64_t N, int64_t B, int64_t V,
-                                       const flce_policy_options_t* opt, float* stats,
+                                       const flce_policy_options_t* opt, float* loss, float* stats,
                                        double* seq_state, void* workspace, size_t workspace_bytes,
                                        void* stream) {
   if (seq_state == nullptr) return FLCE_ERR_NULL_POINTER;
   return policy_impl(logprob, entropy, old_logprob, ref_logprob, advantages, labels, cu_seqlens,
-                     N, B, V, opt, nullptr, stats, seq_state, false, nullptr, nullptr, workspace,
+                     N, B, V, opt, nullptr, loss, stats, seq_state, false, nullptr, nullptr, workspace,
                      workspace_bytes, stream);
 }
 
@@ -449,6 +445,9 @@ flce_status_t flce_policy_loss_backward(const float* logprob, const float* old_l
     return FLCE_ERR_MISALIGNED;
   LossArgs<PolicyLoss> a = policy_args(logprob, nullptr, old_logprob, ref_logprob, advantages,
                                        labels, cu_seqlens, N, B, V, *opt);
+  const LossPlan p = policy_plan(N, B);
+  a.tiles = p.tiles;
+  a.rows = p.rows;
   a.state = const_cast<double*>(seq_state);  // read only by the gradients kernel
   a.out.grad_loss = grad_loss;
   a.out.grad_logprob = grad_logprob;
@@ -459,11 +458,11 @@ flce_status_t flce_policy_loss_backward(const float* logprob, const float* old_l
 flce_status_t flce_policy_loss_forward_backward(
     const float* logprob, const float* entropy, const float* old_logprob, const float* ref_logprob,
     const float* advantages, const int64_t* labels, const int64_t* cu_seqlens, int64_t N, int64_t B,
-    int64_t V, const flce_policy_options_t* opt, const float* grad_loss, float* stats,
+    int64_t V, const flce_policy_options_t* opt, const float* grad_loss, float* loss, float* stats,
     float* grad_logprob, float* grad_entropy, void* workspace, size_t workspace_bytes,
     void* stream) {
   return policy_impl(logprob, entropy, old_logprob, ref_logprob, advantages, labels, cu_seqlens,
-                     N, B, V, opt, grad_loss, stats, nullptr, true, grad_logprob, grad_entropy,
+                     N, B, V, opt, grad_loss, loss, stats, nullptr, true, grad_logprob, grad_entropy,
                      workspace, workspace_bytes, stream);
 }
 
@@ -501,6 +500,9 @@ flce_status_t flce_preference_loss_backward(const int64_t* labels, const int64_t
     return FLCE_ERR_MISALIGNED;
   LossArgs<PreferenceLoss> a =
       preference_args(nullptr, nullptr, labels, cu_seqlens, N, P, V, *opt);
+  const LossPlan p = preference_plan(N, P);
+  a.tiles = p.tiles;
+  a.rows = p.rows;
   a.state = const_cast<double*>(seq_state);  // read only by the gradients kernel
   a.out.grad_loss = grad_loss;
   a.out.grad_logprob = grad_logprob;

@@ -10,35 +10,68 @@
 #include "flce.h"
 #include "flce_plan.hpp"
 
+// Also called in kernels.
+#ifdef __HIPCC__
+#define FLCE_HD __host__ __device__
+#else
+#define FLCE_HD
+#endif
+
 namespace flce {
 
 // ---- losses ----------------------------------------------------------------------
 
-constexpr int kLossTile = 256;        // tokens a wave takes
+constexpr int kLossTile = 256;        // tokens a wave takes at most
+constexpr int kLossRows = kLossTile / 64;
 constexpr int kLossWaves = 4;         // waves a block, parts and gradients kernels
 constexpr int kSmallWaves = 8;        // waves of the one-block kernel
 constexpr int kSeqThreads = 1024;     // threads a block, sequences kernel
-constexpr int64_t kSeqItems = 4096;   // sequences (or pairs) a block of it
+constexpr int64_t kMaxSeqBlocks = 512;
 // Batches up to these sizes take the one-block kernel.
 constexpr int64_t kSmallTokens = 8192;
-constexpr int64_t kSmallItems = 1024;
+constexpr int64_t kSmallSequences = 1024;
+constexpr int64_t kSmallTiles = 128;
 constexpr int64_t kMaxSequences = (int64_t)1 << 21;
 
 // Workspace: header, shares [B + tiles], sequence sums [B], block totals, and
 // the state of the calls that return gradients at once.
 struct LossPlan {
+  int rows;             // rows of 64 tokens a tile
   int64_t tiles;
+  int64_t seq_items;    // items a block of the sequences kernel takes
   int seq_blocks;
   bool small;
   size_t parts, seq_sum, totals, state, total;
 };
 
+// Lanes that add up one sequence's shares: its average number of shares, as a
+// power of two up to a wave.
+FLCE_HD inline int lanes_per_sequence(int64_t B, int64_t tiles) {
+  int g = 1;
+  while (g < 64 && g * B < tiles) g <<= 1;
+  return g;
+}
+
+// Rows a tile: a wave takes its rows one after another, so few as long as the
+// waves do not fill what runs them (the block; the GPU's 1024 SIMDs), then more,
+// for fewer shares.
+inline int loss_rows(int64_t N, bool small) {
+  const int64_t waves = small ? kSmallWaves : 1024;
+  int rows = 1;
+  while (rows < kLossRows && ceil_div(N, 64 * rows) > waves) rows *= 2;
+  return rows;
+}
+
 inline LossPlan make_loss_plan(int64_t N, int64_t B, int64_t items, size_t share_bytes,
                                size_t total_bytes, int64_t state_doubles) {
   LossPlan p{};
-  p.tiles = ceil_div(N, kLossTile);
-  p.seq_blocks = (int)ceil_div(items > 0 ? items : 1, kSeqItems);
-  p.small = N <= kSmallTokens && items <= kSmallItems;
+  p.small = N <= kSmallTokens && B <= kSmallSequences;
+  p.rows = loss_rows(N, p.small);
+  p.tiles = ceil_div(N, 64 * p.rows);
+  // One round of a block's lane groups, or more when that makes too many blocks.
+  const int64_t round = kSeqThreads / lanes_per_sequence(B, p.tiles) / (B / items);
+  p.seq_items = round * ceil_div(ceil_div(items, round), kMaxSeqBlocks);
+  p.seq_blocks = (int)ceil_div(items, p.seq_items);
   size_t off = kHeaderBytes;
   auto take = [&](size_t& field, size_t bytes) {
     field = off;

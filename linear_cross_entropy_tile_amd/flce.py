@@ -22,6 +22,7 @@ missing or the device is not a GPU, calls raise.
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 
 __all__ = [
@@ -151,13 +152,13 @@ _SIG = {
                                                ctypes.c_size_t, _P]),
     "flce_policy_workspace_size": (ctypes.c_int, [_I64, _I64, ctypes.POINTER(ctypes.c_size_t)]),
     "flce_policy_loss_forward": (ctypes.c_int, [_P] * 7 + [_I64] * 3
-                                 + [ctypes.POINTER(FlcePolicyOptions), _P, _P, _P, ctypes.c_size_t,
-                                    _P]),
+                                 + [ctypes.POINTER(FlcePolicyOptions), _P, _P, _P, _P,
+                                    ctypes.c_size_t, _P]),
     "flce_policy_loss_backward": (ctypes.c_int, [_P] * 6 + [_I64] * 3
                                   + [ctypes.POINTER(FlcePolicyOptions), _P, _P, _P, _P, _P]),
     "flce_policy_loss_forward_backward": (ctypes.c_int, [_P] * 7 + [_I64] * 3
                                           + [ctypes.POINTER(FlcePolicyOptions), _P, _P, _P, _P, _P,
-                                             ctypes.c_size_t, _P]),
+                                             _P, ctypes.c_size_t, _P]),
     "flce_preference_workspace_size": (ctypes.c_int, [_I64, _I64,
                                                       ctypes.POINTER(ctypes.c_size_t)]),
     "flce_preference_loss_forward": (ctypes.c_int, [_P] * 4 + [_I64] * 3
@@ -344,10 +345,10 @@ def flce_policy_workspace_size(N: int, B: int) -> int:
 
 
 def flce_policy_loss_forward(logprob, entropy, old_logprob, ref_logprob, advantages, labels,
-                             cu_seqlens, N, B, V, opt, stats, seq_state, workspace,
+                             cu_seqlens, N, B, V, opt, loss, stats, seq_state, workspace,
                              workspace_bytes, stream):
     _check(lib().flce_policy_loss_forward(logprob, entropy, old_logprob, ref_logprob, advantages,
-                                          labels, cu_seqlens, N, B, V, ctypes.byref(opt), stats,
+                                          labels, cu_seqlens, N, B, V, ctypes.byref(opt), loss, stats,
                                           seq_state, workspace, workspace_bytes, stream),
            "flce_policy_loss_forward")
 
@@ -362,12 +363,12 @@ def flce_policy_loss_backward(logprob, old_logprob, ref_logprob, advantages, lab
 
 
 def flce_policy_loss_forward_backward(logprob, entropy, old_logprob, ref_logprob, advantages,
-                                      labels, cu_seqlens, N, B, V, opt, grad_loss, stats,
-                                      grad_logprob, grad_entropy, workspace, workspace_bytes,
-                                      stream):
+                                      labels, cu_seqlens, N, B, V, opt, grad_loss, loss,
+                                      stats, grad_logprob, grad_entropy, workspace,
+                                      workspace_bytes, stream):
     _check(lib().flce_policy_loss_forward_backward(logprob, entropy, old_logprob, ref_logprob,
                                                    advantages, labels, cu_seqlens, N, B, V,
-                                                   ctypes.byref(opt), grad_loss, stats,
+                                                   ctypes.byref(opt), grad_loss, loss, stats,
                                                    grad_logprob, grad_entropy, workspace,
                                                    workspace_bytes, stream),
            "flce_policy_loss_forward_backward")
@@ -712,20 +713,31 @@ def forward_backward(hidden, weight, labels, grad_logprob=None, grad_entropy=Non
 
 # ---- beside the head: embedding, policy loss, preference loss
 
-def _call(dev, fn, *args) -> None:
-    """fn(*args, stream) on torch's current stream of ``dev``, with it current."""
-    cuda = _torch().cuda
-    if cuda.current_device() == dev.index:
-        fn(*args, cuda.current_stream().cuda_stream)
-        return
-    with cuda.device(dev):
-        fn(*args, cuda.current_stream().cuda_stream)
+def _call(dev, name, *args) -> None:
+    """The C entry point ``name``(*args, stream) on torch's current stream of
+    ``dev``, with that device current (ctypes passes an options structure by
+    reference)."""
+    torch = _torch()
+    stream = torch._C._cuda_getCurrentRawStream(dev.index)
+    f = getattr(_LIB or lib(), name)
+    if torch.cuda.current_device() == dev.index:
+        status = f(*args, stream)
+    else:
+        with torch.cuda.device(dev):
+            status = f(*args, stream)
+    if status != 0:
+        raise FlceError(status, name)
 
 
 def _check_devices(dev, *named) -> None:
     for name, t in named:
         if t is not None and t.device != dev:
             raise ValueError(f"{name} must be on {dev}, got {t.device}")
+
+
+# Sizes depend on nothing but their arguments.
+_policy_bytes = functools.lru_cache(maxsize=256)(flce_policy_workspace_size)
+_preference_bytes = functools.lru_cache(maxsize=256)(flce_preference_workspace_size)
 
 
 def _choice(table, value, name):
@@ -776,7 +788,7 @@ def embedding(weight, tokens, layout: str = "hv", scale: float = 1.0, ignore_ind
     nbytes, _ = flce_embedding_workspace_size(N, H, V, opt)
     workspace = _workspace(workspace, nbytes, dev)
     hidden = torch.empty((N, H), dtype=torch.bfloat16, device=dev)
-    _call(dev, flce_embedding_forward, weight.data_ptr(), tokens.data_ptr(), N, H, V,
+    _call(dev, "flce_embedding_forward", weight.data_ptr(), tokens.data_ptr(), N, H, V,
           int(v_begin), V if v_total is None else int(v_total), opt, hidden.data_ptr(),
           workspace.data_ptr(), workspace.numel())
     return {"hidden": hidden, "workspace": workspace}
@@ -817,7 +829,7 @@ def embedding_backward(grad_hidden, tokens, vocab_size: int, layout: str = "hv",
     if not accumulate:
         grad_weight = torch.empty(shape, device=dev, dtype=torch.float32 if gdt == FLCE_GRAD_F32
                                   else torch.bfloat16)
-    _call(dev, flce_embedding_backward, grad_hidden.data_ptr(), tokens.data_ptr(), N, H, V,
+    _call(dev, "flce_embedding_backward", grad_hidden.data_ptr(), tokens.data_ptr(), N, H, V,
           int(v_begin), V if v_total is None else int(v_total), opt, grad_weight.data_ptr(),
           workspace.data_ptr(), workspace.numel())
     return grad_weight
@@ -826,17 +838,18 @@ def embedding_backward(grad_hidden, tokens, vocab_size: int, layout: str = "hv",
 def _token_arrays(labels, cu_seqlens, arrays):
     """Checks int64 [N] labels, int64 cu_seqlens (or None) and the fp32 arrays
     ((name, tensor, size); None tensors skipped); returns the device."""
-    torch = _torch()
+    f32 = _torch().float32
     dev = labels.device
     if cu_seqlens is not None:
         _check_devices(dev, ("cu_seqlens", cu_seqlens))
     for name, t, size in arrays:
         if t is None:
             continue
-        _require(t, torch.float32, 1, name)
-        if t.shape[0] != size:
+        _require(t, f32, 1, name)
+        if t.numel() != size:
             raise ValueError(f"{name} must have {size} element(s)")
-        _check_devices(dev, (name, t))
+        if t.device != dev:
+            raise ValueError(f"{name} must be on {dev}, got {t.device}")
     return dev
 
 
@@ -912,14 +925,15 @@ def policy_loss(logprob, labels, old_logprob, advantages, entropy=None, ref_logp
                               cu_seqlens, None)
     if opt.entropy_coef != 0.0 and entropy is None:
         raise ValueError("entropy_coef needs entropy")
-    workspace = _workspace(workspace, flce_policy_workspace_size(N, B), dev)
+    workspace = _workspace(workspace, _policy_bytes(N, B), dev)
+    loss = torch.empty(1, dtype=torch.float32, device=dev)
     stats = torch.empty(8, dtype=torch.float32, device=dev)
     state = torch.empty((B + 1, 2), dtype=torch.float64, device=dev)
-    _call(dev, flce_policy_loss_forward, logprob.data_ptr(), _ptr(entropy),
+    _call(dev, "flce_policy_loss_forward", logprob.data_ptr(), _ptr(entropy),
           old_logprob.data_ptr(), _ptr(ref_logprob), advantages.data_ptr(), labels.data_ptr(),
-          _ptr(cu_seqlens), N, B, V, opt, stats.data_ptr(), state.data_ptr(),
+          _ptr(cu_seqlens), N, B, V, opt, loss.data_ptr(), stats.data_ptr(), state.data_ptr(),
           workspace.data_ptr(), workspace.numel())
-    return {"loss": stats[0:1], "stats": stats, "seq_state": state, "workspace": workspace}
+    return {"loss": loss, "stats": stats, "seq_state": state, "workspace": workspace}
 
 
 def policy_loss_backward(logprob, labels, old_logprob, advantages, seq_state, grad_loss=None,
@@ -938,7 +952,7 @@ def policy_loss_backward(logprob, labels, old_logprob, advantages, seq_state, gr
     _check_devices(dev, ("seq_state", seq_state))
     glp = torch.empty(N, dtype=torch.float32, device=dev)
     gent = torch.empty(N, dtype=torch.float32, device=dev) if want_entropy else None
-    _call(dev, flce_policy_loss_backward, logprob.data_ptr(), old_logprob.data_ptr(),
+    _call(dev, "flce_policy_loss_backward", logprob.data_ptr(), old_logprob.data_ptr(),
           _ptr(ref_logprob), advantages.data_ptr(), labels.data_ptr(), _ptr(cu_seqlens), N, B, V,
           opt, seq_state.data_ptr(), _ptr(grad_loss), glp.data_ptr(), _ptr(gent))
     return glp, gent
@@ -958,17 +972,18 @@ def policy_loss_forward_backward(logprob, labels, old_logprob, advantages, grad_
                               cu_seqlens, grad_loss)
     if opt.entropy_coef != 0.0 and entropy is None:
         raise ValueError("entropy_coef needs entropy")
-    workspace = _workspace(workspace, flce_policy_workspace_size(N, B), dev)
+    workspace = _workspace(workspace, _policy_bytes(N, B), dev)
+    loss = torch.empty(1, dtype=torch.float32, device=dev)
     stats = torch.empty(8, dtype=torch.float32, device=dev)
     glp = torch.empty(N, dtype=torch.float32, device=dev)
-    out = {"loss": stats[0:1], "stats": stats, "workspace": workspace, "grad_logprob": glp}
+    out = {"loss": loss, "stats": stats, "workspace": workspace, "grad_logprob": glp}
     gent = None
     if entropy is not None:
         gent = out["grad_entropy"] = torch.empty(N, dtype=torch.float32, device=dev)
-    _call(dev, flce_policy_loss_forward_backward, logprob.data_ptr(), _ptr(entropy),
+    _call(dev, "flce_policy_loss_forward_backward", logprob.data_ptr(), _ptr(entropy),
           old_logprob.data_ptr(), _ptr(ref_logprob), advantages.data_ptr(), labels.data_ptr(),
-          _ptr(cu_seqlens), N, B, V, opt, _ptr(grad_loss), stats.data_ptr(), glp.data_ptr(),
-          _ptr(gent), workspace.data_ptr(), workspace.numel())
+          _ptr(cu_seqlens), N, B, V, opt, _ptr(grad_loss), loss.data_ptr(), stats.data_ptr(),
+          glp.data_ptr(), _ptr(gent), workspace.data_ptr(), workspace.numel())
     return out
 
 
@@ -1001,7 +1016,7 @@ def _preference_check(opt, labels, cu_seqlens, grad_loss, arrays):
 def _pair_outputs(P, dev, reduction):
     """The outputs of a preference call: (loss pointer, dict)."""
     torch = _torch()
-    pair, chosen, rejected = torch.empty((3, P), dtype=torch.float32, device=dev).unbind(0)
+    pair, chosen, rejected = (torch.empty(P, dtype=torch.float32, device=dev) for _ in range(3))
     loss = (None if reduction == FLCE_REDUCTION_NONE
             else torch.empty(1, dtype=torch.float32, device=dev))
     return _ptr(loss), {"loss": pair if loss is None else loss, "pair_loss": pair,
@@ -1031,10 +1046,10 @@ def preference_loss(logprob, labels, cu_seqlens, ref_logprob=None, workspace=Non
     _require(logprob, torch.float32, 1, "logprob")
     dev, N, P = _preference_check(opt, labels, cu_seqlens, None,
                                   (("logprob", logprob), ("ref_logprob", ref_logprob)))
-    workspace = _workspace(workspace, flce_preference_workspace_size(N, P), dev)
+    workspace = _workspace(workspace, _preference_bytes(N, P), dev)
     loss, out = _pair_outputs(P, dev, opt.reduction)
     state = torch.empty(2 * P + 1, dtype=torch.float64, device=dev)
-    _call(dev, flce_preference_loss_forward, logprob.data_ptr(), _ptr(ref_logprob),
+    _call(dev, "flce_preference_loss_forward", logprob.data_ptr(), _ptr(ref_logprob),
           labels.data_ptr(), cu_seqlens.data_ptr(), N, P, V, opt, loss,
           out["pair_loss"].data_ptr(), out["chosen_reward"].data_ptr(),
           out["rejected_reward"].data_ptr(), state.data_ptr(), workspace.data_ptr(),
@@ -1055,7 +1070,7 @@ def preference_loss_backward(labels, cu_seqlens, seq_state, grad_loss=None, **op
         raise ValueError(f"seq_state must have {2 * P + 1} elements")
     _check_devices(dev, ("seq_state", seq_state))
     glp = torch.empty(N, dtype=torch.float32, device=dev)
-    _call(dev, flce_preference_loss_backward, labels.data_ptr(), cu_seqlens.data_ptr(), N, P, V,
+    _call(dev, "flce_preference_loss_backward", labels.data_ptr(), cu_seqlens.data_ptr(), N, P, V,
           opt, seq_state.data_ptr(), _ptr(grad_loss), glp.data_ptr())
     return glp
 
@@ -1071,10 +1086,10 @@ def preference_loss_forward_backward(logprob, labels, cu_seqlens, grad_loss=None
     _require(logprob, torch.float32, 1, "logprob")
     dev, N, P = _preference_check(opt, labels, cu_seqlens, grad_loss,
                                   (("logprob", logprob), ("ref_logprob", ref_logprob)))
-    workspace = _workspace(workspace, flce_preference_workspace_size(N, P), dev)
+    workspace = _workspace(workspace, _preference_bytes(N, P), dev)
     loss, out = _pair_outputs(P, dev, opt.reduction)
     glp = torch.empty(N, dtype=torch.float32, device=dev)
-    _call(dev, flce_preference_loss_forward_backward, logprob.data_ptr(), _ptr(ref_logprob),
+    _call(dev, "flce_preference_loss_forward_backward", logprob.data_ptr(), _ptr(ref_logprob),
           labels.data_ptr(), cu_seqlens.data_ptr(), N, P, V, opt, _ptr(grad_loss), loss,
           out["pair_loss"].data_ptr(), out["chosen_reward"].data_ptr(),
           out["rejected_reward"].data_ptr(), glp.data_ptr(), workspace.data_ptr(),

@@ -119,16 +119,19 @@ class PolicyLoss(torch.autograd.Function):
                               out["seq_state"])
         ctx.options = options
         ctx.mark_non_differentiable(out["stats"])
-        return out["loss"].reshape(()).clone(), out["stats"]
+        ctx.set_materialize_grads(False)
+        return out["loss"].reshape(()), out["stats"]
 
     @staticmethod
     @once_differentiable
     def backward(ctx, grad_loss, _grad_stats):
+        if grad_loss is None:
+            return (None,) * 8
         logprob, labels, old_logprob, advantages, ref_logprob, cu_seqlens, state = \
             ctx.saved_tensors
         glp, gent = flce.policy_loss_backward(
             logprob, labels, old_logprob, advantages, state,
-            grad_loss=grad_loss.float().reshape(1).contiguous(), ref_logprob=ref_logprob,
+            grad_loss=grad_loss.reshape(1), ref_logprob=ref_logprob,
             cu_seqlens=cu_seqlens, want_entropy=ctx.needs_input_grad[1], **ctx.options)
         return glp, gent, None, None, None, None, None, None
 
@@ -154,7 +157,8 @@ class PreferenceLoss(torch.autograd.Function):
         ctx.save_for_backward(labels, cu_seqlens, out["seq_state"])
         ctx.options = options
         ctx.mark_non_differentiable(out["chosen_reward"], out["rejected_reward"])
-        loss = out["loss"].clone()
+        ctx.set_materialize_grads(False)
+        loss = out["loss"]
         if options.get("reduction", "mean") != "none":
             loss = loss.reshape(())
         return loss, out["chosen_reward"], out["rejected_reward"]
@@ -162,10 +166,11 @@ class PreferenceLoss(torch.autograd.Function):
     @staticmethod
     @once_differentiable
     def backward(ctx, grad_loss, _grad_chosen, _grad_rejected):
+        if grad_loss is None:
+            return (None,) * 5
         labels, cu_seqlens, state = ctx.saved_tensors
         glp = flce.preference_loss_backward(
-            labels, cu_seqlens, state, grad_loss=grad_loss.float().reshape(-1).contiguous(),
-            **ctx.options)
+            labels, cu_seqlens, state, grad_loss=grad_loss.reshape(-1).contiguous(), **ctx.options)
         return glp, None, None, None, None
 
 

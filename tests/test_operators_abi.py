@@ -45,7 +45,7 @@ def _policy_opt(**kw):
 
 
 def _policy(which, **kw):
-    a = dict(lp=A, e=A, old=A, ref=A, adv=A, lab=A, cu=A, N=4, B=2, V=10, g=None, stats=A,
+    a = dict(lp=A, e=A, old=A, ref=A, adv=A, lab=A, cu=A, N=4, B=2, V=10, g=None, loss=None, stats=A,
              state=A, glp=A, gent=A, ws=A, wsb=BIG)
     o = {k: kw.pop(k) for k in list(kw) if k not in a}
     a.update(kw)
@@ -53,15 +53,15 @@ def _policy(which, **kw):
     L = flce.lib()
     if which == "forward":
         return L.flce_policy_loss_forward(a["lp"], a["e"], a["old"], a["ref"], a["adv"], a["lab"],
-                                          a["cu"], a["N"], a["B"], a["V"], opt, a["stats"],
-                                          a["state"], a["ws"], a["wsb"], None)
+                                          a["cu"], a["N"], a["B"], a["V"], opt, a["loss"],
+                                          a["stats"], a["state"], a["ws"], a["wsb"], None)
     if which == "backward":
         return L.flce_policy_loss_backward(a["lp"], a["old"], a["ref"], a["adv"], a["lab"],
                                            a["cu"], a["N"], a["B"], a["V"], opt, a["state"],
                                            a["g"], a["glp"], a["gent"], None)
     return L.flce_policy_loss_forward_backward(a["lp"], a["e"], a["old"], a["ref"], a["adv"],
                                                a["lab"], a["cu"], a["N"], a["B"], a["V"], opt,
-                                               a["g"], a["stats"], a["glp"], a["gent"], a["ws"],
+                                               a["g"], a["loss"], a["stats"], a["glp"], a["gent"], a["ws"],
                                                a["wsb"], None)
 
 
@@ -89,6 +89,7 @@ def test_policy_rejects(which, kw, code):
     ("forward", dict(stats=None), 1), ("forward", dict(state=None), 1),
     ("forward", dict(ws=None), 1), ("forward", dict(ent=0.1, e=None), 1),
     ("forward", dict(wsb=300), 5), ("forward", dict(state=A + 4), 4), ("forward", dict(ws=A + 8), 4),
+    ("forward", dict(loss=A + 2), 4),
     ("backward", dict(state=None), 1), ("backward", dict(glp=None), 1),
     ("backward", dict(gent=A + 2), 4),
     ("both", dict(glp=None), 1), ("both", dict(stats=None), 1), ("both", dict(wsb=300), 5),
