@@ -443,8 +443,8 @@ flce_status_t flce_embedding_backward(const void* grad_hidden, const int64_t* to
  * A sequence whose offsets decrease or leave [0, N] makes the reduced loss, the
  * statistics and every valid token's gradient NaN, and (preference) its pair's
  * outputs; the results of the other sequences are then unspecified. The status
- * word counts such sequences and the labels of sequences that are neither
- * ignore_index nor in [0, V). */
+ * word counts such sequences or, when there are none, the labels of sequences
+ * that are neither ignore_index nor in [0, V). */
 enum { FLCE_REDUCTION_SEQUENCE_MEAN = 3 };  /* flce_policy_loss_* only */
 enum { FLCE_KL_K1 = 0, FLCE_KL_K2 = 1, FLCE_KL_K3 = 2 };
 enum { FLCE_RATIO_TOKEN = 0, FLCE_RATIO_SEQUENCE = 1 };

@@ -59,19 +59,26 @@ struct TileSeqs {
   int64_t s0, ns;
   int off;
 };
-__device__ __forceinline__ TileSeqs tile_sequences(const int64_t* cu, int64_t B, int64_t t0,
-                                                   int64_t t1) {
+__device__ __forceinline__ TileSeqs tile_sequences(const int64_t* cu, int64_t B, int64_t N,
+                                                   int64_t t0, int64_t t1) {
   const int lane = threadIdx.x & 63;
   if (cu == nullptr) return {0, 1, lane == 0 ? 0 : kLossTile};
+  // Lengths of one batch are of one order, so the tile's offsets are nearly always
+  // among the 64 around its share of the batch: one load. Otherwise a search.
   const int64_t n = B + 1;
-  int64_t s0, c1, v;
-  if (n <= 64) {  // one load has everything
-    const int64_t x = cu[lane < n ? lane : n - 1];
-    const int c0 = __popcll(__builtin_amdgcn_ballot_w64(lane < n && x <= t0));
-    c1 = __popcll(__builtin_amdgcn_ballot_w64(lane < n && x <= t1 - 1));
-    s0 = c0 > 0 ? c0 - 1 : 0;
-    const int from = s0 + lane < n ? (int)s0 + lane : (int)n - 1;
-    v = (int64_t)__shfl((long long)x, from, 64);
+  const int64_t guess = (int64_t)((float)t0 / (float)N * (float)B) - 31;
+  const int64_t w0 = guess < 0 || n <= 64 ? 0 : (guess < n - 64 ? guess : n - 64);
+  int64_t s0, c1, v = cu[w0 + lane < n ? w0 + lane : n - 1];
+  const uint64_t in = __builtin_amdgcn_ballot_w64(w0 + lane < n);
+  const uint64_t m0 = __builtin_amdgcn_ballot_w64(v <= t0) & in;
+  const uint64_t m1 = __builtin_amdgcn_ballot_w64(v <= t1 - 1) & in;
+  if ((w0 == 0 || (m0 & 1) != 0) && (w0 + 64 >= n || (m1 >> 63) == 0)) {
+    const int c0 = __popcll(m0);
+    c1 = w0 + __popcll(m1);
+    const int from = c0 > 0 ? c0 - 1 : 0;
+    s0 = w0 + from;
+    const int last = n - w0 < 64 ? (int)(n - w0) - 1 : 63;
+    v = (int64_t)__shfl((long long)v, from + lane < last ? from + lane : last, 64);
   } else {
     const int64_t c0 = wave_count_le(cu, n, t0);
     s0 = c0 > 0 ? c0 - 1 : 0;
@@ -132,6 +139,9 @@ __device__ __forceinline__ bool label_valid(int64_t y, int64_t ignore_index, int
 
 __device__ __forceinline__ double shfl_down_f64(double v, int d) { return __shfl_down(v, d, 64); }
 
+// The counts of one tile's tokens in one word (at most kLossTile = 256 each).
+constexpr int kCountValid = 1, kCountClipped = 1 << 10, kCountInvalid = 1 << 20;
+
 // Sums over the wave in lane 63: within rows of 16 lanes by shifts of 1, 2, 4 and
 // 8, then row 0 into 1 and 2 into 3, then 1 into 3.
 template <int CTRL, int ROWS>
@@ -176,26 +186,6 @@ struct LossSum {
     inv += o.inv;
     bad += o.bad;
   }
-  __device__ LossSum up(int d) const {
-    LossSum o;
-#pragma unroll
-    for (int k = 0; k < K; ++k) o.x[k] = __shfl_up(x[k], d, 64);
-    o.n = __shfl_up(n, d, 64);
-    o.c = __shfl_up(c, d, 64);
-    o.inv = __shfl_up(inv, d, 64);
-    o.bad = 0;
-    return o;
-  }
-  __device__ LossSum from(int l) const {
-    LossSum o;
-#pragma unroll
-    for (int k = 0; k < K; ++k) o.x[k] = __shfl(x[k], l, 64);
-    o.n = __shfl(n, l, 64);
-    o.c = __shfl(c, l, 64);
-    o.inv = __shfl(inv, l, 64);
-    o.bad = 0;
-    return o;
-  }
   // Sum over the wave, in lane 63.
   __device__ void wave_sum() {
 #pragma unroll
@@ -216,6 +206,53 @@ struct LossSum {
       inv += __shfl_down(inv, d, 64);
       bad += __shfl_down(bad, d, 64);
     }
+  }
+};
+
+// The terms of a token, or of several of one tile.
+template <int K>
+struct Terms {
+  double x[K];
+  int counts;
+  __device__ __forceinline__ void clear() {
+#pragma unroll
+    for (int k = 0; k < K; ++k) x[k] = 0.0;
+    counts = 0;
+  }
+  __device__ __forceinline__ void add(const Terms& o) {
+#pragma unroll
+    for (int k = 0; k < K; ++k) x[k] += o.x[k];
+    counts += o.counts;
+  }
+  __device__ __forceinline__ Terms up(int d) const {
+    Terms o;
+#pragma unroll
+    for (int k = 0; k < K; ++k) o.x[k] = __shfl_up(x[k], d, 64);
+    o.counts = __shfl_up(counts, d, 64);
+    return o;
+  }
+  __device__ __forceinline__ Terms from(int l) const {
+    Terms o;
+#pragma unroll
+    for (int k = 0; k < K; ++k) o.x[k] = __shfl(x[k], l, 64);
+    o.counts = __shfl(counts, l, 64);
+    return o;
+  }
+  // Sum over the wave, in lane 63.
+  __device__ __forceinline__ void wave_sum() {
+#pragma unroll
+    for (int k = 0; k < K; ++k) x[k] = wave_sum_dpp(x[k]);
+    counts = wave_sum_dpp(counts);
+  }
+  __device__ __forceinline__ LossSum<K> share() const {
+    LossSum<K> s;
+#pragma unroll
+    for (int k = 0; k < K; ++k) s.x[k] = x[k];
+    s.n = counts & 1023;
+    s.c = (counts >> 10) & 1023;
+    s.inv = counts >> 20;
+    s.bad = 0;
+    return s;
   }
 };
 
@@ -247,13 +284,41 @@ struct LossArgs {
   int64_t N, B, V, ignore_index;
   int64_t items;                // sequences, or pairs
   int64_t tiles;
-  int rows;                     // of 64 tokens a tile: 1, 2 or 4
+  int rows;                     // of 64 tokens a tile: 1 or kLossRows
   typename Loss::Share* parts;    // [B + tiles]
   typename Loss::Share* seq_sum;  // [B]
   typename Loss::Total* totals;   // [blocks of the sequences kernel]
   int32_t* header;                // [0] invalid labels and offsets, [2] blocks that are done
   double* state;                  // see Loss
 };
+
+// exp(x) - 1, or exp(x): x = n ln 2 + f with |f| <= ln 2 / 2, Taylor's series of
+// exp(f) - 1 to f^11 (the rest is below 10^-13 of it; the rounding of ln 2 adds
+// at most 10^-16 |x|), and 2^n. Near 0 n is 0 and the difference with 1 is never
+// formed. That is far below the fp32 rounding of every output; the library's
+// functions, exact to the last bit, took 3 us more of the 26 of a parts step over
+// 2^21 tokens.
+template <bool MINUS_1>
+__device__ __forceinline__ double exp_f64(double x) {
+  x = x > 1000.0 ? 1000.0 : x;  // keeps NaN
+  x = x < -1000.0 ? -1000.0 : x;
+  const double n = __builtin_rint(x * 1.4426950408889634);
+  const double f = fma(n, -0.6931471805599453, x);
+  double p = 1.0 / 39916800.0;
+  p = fma(p, f, 1.0 / 3628800.0);
+  p = fma(p, f, 1.0 / 362880.0);
+  p = fma(p, f, 1.0 / 40320.0);
+  p = fma(p, f, 1.0 / 5040.0);
+  p = fma(p, f, 1.0 / 720.0);
+  p = fma(p, f, 1.0 / 120.0);
+  p = fma(p, f, 1.0 / 24.0);
+  p = fma(p, f, 1.0 / 6.0);
+  p = fma(p, f, 0.5);
+  p = fma(p * f, f, f);
+  const double e = ldexp(1.0 + p, (int)n);
+  if (!MINUS_1) return e;
+  return n == 0.0 ? p : e - 1.0;
+}
 
 // ---- the clipped policy loss --------------------------------------------------------
 
@@ -278,6 +343,7 @@ struct PolicyLoss {
   // state[2 s + 1]: derivative of the policy term by the mean of d (sequence
   // level); state[2 B]: the batch's factor.
   using Share = LossSum<4>;  // d, policy, kl, entropy
+  using Token = Terms<4>;
   using Total = LossSum<5>;  // weighted: d, policy, kl, entropy, clipped
   static constexpr int kSides = 1;
 
@@ -302,7 +368,7 @@ struct PolicyLoss {
       bound = in.dual;
     else
       clip = false;
-    f = clip ? -bound * A : (A == 0.0 ? 0.0 : -exp(d) * A);  // A = 0: 0 for any ratio
+    f = clip ? -bound * A : (A == 0.0 ? 0.0 : -exp_f64<false>(d) * A);  // A = 0: 0 for any ratio
     df = clip ? 0.0 : f;
   }
   __device__ static void kl_term(const In& in, double x, double& f, double& df) {
@@ -313,23 +379,23 @@ struct PolicyLoss {
       f = 0.5 * x * x;
       df = x;
     } else {
-      const double e = expm1(-x);
+      const double e = exp_f64<true>(-x);
       f = e + x;
       df = -e;
     }
   }
   // The terms of valid token t of sequence s.
   __device__ static void token(const LossArgs<PolicyLoss>& a, const Raw& r, int64_t t, int64_t s,
-                               Share& v) {
+                               Token& v) {
     const In& in = a.in;
     const double d = (double)r.lp - (double)r.old;
     double df;
-    v.n = 1;
+    v.counts = kCountValid;
     v.x[0] = d;
     if (!in.by_sequence) {
       bool clip;
       clipped(in, d, in.advantages[in.adv_seq ? s : t], v.x[1], df, clip);
-      v.c = clip ? 1 : 0;
+      v.counts += clip ? kCountClipped : 0;
     }
     if (in.ref_logprob != nullptr) kl_term(in, (double)r.lp - (double)r.ref, v.x[2], df);
     v.x[3] = r.ent;
@@ -429,6 +495,7 @@ struct PreferenceLoss {
   // state[s]: gradient of the reduced loss by a valid token's logprob of
   // sequence s; state[B] = 1, or NaN after bad offsets.
   using Share = LossSum<1>;  // logprob - ref_logprob
+  using Token = Terms<1>;
   using Total = LossSum<1>;  // the pairs' losses
   static constexpr int kSides = 2;
 
@@ -439,8 +506,8 @@ struct PreferenceLoss {
     return {a.in.logprob[t], a.in.ref_logprob != nullptr ? a.in.ref_logprob[t] : 0.f};
   }
   __device__ static void token(const LossArgs<PreferenceLoss>&, const Raw& r, int64_t, int64_t,
-                               Share& v) {
-    v.n = 1;
+                               Token& v) {
+    v.counts = kCountValid;
     v.x[0] = (double)r.lp - (double)r.ref;
   }
   __device__ static void item(const LossArgs<PreferenceLoss>& a, int64_t i, Total& tot) {
@@ -509,66 +576,57 @@ struct PreferenceLoss {
 
 // ---- the three steps ----------------------------------------------------------------
 
-// A tile's inputs, lane l having the tokens t0 + 64 j + l: all loads are issued at
-// once, and the rows are then taken one after another by a loop that is not
-// unrolled (next() moves the rows up), which keeps the float64 exponentials to
-// one copy.
-template <class Loss, bool READ>
+// A tile's inputs, lane l having the tokens t0 + 64 j + l; all loads are issued at
+// once.
+template <class Loss, int ROWS, bool READ>
 struct TileRows {
-  typename Loss::Raw raw[kLossRows];
-  int64_t y[kLossRows];
+  typename Loss::Raw raw[ROWS];
+  int64_t y[ROWS];
   __device__ __forceinline__ void load(const LossArgs<Loss>& a, int64_t t0) {
 #pragma unroll
-    for (int j = 0; j < kLossRows; ++j) {
-      if (j >= a.rows) break;
+    for (int j = 0; j < ROWS; ++j) {
       const int64_t t = t0 + j * 64 + (threadIdx.x & 63);
       const int64_t tc = t < a.N ? t : a.N - 1;
       y[j] = a.labels[tc];
       if constexpr (READ) raw[j] = Loss::load(a, tc);
     }
   }
-  __device__ __forceinline__ void next() {
-#pragma unroll
-    for (int j = 0; j + 1 < kLossRows; ++j) {
-      y[j] = y[j + 1];
-      raw[j] = raw[j + 1];
-    }
-  }
 };
 
-// Step 1, one wave, one tile. A tile in one or two sequences, the usual case,
-// adds each lane's tokens and reduces them over the wave once a sequence. With
-// more, each row of 64 tokens is scanned with the sequences as segments, the open
-// segment carried to the next row, and the lane with a sequence's last token in
-// the tile has its share. No LDS either way, so the occupancy is the registers'.
-template <class Loss>
+// Step 1, one wave, one tile of ROWS rows of 64 tokens. A tile in one or two
+// sequences, the usual case, adds each lane's tokens and reduces them over the
+// wave once a sequence. With more, each row is scanned with the sequences as
+// segments, the open segment carried to the next row, and the lane with a
+// sequence's last token in the tile has its share. No LDS either way, so the
+// occupancy is the registers'.
+template <class Loss, int ROWS>
 __device__ __forceinline__ void tile_parts(const LossArgs<Loss>& a, int64_t tile) {
-  using Share = typename Loss::Share;
+  using Token = typename Loss::Token;
   const int lane = threadIdx.x & 63;
-  const int64_t t0 = tile * a.rows * 64;
-  const int64_t t1 = a.N - t0 < a.rows * 64 ? a.N : t0 + a.rows * 64;
-  TileRows<Loss, true> in;
+  const int64_t t0 = tile * (ROWS * 64);
+  const int64_t t1 = a.N - t0 < ROWS * 64 ? a.N : t0 + ROWS * 64;
+  TileRows<Loss, ROWS, true> in;
   in.load(a, t0);
-  const TileSeqs r = tile_sequences(a.cu, a.B, t0, t1);
+  const TileSeqs r = tile_sequences(a.cu, a.B, a.N, t0, t1);
   if (r.ns <= 0) return;
-  Share v0, v1;  // up to two sequences: their sums; more: v0 is the carried segment's
+  Token v0, v1;  // up to two sequences: their sums; more: v0 is the carried segment's
   v0.clear();
   v1.clear();
   int rank0 = -1;        // the carried segment
   bool any0 = false, any1 = false;
-#pragma unroll 1
-  for (int j = 0; j < a.rows; ++j, in.next()) {
+#pragma unroll
+  for (int j = 0; j < ROWS; ++j) {
     const int tl = j * 64 + lane;
     const int64_t t = t0 + tl;
     int rank = token_rank(a.cu, r, t0, tl);
     if (t >= a.N) rank = -1;
-    Share v;
+    Token v;
     v.clear();
     if (rank >= 0) {
-      if (label_valid(in.y[0], a.ignore_index, a.V))
-        Loss::token(a, in.raw[0], t, r.s0 + rank, v);
-      else if (in.y[0] != a.ignore_index)
-        v.inv = 1;
+      if (label_valid(in.y[j], a.ignore_index, a.V))
+        Loss::token(a, in.raw[j], t, r.s0 + rank, v);
+      else if (in.y[j] != a.ignore_index)
+        v.counts = kCountInvalid;
     }
     if (r.ns <= 2) {
       if (rank == 0) {
@@ -586,24 +644,25 @@ __device__ __forceinline__ void tile_parts(const LossArgs<Loss>& a, int64_t tile
     const int head = 63 - __builtin_clzll(heads & (~(uint64_t)0 >> (63 - lane)));
 #pragma unroll 1
     for (int d = 1; d < 64; d <<= 1) {
-      const Share o = v.up(d);
+      const Token o = v.up(d);
       if (lane - d >= head) v.add(o);
     }
     if (rank == rank0 && rank >= 0) v.add(v0);  // only the first segment can match
     const bool ends = ends_sequence(a.cu, r, t0, tl, rank < 0 ? 0 : rank);
-    if (rank >= 0 && (ends || t + 1 == t1)) a.parts[r.s0 + rank + tile] = v;
-    v0 = v.from(63);
-    rank0 = __shfl(rank, 63, 64);
+    if (rank >= 0 && (ends || t + 1 == t1)) a.parts[r.s0 + rank + tile] = v.share();
+    if (j + 1 < ROWS) {
+      v0 = v.from(63);
+      rank0 = __shfl(rank, 63, 64);
+    }
   }
   if (r.ns > 2) return;
-#pragma unroll 1
-  for (int i = 0; i < 2; ++i) {
-    if (__builtin_amdgcn_ballot_w64(any0) != 0) {
-      v0.wave_sum();
-      if (lane == 63) a.parts[r.s0 + i + tile] = v0;
-    }
-    v0 = v1;
-    any0 = any1;
+  if (__builtin_amdgcn_ballot_w64(any0) != 0) {
+    v0.wave_sum();
+    if (lane == 63) a.parts[r.s0 + tile] = v0.share();
+  }
+  if (__builtin_amdgcn_ballot_w64(any1) != 0) {
+    v1.wave_sum();
+    if (lane == 63) a.parts[r.s0 + 1 + tile] = v1.share();
   }
 }
 
@@ -617,7 +676,7 @@ __device__ __forceinline__ SeqParts seq_parts(const int64_t* cu, int64_t N, int 
   const int64_t b = seq_begin(cu, s), e = seq_end(cu, s, N);
   if (b < 0 || e < b || e > N) return {0, 0, true};
   if (b == e) return {0, 0, false};
-  const int sh = 5 + __builtin_ffs(rows);  // log2 of the tile: rows is 1, 2 or 4
+  const int sh = 5 + __builtin_ffs(rows);  // log2 of the tile: rows is a power of two
   return {b >> sh, ((e - 1) >> sh) - (b >> sh) + 1, false};
 }
 
@@ -651,10 +710,8 @@ __device__ __forceinline__ typename Loss::Total sum_sequences(const LossArgs<Los
         mine = false;
       } else {
         for (int64_t q = k; q < p.count; q += g) v.add(a.parts[s + p.p0 + q]);
-        if (p.bad && k == 0) {
-          v.x[0] = __builtin_nan("");
-          v.bad = 1;
-        }
+        v.bad = p.bad && k == 0 ? 1 : 0;
+        if (v.bad != 0) v.x[0] = __builtin_nan("");
       }
     }
     v.group_sum(g);
@@ -689,37 +746,37 @@ template <class Loss>
 __device__ __forceinline__ void finish_batch(const LossArgs<Loss>& a,
                                              const typename Loss::Total& t) {
   if (threadIdx.x == 0) {
-    a.header[0] = t.inv + t.bad;
+    a.header[0] = t.bad != 0 ? t.bad : t.inv;  // shares are undefined beside bad offsets
     a.header[1] = t.n;
     Loss::finish(a, t);
   }
 }
 
 // Step 3, one wave, one tile.
-template <class Loss>
+template <class Loss, int ROWS>
 __device__ __forceinline__ void tile_grads(const LossArgs<Loss>& a, int64_t tile) {
-  const int64_t t0 = tile * a.rows * 64;
-  const int64_t t1 = a.N - t0 < a.rows * 64 ? a.N : t0 + a.rows * 64;
-  TileRows<Loss, Loss::kGradReads> in;
+  const int64_t t0 = tile * (ROWS * 64);
+  const int64_t t1 = a.N - t0 < ROWS * 64 ? a.N : t0 + ROWS * 64;
+  TileRows<Loss, ROWS, Loss::kGradReads> in;
   in.load(a, t0);
-  const TileSeqs r = tile_sequences(a.cu, a.B, t0, t1);
+  const TileSeqs r = tile_sequences(a.cu, a.B, a.N, t0, t1);
   const double scale = Loss::grad_scale(a);
-#pragma unroll 1
-  for (int j = 0; j < a.rows; ++j, in.next()) {
+#pragma unroll
+  for (int j = 0; j < ROWS; ++j) {
     const int tl = j * 64 + (threadIdx.x & 63);
     const int rank = token_rank(a.cu, r, t0, tl);
     const int64_t t = t0 + tl;
     if (t >= a.N) continue;
-    const bool valid = rank >= 0 && label_valid(in.y[0], a.ignore_index, a.V);
-    Loss::grad(a, in.raw[0], scale, t, valid ? r.s0 + rank : -1);
+    const bool valid = rank >= 0 && label_valid(in.y[j], a.ignore_index, a.V);
+    Loss::grad(a, in.raw[j], scale, t, valid ? r.s0 + rank : -1);
   }
 }
 
-template <class Loss>
+template <class Loss, int ROWS>
 __global__ void __launch_bounds__(64 * kLossWaves) loss_parts_kernel(LossArgs<Loss> a) {
   if (blockIdx.x == 0 && threadIdx.x == 0) a.header[2] = 0;  // for the next kernel's count
   const int64_t tile = (int64_t)blockIdx.x * kLossWaves + (threadIdx.x >> 6);
-  if (tile < a.tiles) tile_parts(a, tile);
+  if (tile < a.tiles) tile_parts<Loss, ROWS>(a, tile);
 }
 
 // A block takes `per` items; the block that is done last adds up the blocks'
@@ -751,17 +808,17 @@ __global__ void __launch_bounds__(kSeqThreads) loss_sequences_kernel(LossArgs<Lo
   finish_batch(a, t);
 }
 
-template <class Loss>
+template <class Loss, int ROWS>
 __global__ void __launch_bounds__(64 * kLossWaves) loss_grads_kernel(LossArgs<Loss> a) {
   const int64_t tile = (int64_t)blockIdx.x * kLossWaves + (threadIdx.x >> 6);
-  if (tile < a.tiles) tile_grads(a, tile);
+  if (tile < a.tiles) tile_grads<Loss, ROWS>(a, tile);
 }
 
 // All three steps in one block, for small batches; the steps exchange their sums
 // through LDS.
 template <class Loss, bool GRADS>
 __global__ void __launch_bounds__(64 * kSmallWaves) loss_small_kernel(LossArgs<Loss> a) {
-  __shared__ typename Loss::Share parts[kSmallSequences + kSmallTiles];
+  __shared__ typename Loss::Share parts[kSmallSequences + kSmallTokens / 64];
   __shared__ typename Loss::Share seq_sum[kSmallSequences];
   __shared__ double state[2 * kSmallSequences + 2];
   double* const out_state = a.state;  // the caller's, or null
@@ -769,7 +826,7 @@ __global__ void __launch_bounds__(64 * kSmallWaves) loss_small_kernel(LossArgs<L
   a.seq_sum = seq_sum;
   a.state = state;
   const int w = threadIdx.x >> 6;
-  for (int64_t tile = w; tile < a.tiles; tile += kSmallWaves) tile_parts(a, tile);
+  for (int64_t tile = w; tile < a.tiles; tile += kSmallWaves) tile_parts<Loss, 1>(a, tile);
   __syncthreads();
   finish_batch(a, sum_sequences(a, 0, a.items));
   __syncthreads();
@@ -777,7 +834,7 @@ __global__ void __launch_bounds__(64 * kSmallWaves) loss_small_kernel(LossArgs<L
     for (int i = threadIdx.x; i < Loss::state_size((int)a.B); i += blockDim.x)
       out_state[i] = state[i];
   if constexpr (GRADS)
-    for (int64_t tile = w; tile < a.tiles; tile += kSmallWaves) tile_grads(a, tile);
+    for (int64_t tile = w; tile < a.tiles; tile += kSmallWaves) tile_grads<Loss, 1>(a, tile);
 }
 
 }  // namespace flce

@@ -17,7 +17,6 @@ namespace {
 
 using namespace flce;
 
-static_assert(kSmallTiles * 64 >= kSmallTokens, "a small batch's tiles have 64 tokens or more");
 static_assert(sizeof(PolicyLoss::Share) == sum_bytes(4) && sizeof(PolicyLoss::Total) == sum_bytes(5) &&
                   sizeof(PreferenceLoss::Share) == sum_bytes(1) &&
                   sizeof(PreferenceLoss::Total) == sum_bytes(1),
@@ -30,7 +29,10 @@ flce_status_t run_grads(const LossArgs<Loss>& a, hipStream_t st) {
   if (a.tiles == 0) return FLCE_OK;
   const int grid = (int)ceil_div(a.tiles, kLossWaves);
   return launch(K_LOSS_GRADS, st, [&] {
-    loss_grads_kernel<Loss><<<grid, 64 * kLossWaves, 0, st>>>(a);
+    if (a.rows == 1)
+      loss_grads_kernel<Loss, 1><<<grid, 64 * kLossWaves, 0, st>>>(a);
+    else
+      loss_grads_kernel<Loss, kLossRows><<<grid, 64 * kLossWaves, 0, st>>>(a);
   });
 }
 
@@ -57,7 +59,10 @@ flce_status_t run_loss(LossArgs<Loss>& a, const LossPlan& p, bool grads, void* w
   // At least one block, which readies the header for the next kernel.
   const int grid = (int)ceil_div(a.tiles > 0 ? a.tiles : 1, kLossWaves);
   FLCE_TRY(launch(K_LOSS_PARTS, st, [&] {
-    loss_parts_kernel<Loss><<<grid, 64 * kLossWaves, 0, st>>>(a);
+    if (a.rows == 1)
+      loss_parts_kernel<Loss, 1><<<grid, 64 * kLossWaves, 0, st>>>(a);
+    else
+      loss_parts_kernel<Loss, kLossRows><<<grid, 64 * kLossWaves, 0, st>>>(a);
   }));
   FLCE_TRY(launch(K_LOSS_SEQUENCES, st, [&] {
     loss_sequences_kernel<Loss><<<p.seq_blocks, kSeqThreads, 0, st>>>(a, p.seq_items);

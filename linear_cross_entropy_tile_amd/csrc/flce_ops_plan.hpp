@@ -28,9 +28,8 @@ constexpr int kSmallWaves = 8;        // waves of the one-block kernel
 constexpr int kSeqThreads = 1024;     // threads a block, sequences kernel
 constexpr int64_t kMaxSeqBlocks = 512;
 // Batches up to these sizes take the one-block kernel.
-constexpr int64_t kSmallTokens = 8192;
+constexpr int64_t kSmallTokens = 4096;
 constexpr int64_t kSmallSequences = 1024;
-constexpr int64_t kSmallTiles = 128;
 constexpr int64_t kMaxSequences = (int64_t)1 << 21;
 
 // Workspace: header, shares [B + tiles], sequence sums [B], block totals, and
@@ -52,21 +51,16 @@ FLCE_HD inline int lanes_per_sequence(int64_t B, int64_t tiles) {
   return g;
 }
 
-// Rows a tile: a wave takes its rows one after another, so few as long as the
-// waves do not fill what runs them (the block; the GPU's 1024 SIMDs), then more,
-// for fewer shares.
-inline int loss_rows(int64_t N, bool small) {
-  const int64_t waves = small ? kSmallWaves : 1024;
-  int rows = 1;
-  while (rows < kLossRows && ceil_div(N, 64 * rows) > waves) rows *= 2;
-  return rows;
-}
+// Rows a tile: one while that gives the GPU's 1024 SIMDs four waves or fewer each,
+// so that a wave's chain of dependent loads is short; then kLossRows, for fewer
+// shares and more loads in flight a wave.
+inline int loss_rows(int64_t N) { return ceil_div(N, 64) <= 4096 ? 1 : kLossRows; }
 
 inline LossPlan make_loss_plan(int64_t N, int64_t B, int64_t items, size_t share_bytes,
                                size_t total_bytes, int64_t state_doubles) {
   LossPlan p{};
   p.small = N <= kSmallTokens && B <= kSmallSequences;
-  p.rows = loss_rows(N, p.small);
+  p.rows = loss_rows(N);
   p.tiles = ceil_div(N, 64 * p.rows);
   // One round of a block's lane groups, or more when that makes too many blocks.
   const int64_t round = kSeqThreads / lanes_per_sequence(B, p.tiles) / (B / items);
