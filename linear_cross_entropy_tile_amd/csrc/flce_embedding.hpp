@@ -24,6 +24,8 @@
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
+#include <type_traits>
+
 #include "flce_ops_plan.hpp"
 
 namespace flce {
@@ -53,30 +55,48 @@ __device__ __forceinline__ eu32x4 pack8(const float (&v)[8]) {
                 bf16_pair(v[6], v[7])};
 }
 
-// Eight consecutive values (16 or 32 bytes, 16-byte aligned) from an array of
-// bf16 or fp32.
-template <bool F32>
-__device__ __forceinline__ void load8(const void* p, int64_t i, float (&v)[8]) {
+// W = 4 or 8 consecutive values of an array of bf16 or fp32, aligned to their
+// bytes or to 16.
+template <bool F32, int W>
+__device__ __forceinline__ void load_w(const void* p, int64_t i, float (&v)[W]) {
   if constexpr (F32) {
     const ef32x4* q = reinterpret_cast<const ef32x4*>(static_cast<const float*>(p) + i);
-    const ef32x4 a = q[0], b = q[1];
 #pragma unroll
-    for (int k = 0; k < 4; ++k) {
-      v[k] = a[k];
-      v[4 + k] = b[k];
+    for (int j = 0; j < W / 4; ++j) {
+      const ef32x4 x = q[j];
+#pragma unroll
+      for (int k = 0; k < 4; ++k) v[4 * j + k] = x[k];
     }
   } else {
-    unpack8(*reinterpret_cast<const eu32x4*>(static_cast<const uint16_t*>(p) + i), v);
+    typedef uint32_t words __attribute__((ext_vector_type(W / 2)));
+    const words x = *reinterpret_cast<const words*>(static_cast<const uint16_t*>(p) + i);
+#pragma unroll
+    for (int j = 0; j < W / 2; ++j) {
+      v[2 * j] = bf16_lo(x[j]);
+      v[2 * j + 1] = bf16_hi(x[j]);
+    }
   }
 }
-template <bool F32>
-__device__ __forceinline__ void store8(void* p, int64_t i, const float (&v)[8]) {
+// Outputs are streamed past the caches (nontemporal): they are larger than the
+// caches and would push out the inputs. A lookup of 32768 rows of 4096 values took
+// 77 us without and takes 54 us; an fp32 gradient of [32000, 4096] 125 and 107 us.
+template <class T>
+__device__ __forceinline__ void stream(T* p, const T& v) {
+  __builtin_nontemporal_store(v, p);
+}
+template <bool F32, int W>
+__device__ __forceinline__ void store_w(void* p, int64_t i, const float (&v)[W]) {
   if constexpr (F32) {
     ef32x4* q = reinterpret_cast<ef32x4*>(static_cast<float*>(p) + i);
-    q[0] = ef32x4{v[0], v[1], v[2], v[3]};
-    q[1] = ef32x4{v[4], v[5], v[6], v[7]};
+#pragma unroll
+    for (int j = 0; j < W / 4; ++j)
+      stream(q + j, ef32x4{v[4 * j], v[4 * j + 1], v[4 * j + 2], v[4 * j + 3]});
   } else {
-    *reinterpret_cast<eu32x4*>(static_cast<uint16_t*>(p) + i) = pack8(v);
+    typedef uint32_t words __attribute__((ext_vector_type(W / 2)));
+    words x;
+#pragma unroll
+    for (int j = 0; j < W / 2; ++j) x[j] = bf16_pair(v[2 * j], v[2 * j + 1]);
+    stream(reinterpret_cast<words*>(static_cast<uint16_t*>(p) + i), x);
   }
 }
 
@@ -174,91 +194,73 @@ __device__ __forceinline__ int block_exclusive(int v, int* sh) {
   return off + x - v;
 }
 
-constexpr int kSortWaves = 16;
-constexpr int kSortDigits = 512;
+// Up to kRankTokens tokens: every item's place is counted, N compares an item
+// spread over the whole GPU, in one launch and without a dependence on any other
+// item's place. 32 items a block; thread (part, item) compares the item with every
+// 32nd group of 32 keys, four keys a (broadcast) LDS read. Equal keys keep their
+// order: earlier groups count keys <= the item's, later ones keys < it, and the
+// item's own group goes by the position. Keys stay below 2^23, so x < t is the sign
+// of x - t: three VALU operations a compare, no condition codes (whose hazards cost
+// as much again).
+constexpr int kRankItems = 32;
+constexpr int kRankThreads = 1024;
 
-// All passes in one block with the keys in LDS: 1024 * ITEMS items. Item order is
-// wave, then round, then lane, so ranks by (wave, round, lane) keep it.
-template <int ITEMS>
-__global__ void __launch_bounds__(64 * kSortWaves) embed_sort_block_kernel(TokenArgs a, int passes,
-                                                                           int bits, int32_t* key,
-                                                                           int32_t* perm) {
-  constexpr int kCap = 64 * kSortWaves * ITEMS;
-  __shared__ uint32_t skey[kCap];
-  __shared__ uint32_t sperm[kCap];
-  __shared__ uint16_t cnt[kSortWaves][kSortDigits];
-  __shared__ int base[kSortDigits];
-  __shared__ int sh[kSortWaves];
-  const int lane = threadIdx.x & 63, w = threadIdx.x >> 6;
-  const int nd = 1 << bits;
-  const uint32_t last = (uint32_t)(((uint64_t)1 << (passes * bits)) - 1);  // >= every key
-  uint32_t k[ITEMS], p[ITEMS];
-  int rank[ITEMS];
+// -1 if x < t, else 0.
+__device__ __forceinline__ int minus_less(uint32_t x, uint32_t t) {
+  return (int)(x - t) >> 31;
+}
+
+__global__ void __launch_bounds__(kRankThreads) embed_rank_kernel(TokenArgs a, int32_t* key_out,
+                                                                  int32_t* perm_out) {
+  extern __shared__ uint32_t keys[];  // N, rounded up to groups
+  __shared__ int count[kRankItems];
+  __shared__ int sh[kRankThreads / 64];
+  const int tid = threadIdx.x;
+  const int N = (int)a.N, groups = (N + kRankItems - 1) / kRankItems;
   int inv = 0, n = 0;
-#pragma unroll
-  for (int j = 0; j < ITEMS; ++j) {
-    const int i = (w * ITEMS + j) * 64 + lane;
-    k[j] = last;
-    p[j] = (uint32_t)i;
-    if (i < a.N) {
+  for (int i = tid; i < groups * kRankItems; i += kRankThreads) {
+    uint32_t k = 1u << 24;  // past the end: above every bound
+    if (i < N) {
       bool bad;
-      k[j] = (uint32_t)token_key(a, a.tokens[i], bad);
-      n += k[j] < (uint32_t)a.Vs ? 1 : 0;
+      k = (uint32_t)token_key(a, a.tokens[i], bad);
+      n += k < (uint32_t)a.Vs ? 1 : 0;
       inv += bad ? 1 : 0;
     }
+    keys[i] = k;
   }
-  inv = block_sum_int(inv, sh);
-  n = block_sum_int(n, sh);
-  if (threadIdx.x == 0) {
-    a.header[0] = inv;
-    a.header[1] = n;
-  }
-  for (int pass = 0; pass < passes; ++pass) {
-    const int shift = pass * bits;
-    for (int i = threadIdx.x; i < kSortWaves * nd; i += 64 * kSortWaves) {
-      const int cw = i >> bits;
-      cnt[cw][i & (nd - 1)] = 0;
-    }
-    __syncthreads();
-#pragma unroll
-    for (int j = 0; j < ITEMS; ++j)
-      rank[j] = wave_rank((k[j] >> shift) & (uint32_t)(nd - 1), bits, cnt[w]);
-    __syncthreads();
-    int total = 0;
-    if ((int)threadIdx.x < nd) {
-      for (int v = 0; v < kSortWaves; ++v) {
-        const int c = cnt[v][threadIdx.x];
-        cnt[v][threadIdx.x] = (uint16_t)total;  // <= 16384 - 1 where an item follows
-        total += c;
-      }
-    }
-    const int off = block_exclusive(total, sh);
-    if ((int)threadIdx.x < nd) base[threadIdx.x] = off;
-    __syncthreads();
-#pragma unroll
-    for (int j = 0; j < ITEMS; ++j) {
-      const uint32_t d = (k[j] >> shift) & (uint32_t)(nd - 1);
-      const int q = base[d] + cnt[w][d] + rank[j];
-      skey[q] = k[j];
-      sperm[q] = p[j];
-    }
-    __syncthreads();
-#pragma unroll
-    for (int j = 0; j < ITEMS; ++j) {
-      const int i = (w * ITEMS + j) * 64 + lane;
-      k[j] = skey[i];
-      p[j] = sperm[i];
-    }
-    __syncthreads();
-  }
-#pragma unroll
-  for (int j = 0; j < ITEMS; ++j) {
-    const int i = (w * ITEMS + j) * 64 + lane;
-    if (i < a.N) {
-      key[i] = (int32_t)k[j];
-      perm[i] = (int32_t)p[j];
+  if (tid < kRankItems) count[tid] = 0;
+  if (blockIdx.x == 0) {
+    inv = block_sum_int(inv, sh);
+    n = block_sum_int(n, sh);
+    if (tid == 0) {
+      a.header[0] = inv;
+      a.header[1] = n;
     }
   }
+  __syncthreads();
+  const int item = tid & (kRankItems - 1), part = tid / kRankItems;
+  const int own = (int)blockIdx.x;  // the block's group of items
+  if (own >= groups) return;        // no tokens at all
+  const uint32_t k = keys[own * kRankItems + item];
+  int c = 0;
+  for (int g = part; g < groups; g += kRankThreads / kRankItems) {
+    const eu32x4* q = reinterpret_cast<const eu32x4*>(keys + g * kRankItems);
+    const uint32_t t = g < own ? k + 1 : k;
+    const int tie = g == own ? item : 0;  // own group: equal keys before the item count too
+#pragma unroll
+    for (int j = 0; j < kRankItems / 4; ++j) {
+      const eu32x4 x = q[j];
+      c += minus_less(x[0], t) + minus_less(x[1], t);
+      c += minus_less(x[2], t) + minus_less(x[3], t);
+    }
+    for (int e = 0; e < tie; ++e) c -= keys[g * kRankItems + e] == k ? 1 : 0;
+  }
+  atomicAdd(&count[item], -c);  // of whole numbers: the order does not matter
+  __syncthreads();
+  const int i = own * kRankItems + item;
+  if (tid >= kRankItems || i >= N) return;
+  key_out[count[item]] = (int32_t)k;
+  perm_out[count[item]] = i;
 }
 
 // The larger sort, a pass: digit counts of every tile of kSortTile items, the
@@ -402,61 +404,57 @@ struct GatherArgs {
   float scale;
   uint16_t* out;
   int count_block;            // 1: the last block of grid.x fills the header
-  int tpr;                    // threads a row (table lookup)
+  int lanes;                  // lanes a row (table lookup): a power of two, 8 to 64
 };
 
-constexpr int kGatherRows = 4;  // rows a thread has in flight
+// Rows of a table [Vs,H], eight values a lane. Wide rows: a wave takes a row and a
+// chunk of kGatherLoads * 512 of its values, all loads in flight before the first
+// store. Narrow ones (lanes < 64): a wave takes 64 / lanes rows at a time.
+constexpr int kGatherLoads = 5;
 
-// Rows of a table [Vs,H]: tpr threads a row, 8 values each.
+__device__ __forceinline__ eu32x4 scaled8(const eu32x4& w, float scale) {
+  if (scale == 1.f) return w;
+  float v[8];
+  unpack8(w, v);
+#pragma unroll
+  for (int e = 0; e < 8; ++e) v[e] *= scale;
+  return pack8(v);
+}
+
 __global__ void __launch_bounds__(256) embed_gather_rows_kernel(GatherArgs a) {
   __shared__ int sh[4];
   if (a.count_block != 0 && blockIdx.x == gridDim.x - 1) {
     if (blockIdx.y == 0) count_tokens(a.t, sh);
     return;
   }
-  const int per = 256 / a.tpr;  // rows side by side
-  const int64_t h = ((int64_t)blockIdx.y * a.tpr + threadIdx.x % a.tpr) * 8;
-  const int64_t r0 = (int64_t)blockIdx.x * per * kGatherRows + threadIdx.x / a.tpr;
-  int32_t key[kGatherRows];
-  int inv = 0, n = 0;
-#pragma unroll
-  for (int j = 0; j < kGatherRows; ++j) {
-    const int64_t i = r0 + j * per;
-    bool bad = false;
-    key[j] = i < a.t.N ? token_key(a.t, a.t.tokens[i], bad) : (int32_t)a.t.Vs;
-    inv += bad ? 1 : 0;
-    n += key[j] < a.t.Vs ? 1 : 0;
-  }
+  const int lane = threadIdx.x & 63, w = threadIdx.x >> 6;
+  const int side = 64 / a.lanes;  // rows a wave takes side by side
+  const int64_t i = ((int64_t)blockIdx.x * 4 + w) * side + lane / a.lanes;
+  const int k = lane & (a.lanes - 1);
+  bool bad = false;
+  const bool on = i < a.t.N;
+  const int32_t key = on ? token_key(a.t, a.t.tokens[i], bad) : (int32_t)a.t.Vs;
   if (a.count_block == 0 && blockIdx.y == 0) {
-    // One thread a row counts.
-    inv = block_sum_int(threadIdx.x % a.tpr == 0 ? inv : 0, sh);
-    n = block_sum_int(threadIdx.x % a.tpr == 0 ? n : 0, sh);
-    if (threadIdx.x == 0) {
-      if (inv != 0) atomicAdd(&a.t.header[0], inv);
-      if (n != 0) atomicAdd(&a.t.header[1], n);
-    }
+    // Invalid tokens only: an atomic a block on one address would take longer than
+    // the copy.
+    const uint64_t inv = __builtin_amdgcn_ballot_w64(k == 0 && bad);
+    if (inv != 0 && lane == 0) atomicAdd(&a.t.header[0], __popcll(inv));
   }
-  if (h >= a.H) return;
-  eu32x4 w[kGatherRows];
+  if (!on) return;
+  const int64_t h0 = ((int64_t)blockIdx.y * kGatherLoads * a.lanes + k) * 8;
+  const uint16_t* src = a.weight + (int64_t)key * a.H;
+  uint16_t* dst = a.out + i * a.H;
+  eu32x4 v[kGatherLoads];
 #pragma unroll
-  for (int j = 0; j < kGatherRows; ++j) {
-    w[j] = eu32x4{0u, 0u, 0u, 0u};
-    if (key[j] < a.t.Vs)
-      w[j] = *reinterpret_cast<const eu32x4*>(a.weight + (int64_t)key[j] * a.H + h);
+  for (int j = 0; j < kGatherLoads; ++j) {
+    const int64_t h = h0 + (int64_t)j * a.lanes * 8;
+    v[j] = eu32x4{0u, 0u, 0u, 0u};
+    if (key < a.t.Vs && h < a.H) v[j] = *reinterpret_cast<const eu32x4*>(src + h);
   }
 #pragma unroll
-  for (int j = 0; j < kGatherRows; ++j) {
-    const int64_t i = r0 + j * per;
-    if (i >= a.t.N) continue;
-    eu32x4 o = w[j];
-    if (a.scale != 1.f && key[j] < a.t.Vs) {
-      float v[8];
-      unpack8(w[j], v);
-#pragma unroll
-      for (int e = 0; e < 8; ++e) v[e] *= a.scale;
-      o = pack8(v);
-    }
-    *reinterpret_cast<eu32x4*>(a.out + i * a.H + h) = o;
+  for (int j = 0; j < kGatherLoads; ++j) {
+    const int64_t h = h0 + (int64_t)j * a.lanes * 8;
+    if (h < a.H) stream(reinterpret_cast<eu32x4*>(dst + h), scaled8(v[j], a.scale));
   }
 }
 
@@ -464,16 +462,21 @@ __global__ void __launch_bounds__(256) embed_gather_rows_kernel(GatherArgs a) {
 // hidden values; lane (t, g) gathers 8 values of token t down the rows 8 g .. and
 // stores them as 16 bytes, 128 contiguous bytes a token.
 constexpr int kGatherTokens = 32;  // tokens a block
+constexpr int kGatherGridY = 32768;
 
 __global__ void __launch_bounds__(256) embed_gather_cols_kernel(GatherArgs a) {
   __shared__ int sh[4];
-  if (a.count_block != 0 && blockIdx.x == gridDim.x - 1) {
-    if (blockIdx.y == 0) count_tokens(a.t, sh);
+  if (a.count_block != 0 && blockIdx.y == gridDim.y - 1) {
+    if (blockIdx.x == 0) count_tokens(a.t, sh);
     return;
   }
   const int lane = threadIdx.x & 63;
-  const int64_t i = (int64_t)blockIdx.x * kGatherTokens + (threadIdx.x >> 6) * 8 + (lane & 7);
-  const int64_t h = (int64_t)blockIdx.y * 64 + (lane >> 3) * 8;
+  // Blocks go to the 8 XCDs in turn, each with an L2 of its own. grid.x is a multiple
+  // of 8, so a chunk of 64 rows of the weight stays with one XCD, and the tokens of
+  // a line, neighbours in the sorted order, find it in that L2.
+  const int64_t blk = (int64_t)blockIdx.z * kGatherGridY + blockIdx.y;
+  const int64_t i = blk * kGatherTokens + (threadIdx.x >> 6) * 8 + (lane & 7);
+  const int64_t h = (int64_t)blockIdx.x * 64 + (lane >> 3) * 8;
   if (i >= a.t.N || h >= a.H) return;
   bool bad;
   const int32_t key = a.key != nullptr ? a.key[i] : token_key(a.t, a.t.tokens[i], bad);
@@ -503,95 +506,132 @@ struct GradArgs {
   const void* grad;           // [N,H]
   const int32_t *key, *perm;  // sorted
   const int32_t* header;      // [1] tokens of the slice: the sorted positions that count
-  int32_t* starts;            // [Vs + 1]
+  int32_t* strips;            // [strips + 1] first sorted position of every strip of 64 rows
   float* part;                // [2 * pieces][H]
   int64_t N, H, Vs;
   float scale;
   void* out;
-  int start_blocks;           // blocks of the segments kernel that fill starts
+  int strip_blocks;           // blocks of the segments kernel that fill strips
   int chunks;                 // column chunks a piece
-  int tpr;                    // threads a row (table layout)
+  int lanes;                  // lanes a row, eight values each: a power of two, 8 to 64
+  int64_t range;              // hidden values a block takes
 };
 
-// acc += gradient rows of the sorted positions [b, e), in order.
-template <bool HF32>
-__device__ __forceinline__ void add_rows(const GradArgs& a, int64_t b, int64_t e, int64_t h,
-                                         float (&acc)[8]) {
-  int64_t i = b;
-  for (; i + 4 <= e; i += 4) {
-    float v[4][8];
+// acc += gradient rows of the sorted positions [b, e), in order. All `lanes` lanes of
+// a group call it with the same range, lane k of them holding W columns from each of
+// h[0 .. U); a lane reads one position's row number for the group at a time. DEEP
+// rows are in flight at once.
+template <bool HF32, int W, int U, int DEEP>
+__device__ __forceinline__ void add_rows(const GradArgs& a, int64_t b, int64_t e, int lanes, int k,
+                                         const int64_t (&h)[U], float (&acc)[U][W]) {
+  const int first = (threadIdx.x & 63) - k;
+  for (int64_t c = b; c < e; c += lanes) {
+    const int32_t row = c + k < e ? a.perm[c + k] : 0;
+    const int m = e - c < lanes ? (int)(e - c) : lanes;
+    int j = 0;
+    for (; j + DEEP <= m; j += DEEP) {
+      float v[DEEP][U][W];
 #pragma unroll
-    for (int j = 0; j < 4; ++j) load8<HF32>(a.grad, (int64_t)a.perm[i + j] * a.H + h, v[j]);
+      for (int d = 0; d < DEEP; ++d) {
+        const int64_t at = (int64_t)__shfl(row, first + j + d, 64) * a.H;
 #pragma unroll
-    for (int j = 0; j < 4; ++j)
+        for (int u = 0; u < U; ++u) load_w<HF32, W>(a.grad, at + h[u], v[d][u]);
+      }
 #pragma unroll
-      for (int c = 0; c < 8; ++c) acc[c] += v[j][c];
-  }
-  for (; i < e; ++i) {
-    float v[8];
-    load8<HF32>(a.grad, (int64_t)a.perm[i] * a.H + h, v);
+      for (int d = 0; d < DEEP; ++d)
 #pragma unroll
-    for (int c = 0; c < 8; ++c) acc[c] += v[c];
+        for (int u = 0; u < U; ++u)
+#pragma unroll
+          for (int q = 0; q < W; ++q) acc[u][q] += v[d][u][q];
+    }
+    for (; j < m; ++j) {
+      const int64_t at = (int64_t)__shfl(row, first + j, 64) * a.H;
+      float v[U][W];
+#pragma unroll
+      for (int u = 0; u < U; ++u) load_w<HF32, W>(a.grad, at + h[u], v[u]);
+#pragma unroll
+      for (int u = 0; u < U; ++u)
+#pragma unroll
+        for (int q = 0; q < W; ++q) acc[u][q] += v[u][q];
+    }
   }
 }
 
 // The sum of the run [b, e): directly, or from its pieces' sums.
-template <bool HF32>
-__device__ __forceinline__ void run_sum(const GradArgs& a, int64_t b, int64_t e, int64_t h,
-                                        float (&acc)[8]) {
+template <bool HF32, int W, int U, int DEEP>
+__device__ __forceinline__ void run_sum(const GradArgs& a, int64_t b, int64_t e, int lanes, int k,
+                                        const int64_t (&h)[U], float (&acc)[U][W]) {
 #pragma unroll
-  for (int c = 0; c < 8; ++c) acc[c] = 0.f;
+  for (int u = 0; u < U; ++u)
+#pragma unroll
+    for (int q = 0; q < W; ++q) acc[u][q] = 0.f;
   if (e - b <= kPiece) {
-    add_rows<HF32>(a, b, e, h, acc);
+    add_rows<HF32, W, U, DEEP>(a, b, e, lanes, k, h, acc);
     return;
   }
-  const int64_t p0 = b / kPiece, p1 = (e - 1) / kPiece;
-  int64_t p = p0;
-  if (b > p0 * kPiece) {  // starts inside its first piece
-    load8<true>(a.part, (2 * p0 + 1) * a.H + h, acc);
+  const int64_t p1 = (e - 1) / kPiece;
+  int64_t p = b / kPiece;
+  if (b > p * kPiece) {  // starts inside its first piece
+#pragma unroll
+    for (int u = 0; u < U; ++u) load_w<true, W>(a.part, (2 * p + 1) * a.H + h[u], acc[u]);
     ++p;
   }
-  for (; p + 4 <= p1 + 1; p += 4) {
-    float v[4][8];
+  for (; p + DEEP <= p1 + 1; p += DEEP) {
+    float v[DEEP][U][W];
 #pragma unroll
-    for (int j = 0; j < 4; ++j) load8<true>(a.part, 2 * (p + j) * a.H + h, v[j]);
+    for (int d = 0; d < DEEP; ++d)
 #pragma unroll
-    for (int j = 0; j < 4; ++j)
+      for (int u = 0; u < U; ++u) load_w<true, W>(a.part, 2 * (p + d) * a.H + h[u], v[d][u]);
 #pragma unroll
-      for (int c = 0; c < 8; ++c) acc[c] += v[j][c];
+    for (int d = 0; d < DEEP; ++d)
+#pragma unroll
+      for (int u = 0; u < U; ++u)
+#pragma unroll
+        for (int q = 0; q < W; ++q) acc[u][q] += v[d][u][q];
   }
   for (; p <= p1; ++p) {
-    float v[8];
-    load8<true>(a.part, 2 * p * a.H + h, v);
+    float v[U][W];
 #pragma unroll
-    for (int c = 0; c < 8; ++c) acc[c] += v[c];
+    for (int u = 0; u < U; ++u) load_w<true, W>(a.part, 2 * p * a.H + h[u], v[u]);
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+#pragma unroll
+      for (int q = 0; q < W; ++q) acc[u][q] += v[u][q];
   }
 }
 
-// First blocks: starts[v], the first sorted position with key >= v. The others:
-// one piece and column chunk each, summing the split runs that overlap it.
+__device__ __forceinline__ int64_t lower_bound(const int32_t* key, int64_t lo, int64_t hi,
+                                               int64_t v) {
+  while (lo < hi) {
+    const int64_t mid = (lo + hi) >> 1;
+    if (key[mid] < v)
+      lo = mid + 1;
+    else
+      hi = mid;
+  }
+  return lo;
+}
+
+__device__ __forceinline__ void store_part(const GradArgs& a, int64_t slot, int64_t h,
+                                           const float (&v)[4]) {
+  *reinterpret_cast<ef32x4*>(a.part + slot * a.H + h) = ef32x4{v[0], v[1], v[2], v[3]};
+}
+
+// First blocks: the strips. The others: one piece and column chunk each, summing the
+// split runs that overlap it, 16 rows in flight.
 template <bool HF32>
 __global__ void __launch_bounds__(256) embed_segments_kernel(GradArgs a) {
   const int64_t n = a.header[1];
-  if ((int)blockIdx.x < a.start_blocks) {
-    const int64_t v = (int64_t)blockIdx.x * blockDim.x + threadIdx.x;
-    if (v > a.Vs) return;
-    int64_t lo = 0, hi = n;
-    while (lo < hi) {
-      const int64_t mid = (lo + hi) >> 1;
-      if (a.key[mid] < v)
-        lo = mid + 1;
-      else
-        hi = mid;
-    }
-    a.starts[v] = (int32_t)lo;
+  if ((int)blockIdx.x < a.strip_blocks) {
+    const int64_t s = (int64_t)blockIdx.x * blockDim.x + threadIdx.x;
+    const int64_t v = s * kStrip < a.Vs ? s * kStrip : a.Vs;
+    if (s * kStrip < a.Vs + kStrip) a.strips[s] = (int32_t)lower_bound(a.key, 0, n, v);
     return;
   }
-  const int64_t id = (int64_t)blockIdx.x - a.start_blocks;
+  const int64_t id = (int64_t)blockIdx.x - a.strip_blocks;
   const int64_t piece = id / a.chunks;
   const int64_t q0 = piece * kPiece;
   if (q0 >= n) return;
-  const int64_t h = ((id % a.chunks) * blockDim.x + threadIdx.x) * 8;
   // Keys around the piece: positions q0 - 32 .. q0 + 31 and q0 + 32 .. q0 + 95;
   // -1 (no key) outside the slice's tokens.
   const int lane = threadIdx.x & 63;
@@ -611,122 +651,187 @@ __global__ void __launch_bounds__(256) embed_segments_kernel(GradArgs a) {
   const int tail = __popcll(l0 >> kPiece);          // of `last`, within the piece
   const bool split_first = __popcll(f0) + __popcll(f1) > kPiece;
   const bool split_last = last != first && tail + __popcll(l1) > kPiece;
-  if (h >= a.H) return;
+  const int64_t h = ((id % a.chunks) * blockDim.x + threadIdx.x) * 4;
+  const bool on = h < a.H;           // the whole wave takes part in the row numbers' exchange
+  const int64_t hc[1] = {on ? h : a.H - 4};
   if (split_first) {
-    float acc[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-    add_rows<HF32>(a, q0, q0 + head, h, acc);
-    store8<true>(a.part, 2 * piece * a.H + h, acc);
+    float acc[1][4] = {};
+    add_rows<HF32, 4, 1, 16>(a, q0, q0 + head, 64, lane, hc, acc);
+    if (on) store_part(a, 2 * piece, h, acc[0]);
   }
   if (split_last) {
-    float acc[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-    add_rows<HF32>(a, qe - tail, qe, h, acc);
-    store8<true>(a.part, (2 * piece + 1) * a.H + h, acc);
+    float acc[1][4] = {};
+    add_rows<HF32, 4, 1, 16>(a, qe - tail, qe, 64, lane, hc, acc);
+    if (on) store_part(a, 2 * piece + 1, h, acc[0]);
   }
 }
 
-constexpr int kGradRows = 8;  // rows a thread takes one after another
+// Rows of a table gradient [Vs,H]: a block takes kGradRows consecutive rows, whole
+// or in column ranges, W values (16 bytes of output) a lane, so that what the GPU
+// writes at a time is close together and every store instruction writes whole
+// lines.
+constexpr int kGradRows = 4;
+constexpr int kGradSteps = 4;  // column steps in flight
 
-// Rows of a table gradient [Vs,H].
 template <bool HF32, bool GF32, bool ACC>
 __global__ void __launch_bounds__(256) embed_grad_rows_kernel(GradArgs a) {
-  const int per = 256 / a.tpr;
-  const int64_t h = ((int64_t)blockIdx.y * a.tpr + threadIdx.x % a.tpr) * 8;
-  const int64_t v0 = (int64_t)blockIdx.x * per * kGradRows + threadIdx.x / a.tpr;
-  if (h >= a.H) return;
-#pragma unroll 2
-  for (int j = 0; j < kGradRows; ++j) {
-    const int64_t v = v0 + j * per;
-    if (v >= a.Vs) return;
-    const int64_t b = a.starts[v], e = a.starts[v + 1];
-    float acc[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+  constexpr int W = GF32 ? 4 : 8;
+  __shared__ int32_t st[kGradRows + 1];
+  const int64_t v0 = (int64_t)blockIdx.x * kGradRows;
+  const int64_t b0 = a.strips[v0 / kStrip], e0 = a.strips[v0 / kStrip + 1];
+  if (ACC && b0 == e0) return;
+  if (b0 < e0) {
+    if (threadIdx.x <= kGradRows)
+      st[threadIdx.x] = (int32_t)lower_bound(a.key, b0, e0, v0 + threadIdx.x);
+    __syncthreads();
+  }
+  const int nv = a.Vs - v0 < kGradRows ? (int)(a.Vs - v0) : kGradRows;
+  const int k = threadIdx.x & (a.lanes - 1);
+  const int64_t h0 = (int64_t)blockIdx.y * a.range;
+  const int64_t h1 = h0 + a.range < a.H ? h0 + a.range : a.H;
+  for (int r = threadIdx.x / a.lanes; r < nv; r += 256 / a.lanes) {
+    const int64_t b = b0 < e0 ? st[r] : 0, e = b0 < e0 ? st[r + 1] : 0;
     if (b == e) {
-      if constexpr (!ACC) store8<GF32>(a.out, v * a.H + h, acc);
+      if constexpr (!ACC) {
+        const float zero[W] = {};
+        for (int64_t h = h0 + k * W; h < h1; h += a.lanes * W)
+          store_w<GF32, W>(a.out, (v0 + r) * a.H + h, zero);
+      }
       continue;
     }
-    run_sum<HF32>(a, b, e, h, acc);
+    for (int64_t hs = h0; hs < h1; hs += a.lanes * W * kGradSteps) {
+      int64_t h[kGradSteps];
+      float acc[kGradSteps][W];
 #pragma unroll
-    for (int c = 0; c < 8; ++c) acc[c] *= a.scale;
-    if constexpr (ACC) {
-      float old[8];
-      load8<GF32>(a.out, v * a.H + h, old);
+      for (int u = 0; u < kGradSteps; ++u) {
+        h[u] = hs + ((int64_t)u * a.lanes + k) * W;
+        if (h[u] >= h1) h[u] = h1 - W;  // the same values as the range's last lane
+      }
+      run_sum<HF32, W, kGradSteps, 2>(a, b, e, a.lanes, k, h, acc);
 #pragma unroll
-      for (int c = 0; c < 8; ++c) acc[c] += old[c];
+      for (int u = 0; u < kGradSteps; ++u) {
+        if (hs + ((int64_t)u * a.lanes + k) * W >= h1) continue;
+#pragma unroll
+        for (int q = 0; q < W; ++q) acc[u][q] *= a.scale;
+        const int64_t at = (v0 + r) * a.H + h[u];
+        if constexpr (ACC) {
+          float old[W];
+          load_w<GF32, W>(a.out, at, old);
+#pragma unroll
+          for (int q = 0; q < W; ++q) acc[u][q] += old[q];
+        }
+        store_w<GF32, W>(a.out, at, acc[u]);
+      }
     }
-    store8<GF32>(a.out, v * a.H + h, acc);
   }
 }
 
-// Columns of a weight gradient [H,Vs]: a block takes a strip of 64 columns and
-// 128 hidden values, sums the strip's runs to an LDS tile (16 lanes a run, 8
-// values each) and writes the tile's rows, 128 (bf16) or 256 bytes each. VEC:
-// rows start 16-byte aligned (Vs a multiple of 8), eight columns a thread;
+// Columns of a weight gradient [H,Vs]: a block takes a strip of 64 columns and 128
+// hidden values, sums the runs of the columns that have one to an LDS tile (16 lanes
+// a run, 8 values each; the other columns stay as the tile was cleared) and writes
+// the tile's rows, 128 (bf16) or 256 bytes each. Neighbouring strips run together,
+// so that the GPU's writes of a row lie together; taking a strip's hidden values
+// together instead, or 256 or 512 of them a block, was 3 to 30 % slower.
+// The tile holds what is stored, bf16 or fp32, so twice as many blocks fit where
+// that is bf16; sums that are added to what is there stay fp32 until then. VEC:
+// rows start 16-byte aligned (Vs a multiple of 8), 16 bytes of a row a thread;
 // otherwise one column a thread.
-constexpr int kStrip = 64;
 constexpr int kStripH = 128;
 
 template <bool HF32, bool GF32, bool ACC, bool VEC>
 __global__ void __launch_bounds__(256) embed_grad_cols_kernel(GradArgs a) {
-  __shared__ float tile[kStripH][kStrip + 1];
+  constexpr bool TF32 = GF32 || ACC;
+  using T = std::conditional_t<TF32, float, uint16_t>;
+  constexpr int kPitch = TF32 ? kStrip + 1 : kStrip + 2;
+  __shared__ __attribute__((aligned(16))) T tile[kStripH * kPitch];
   __shared__ int32_t st[kStrip + 1];
+  __shared__ uint8_t used[kStrip];
   const int tid = threadIdx.x;
   const int64_t v0 = (int64_t)blockIdx.x * kStrip;
-  const int64_t h0 = (int64_t)blockIdx.y * kStripH;
   const int nv = a.Vs - v0 < kStrip ? (int)(a.Vs - v0) : kStrip;
+  const int64_t b0 = a.strips[blockIdx.x], e0 = a.strips[blockIdx.x + 1];
+  const bool any = b0 < e0;
+  if (ACC && !any) return;
+  int nu = 0;
+  if (any) {
+    if (tid <= kStrip) st[tid] = (int32_t)lower_bound(a.key, b0, e0, v0 + tid);
+    // Added to what is there, -0 changes nothing, the sign of a zero included.
+    for (int i = tid; i < kStripH * kPitch; i += 256) tile[i] = ACC ? (T)-0.f : (T)0;
+    __syncthreads();
+    const int lane = tid & 63;
+    const uint64_t mask = __builtin_amdgcn_ballot_w64(st[lane] < st[lane + 1]);
+    nu = __popcll(mask);
+    if (tid < 64 && ((mask >> lane) & 1) != 0) used[lanes_below(mask)] = (uint8_t)lane;
+    __syncthreads();
+  }
+  const int64_t h0 = (int64_t)blockIdx.y * kStripH;
   const int nh = a.H - h0 < kStripH ? (int)(a.H - h0) : kStripH;
-  if (tid <= kStrip) st[tid] = a.starts[v0 + (tid < nv ? tid : nv)];
-  __syncthreads();
-  const bool empty = st[0] == st[kStrip];
-  if (empty && ACC) return;
-  if (!empty) {
-    const int hl = (tid & 15) * 8;
-    for (int r = tid >> 4; r < kStrip; r += 16) {
-      const int64_t b = st[r], e = st[r + 1];
+  if (any) {
+    const int k = tid & 15, hl = k * 8;
+    for (int u = tid >> 4; u < nu; u += 16) {
+      const int r = used[u];
+      const int64_t h[1] = {hl < nh ? h0 + hl : a.H - 8};
+      float sum[1][8];
+      run_sum<HF32, 8, 1, 4>(a, st[r], st[r + 1], 16, k, h, sum);
       float acc[8];
-      if (b < e && hl < nh) {
-        run_sum<HF32>(a, b, e, h0 + hl, acc);
 #pragma unroll
-        for (int c = 0; c < 8; ++c) acc[c] *= a.scale;
-      } else {
-        // Added to what is there, -0 changes nothing, the sign of a zero included.
+      for (int c = 0; c < 8; ++c) acc[c] = sum[0][c] * a.scale;
 #pragma unroll
-        for (int c = 0; c < 8; ++c) acc[c] = ACC ? -0.f : 0.f;
+      for (int c = 0; c < 8; ++c) {
+        if constexpr (TF32)
+          tile[(hl + c) * kPitch + r] = acc[c];
+        else
+          tile[(hl + c) * kPitch + r] = (uint16_t)(bf16_pair(acc[c], 0.f) & 0xFFFFu);
       }
-#pragma unroll
-      for (int c = 0; c < 8; ++c) tile[hl + c][r] = acc[c];
     }
     __syncthreads();
   }
   if constexpr (VEC) {
-    const int c0 = (tid & 7) * 8;
-    if (c0 >= nv) return;
-    for (int r = tid >> 3; r < nh; r += 32) {
-      float v[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-      if (!empty) {
+    constexpr int W = GF32 ? 4 : 8, kPer = kStrip / W;  // values a thread, threads a row
+    const int c0 = tid % kPer * W;
+    if (c0 < nv) {
+      for (int r = tid / kPer; r < nh; r += 256 / kPer) {
+        const int64_t at = (h0 + r) * a.Vs + v0 + c0;
+        if constexpr (TF32) {
+          float v[W] = {};
+          if (any) {
 #pragma unroll
-        for (int c = 0; c < 8; ++c) v[c] = tile[r][c0 + c];
-      }
-      const int64_t at = (h0 + r) * a.Vs + v0 + c0;
-      if constexpr (ACC) {
-        float old[8];
-        load8<GF32>(a.out, at, old);
+            for (int c = 0; c < W; ++c) v[c] = tile[r * kPitch + c0 + c];
+          }
+          if constexpr (ACC) {
+            float old[W];
+            load_w<GF32, W>(a.out, at, old);
 #pragma unroll
-        for (int c = 0; c < 8; ++c) v[c] += old[c];
+            for (int c = 0; c < W; ++c) v[c] += old[c];
+          }
+          store_w<GF32, W>(a.out, at, v);
+        } else {
+          eu32x4 v = eu32x4{0u, 0u, 0u, 0u};
+          if (any) {
+            const uint32_t* q = reinterpret_cast<const uint32_t*>(tile + r * kPitch + c0);
+#pragma unroll
+            for (int c = 0; c < 4; ++c) v[c] = q[c];
+          }
+          stream(reinterpret_cast<eu32x4*>(static_cast<uint16_t*>(a.out) + at), v);
+        }
       }
-      store8<GF32>(a.out, at, v);
     }
   } else {
     const int c = tid & 63;
-    if (c >= nv) return;
-    for (int r = tid >> 6; r < nh; r += 4) {
-      float v = empty ? 0.f : tile[r][c];
-      const int64_t at = (h0 + r) * a.Vs + v0 + c;
-      if constexpr (GF32) {
-        float* o = static_cast<float*>(a.out) + at;
-        *o = ACC ? v + *o : v;
-      } else {
-        uint16_t* o = static_cast<uint16_t*>(a.out) + at;
-        if constexpr (ACC) v += bf16_lo(*o);
-        *o = (uint16_t)(bf16_pair(v, 0.f) & 0xFFFFu);
+    if (c < nv) {
+      for (int r = tid >> 6; r < nh; r += 4) {
+        const int64_t at = (h0 + r) * a.Vs + v0 + c;
+        const T v = any ? tile[r * kPitch + c] : (T)0;
+        if constexpr (GF32) {
+          float* o = static_cast<float*>(a.out) + at;
+          *o = ACC ? v + *o : v;
+        } else {
+          uint16_t* o = static_cast<uint16_t*>(a.out) + at;
+          if constexpr (ACC)
+            *o = (uint16_t)(bf16_pair(v + bf16_lo(*o), 0.f) & 0xFFFFu);
+          else
+            *o = v;
+        }
       }
     }
   }

@@ -233,16 +233,12 @@ flce_status_t sort_tokens(const TokenArgs& t, const EmbedPlan& p, void* ws, int3
   const SortPlan& s = p.sort;
   *key = k1;
   *perm = p1;
-  if (t.N == 0) return clear_header(t, st);
-  if (s.one_block) {
+  if (s.by_rank) {
+    // Without a token one block still writes the header.
+    const int64_t groups = ceil_div(t.N, kRankItems);
+    const size_t lds = 4 * (size_t)groups * kRankItems;
     return launch(K_EMBED_SORT, st, [&] {
-      const int threads = 64 * kSortWaves;
-      if (t.N <= threads)
-        embed_sort_block_kernel<1><<<1, threads, 0, st>>>(t, s.passes, s.bits, k1, p1);
-      else if (t.N <= 4 * threads)
-        embed_sort_block_kernel<4><<<1, threads, 0, st>>>(t, s.passes, s.bits, k1, p1);
-      else
-        embed_sort_block_kernel<16><<<1, threads, 0, st>>>(t, s.passes, s.bits, k1, p1);
+      embed_rank_kernel<<<(unsigned)(groups > 0 ? groups : 1), kRankThreads, lds, st>>>(t, k1, p1);
     });
   }
   int32_t* k2 = reinterpret_cast<int32_t*>(wsp(ws, p.key2));
@@ -276,18 +272,28 @@ flce_status_t sort_tokens(const TokenArgs& t, const EmbedPlan& p, void* ws, int3
   return FLCE_OK;
 }
 
-// Threads that share a row of H values, eight each: a power of two.
-int row_threads(int64_t H) {
+// Lanes that share a row of H values, eight each.
+int row_lanes(int64_t H) {
   int t = 8;
-  while (t < 256 && (int64_t)t * 8 < H) t <<= 1;
+  while (t < 64 && (int64_t)t * 8 < H) t <<= 1;
   return t;
 }
 
+// Hidden values a block of the gradient takes, of `unit` at a time: all of them, or
+// as few as it takes to give every CU four blocks.
+int64_t grad_range(int64_t H, int64_t unit, int64_t blocks) {
+  const int64_t units = ceil_div(H, unit);
+  int64_t parts = ceil_div(4 * kNumCUs, blocks);
+  if (parts > units) parts = units;
+  return ceil_div(units, parts) * unit;
+}
+
 template <bool HF32, bool GF32, bool ACC>
-void launch_grad(const GradArgs& a, int layout, hipStream_t st) {
+void launch_grad(GradArgs a, int layout, hipStream_t st) {
   if (layout == FLCE_EMBED_VH) {
-    const int64_t rows = (int64_t)(256 / a.tpr) * kGradRows;
-    const dim3 grid((unsigned)ceil_div(a.Vs, rows), (unsigned)ceil_div(a.H, (int64_t)a.tpr * 8));
+    const int64_t blocks = ceil_div(a.Vs, kGradRows);
+    a.range = grad_range(a.H, (int64_t)a.lanes * (GF32 ? 4 : 8), blocks);
+    const dim3 grid((unsigned)blocks, (unsigned)ceil_div(a.H, a.range));
     embed_grad_rows_kernel<HF32, GF32, ACC><<<grid, 256, 0, st>>>(a);
     return;
   }
@@ -341,20 +347,21 @@ flce_status_t flce_embedding_forward(const void* weight, const int64_t* tokens, 
       a.key = key;
       a.perm = perm;
     } else {
-      a.count_block = 1;
+      a.count_block = 1;  // one more block row, whose first block counts the tokens
     }
-    const dim3 grid((unsigned)(ceil_div(N, kGatherTokens) + a.count_block),
-                    (unsigned)ceil_div(H, 64));
+    const int64_t blocks = ceil_div(N, kGatherTokens) + a.count_block;
+    const dim3 grid((unsigned)(ceil_div(H, 64 * 8) * 8),
+                    (unsigned)(blocks < kGatherGridY ? blocks : kGatherGridY),
+                    (unsigned)ceil_div(blocks, kGatherGridY));
     return launch(K_EMBED_GATHER, st, [&] { embed_gather_cols_kernel<<<grid, 256, 0, st>>>(a); });
   }
   // One more block counts the tokens of a small batch beside the copy; in a
   // large one every block counts its own.
   a.count_block = N <= kCountBlockTokens ? 1 : 0;
   if (a.count_block == 0) FLCE_TRY(clear_header(a.t, st));
-  a.tpr = row_threads(H);
-  const int64_t rows = (int64_t)(256 / a.tpr) * kGatherRows;
-  const dim3 grid((unsigned)(ceil_div(N, rows) + a.count_block),
-                  (unsigned)ceil_div(H, (int64_t)a.tpr * 8));
+  a.lanes = row_lanes(H);
+  const dim3 grid((unsigned)(ceil_div(N, 4 * (64 / a.lanes)) + a.count_block),
+                  (unsigned)ceil_div(H, (int64_t)a.lanes * 8 * kGatherLoads));
   return launch(K_EMBED_GATHER, st, [&] { embed_gather_rows_kernel<<<grid, 256, 0, st>>>(a); });
 }
 
@@ -372,6 +379,7 @@ flce_status_t flce_embedding_backward(const void* grad_hidden, const int64_t* to
   if (workspace_bytes < p.b_total) return FLCE_ERR_WORKSPACE_TOO_SMALL;
   hipStream_t st = static_cast<hipStream_t>(stream);
   const TokenArgs t = token_args(tokens, N, Vs, v_begin, V_total, opt->ignore_index, workspace);
+  int32_t* strips = reinterpret_cast<int32_t*>(wsp(workspace, p.strips));
   int32_t *key, *perm;
   FLCE_TRY(sort_tokens(t, p, workspace, &key, &perm, st));
   GradArgs a{};
@@ -379,20 +387,20 @@ flce_status_t flce_embedding_backward(const void* grad_hidden, const int64_t* to
   a.key = key;
   a.perm = perm;
   a.header = t.header;
-  a.starts = reinterpret_cast<int32_t*>(wsp(workspace, p.starts));
+  a.strips = strips;
   a.part = reinterpret_cast<float*>(wsp(workspace, p.part));
   a.N = N;
   a.H = H;
   a.Vs = Vs;
   a.scale = (float)opt->scale;
   a.out = grad_weight;
-  a.tpr = row_threads(H);
+  a.lanes = row_lanes(H);
   const bool hf = opt->hidden_dtype == FLCE_GRAD_F32, gf = opt->grad_dtype == FLCE_GRAD_F32;
   const bool acc = opt->accumulate != 0;
-  const int threads = a.tpr < 64 ? 64 : a.tpr;
-  a.start_blocks = (int)ceil_div(Vs + 1, threads);
-  a.chunks = (int)ceil_div(H, (int64_t)threads * 8);
-  const int64_t blocks = a.start_blocks + ceil_div(N, kPiece) * a.chunks;
+  const int threads = H <= 256 ? 64 : (H <= 512 ? 128 : 256);
+  a.strip_blocks = (int)ceil_div(ceil_div(Vs, kStrip) + 1, threads);
+  a.chunks = (int)ceil_div(H, (int64_t)threads * 4);
+  const int64_t blocks = a.strip_blocks + ceil_div(N, kPiece) * a.chunks;
   FLCE_TRY(launch(K_EMBED_SEGMENTS, st, [&] {
     if (hf)
       embed_segments_kernel<true><<<(unsigned)blocks, threads, 0, st>>>(a);

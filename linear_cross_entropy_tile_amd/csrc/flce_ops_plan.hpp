@@ -135,7 +135,8 @@ inline bool aligned_to(const void* p, size_t a) { return ((uintptr_t)p & (a - 1)
 // ---- embedding --------------------------------------------------------------------
 
 constexpr int kPiece = 32;                    // sorted positions a piece; longer runs are split
-constexpr int64_t kSortOneBlock = 16384;      // tokens that one block sorts in LDS
+constexpr int kStrip = 64;                    // rows (ids) a block of the gradient takes
+constexpr int64_t kRankTokens = 16384;        // tokens sorted by counting every place
 constexpr int kSortTile = 4096;               // tokens a block of the larger sort takes
 constexpr int kMaxDigitBits = 11;
 
@@ -144,15 +145,14 @@ constexpr int kMaxDigitBits = 11;
 struct SortPlan {
   int passes, bits;     // digit passes of `bits` bits each
   int64_t tiles;        // blocks of the larger sort
-  bool one_block;
+  bool by_rank;
 };
 inline SortPlan make_sort_plan(int64_t N, int64_t Vs) {
   SortPlan s{};
   int total = 1;
   while (((int64_t)1 << total) <= Vs) ++total;  // the keys 0 .. Vs
-  s.one_block = N <= kSortOneBlock;
-  const int digit = s.one_block ? 9 : kMaxDigitBits;
-  s.passes = (total + digit - 1) / digit;
+  s.by_rank = N <= kRankTokens;
+  s.passes = (total + kMaxDigitBits - 1) / kMaxDigitBits;
   s.bits = (total + s.passes - 1) / s.passes;
   s.tiles = ceil_div(N, kSortTile);
   return s;
@@ -162,7 +162,7 @@ struct EmbedPlan {
   SortPlan sort;
   bool sorted;          // the forward gathers in sorted order
   size_t key, perm, key2, perm2, counts, totals;  // sort
-  size_t starts;        // backward: first sorted position of every row, [Vs + 1]
+  size_t strips;        // backward: first sorted position of every strip, [strips + 1]
   size_t part;          // backward: sums of split runs, [2 * pieces, H] fp32
   size_t f_total, b_total;
 };
@@ -183,14 +183,14 @@ inline EmbedPlan make_embed_plan(int64_t N, int64_t H, int64_t Vs, int layout) {
   };
   take(p.key, 4 * (size_t)N);
   take(p.perm, 4 * (size_t)N);
-  if (!p.sort.one_block) {
+  if (!p.sort.by_rank) {
     take(p.key2, 4 * (size_t)N);
     take(p.perm2, 4 * (size_t)N);
     take(p.counts, 4 * ((size_t)p.sort.tiles << p.sort.bits));
     take(p.totals, (size_t)4 << p.sort.bits);
   }
   p.f_total = p.sorted ? off : kHeaderBytes;
-  take(p.starts, 4 * ((size_t)Vs + 1));
+  take(p.strips, 4 * ((size_t)ceil_div(Vs, kStrip) + 1));
   take(p.part, 4 * 2 * (size_t)ceil_div(N, kPiece) * (size_t)H);
   p.b_total = off;
   return p;
