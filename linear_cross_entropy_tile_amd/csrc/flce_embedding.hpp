@@ -15,7 +15,8 @@
 // runs longer than kPiece positions are cut at multiples of kPiece, the pieces
 // summed in parallel to fp32 rows, and those summed in order by the row's owner.
 // At most two split runs overlap a piece (the one that comes in and the one that
-// goes out), so 2 rows a piece hold them.
+// goes out), so 2 rows a piece hold them. In large batches the sums of kPieces2
+// consecutive pieces inside one run are added up once more.
 //
 // What bounds them: the bytes (the lookup its output and the distinct rows, the
 // gradient the write of all of dE), and for small batches the sort's latency.
@@ -126,20 +127,25 @@ __device__ __forceinline__ int block_sum_int(int v, int* sh) {
   return r;
 }
 
-// One block: the header's counts.
+// One block: the header's count of invalid tokens.
 __device__ __forceinline__ void count_tokens(const TokenArgs& a, int* sh) {
-  int inv = 0, n = 0;
-  for (int64_t i = threadIdx.x; i < a.N; i += blockDim.x) {
-    bool bad;
-    n += token_key(a, a.tokens[i], bad) < a.Vs ? 1 : 0;
-    inv += bad ? 1 : 0;
+  int inv = 0;
+  for (int64_t i0 = threadIdx.x; i0 < a.N; i0 += 8 * blockDim.x) {
+    int64_t x[8];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      const int64_t i = i0 + (int64_t)j * blockDim.x;
+      x[j] = i < a.N ? a.tokens[i] : a.ignore_index;
+    }
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      bool bad;
+      (void)token_key(a, x[j], bad);
+      inv += bad ? 1 : 0;
+    }
   }
   inv = block_sum_int(inv, sh);
-  n = block_sum_int(n, sh);
-  if (threadIdx.x == 0) {
-    a.header[0] = inv;
-    a.header[1] = n;
-  }
+  if (threadIdx.x == 0) a.header[0] = inv;
 }
 
 __global__ void __launch_bounds__(64) embed_clear_kernel(int32_t* header) {
@@ -270,8 +276,8 @@ struct SortArgs {
   TokenArgs t;
   const int32_t *key_in, *perm_in;  // null: from the tokens
   int32_t *key_out, *perm_out;
-  int32_t* counts;                  // [digit][tile]
-  int64_t tiles;
+  int32_t* counts;                  // [digit][tile], rows `pitch` apart
+  int64_t pitch;
   int shift, bits;
 };
 
@@ -302,7 +308,7 @@ __global__ void __launch_bounds__(256) embed_sort_count_kernel(SortArgs a) {
     }
   }
   __syncthreads();
-  for (int d = threadIdx.x; d < nd; d += 256) a.counts[d * a.tiles + blockIdx.x] = hist[d];
+  for (int d = threadIdx.x; d < nd; d += 256) a.counts[d * a.pitch + blockIdx.x] = hist[d];
   if (a.key_in == nullptr) {
     inv = block_sum_int(inv, sh);
     n = block_sum_int(n, sh);
@@ -313,24 +319,32 @@ __global__ void __launch_bounds__(256) embed_sort_count_kernel(SortArgs a) {
   }
 }
 
-// A wave a digit: counts[d][*] becomes its exclusive prefix over the tiles, the
-// digit's total goes to totals[d].
+// A wave a digit, four tiles a lane: counts[d][*] becomes its exclusive prefix over
+// the tiles, the digit's total goes to totals[d]. Rows are padded to four tiles.
 __global__ void __launch_bounds__(256) embed_sort_scan_kernel(int32_t* counts, int64_t tiles,
-                                                              int nd, int32_t* totals) {
+                                                              int64_t pitch, int nd,
+                                                              int32_t* totals) {
+  typedef int32_t i32x4 __attribute__((ext_vector_type(4)));
   const int lane = threadIdx.x & 63;
   const int d = blockIdx.x * 4 + (threadIdx.x >> 6);
   if (d >= nd) return;
-  int32_t* c = counts + d * tiles;
   int run = 0;
-  for (int64_t t0 = 0; t0 < tiles; t0 += 64) {
-    const int64_t t = t0 + lane;
-    const int v = t < tiles ? c[t] : 0;
-    int x = v;
+  for (int64_t t0 = 0; t0 < tiles; t0 += 256) {
+    const int64_t t = t0 + lane * 4;
+    i32x4* c = reinterpret_cast<i32x4*>(counts + d * pitch + t);
+    i32x4 v = {0, 0, 0, 0};
+    if (t < tiles) v = *c;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) v[k] = t + k < tiles ? v[k] : 0;
+    const int sum = v[0] + v[1] + v[2] + v[3];
+    int x = sum;
     for (int s = 1; s < 64; s <<= 1) {
       const int y = __shfl_up(x, s, 64);
       if (lane >= s) x += y;
     }
-    if (t < tiles) c[t] = run + x - v;
+    const int before = run + x - sum;
+    if (t < tiles)
+      *c = i32x4{before, before + v[0], before + v[0] + v[1], before + v[0] + v[1] + v[2]};
     run += __shfl(x, 63, 64);
   }
   if (lane == 0) totals[d] = run;
@@ -358,7 +372,7 @@ __global__ void __launch_bounds__(64 * kSortMoveWaves) embed_sort_move_kernel(So
 #pragma unroll
   for (int q = 0; q < kPer; ++q) {
     const int d = threadIdx.x * kPer + q;
-    if (d < nd) base[d] = off + a.counts[d * a.tiles + blockIdx.x];
+    if (d < nd) base[d] = off + a.counts[d * a.pitch + blockIdx.x];
     off += t[q];
   }
   __syncthreads();
@@ -403,7 +417,7 @@ struct GatherArgs {
   int64_t H;
   float scale;
   uint16_t* out;
-  int count_block;            // 1: the last block of grid.x fills the header
+  int count_block;            // 1: one more block counts the invalid tokens
   int lanes;                  // lanes a row (table lookup): a power of two, 8 to 64
 };
 
@@ -423,13 +437,13 @@ __device__ __forceinline__ eu32x4 scaled8(const eu32x4& w, float scale) {
 
 __global__ void __launch_bounds__(256) embed_gather_rows_kernel(GatherArgs a) {
   __shared__ int sh[4];
-  if (a.count_block != 0 && blockIdx.x == gridDim.x - 1) {
+  if (a.count_block != 0 && blockIdx.x == 0) {
     if (blockIdx.y == 0) count_tokens(a.t, sh);
     return;
   }
   const int lane = threadIdx.x & 63, w = threadIdx.x >> 6;
   const int side = 64 / a.lanes;  // rows a wave takes side by side
-  const int64_t i = ((int64_t)blockIdx.x * 4 + w) * side + lane / a.lanes;
+  const int64_t i = ((int64_t)(blockIdx.x - a.count_block) * 4 + w) * side + lane / a.lanes;
   const int k = lane & (a.lanes - 1);
   bool bad = false;
   const bool on = i < a.t.N;
@@ -508,6 +522,7 @@ struct GradArgs {
   const int32_t* header;      // [1] tokens of the slice: the sorted positions that count
   int32_t* strips;            // [strips + 1] first sorted position of every strip of 64 rows
   float* part;                // [2 * pieces][H]
+  float* part2;               // [large pieces][H], or null
   int64_t N, H, Vs;
   float scale;
   void* out;
@@ -557,6 +572,12 @@ __device__ __forceinline__ void add_rows(const GradArgs& a, int64_t b, int64_t e
   }
 }
 
+// Whether the run [b, e) has a sum of the kPieces2 pieces from p on.
+__device__ __forceinline__ bool large_piece(const GradArgs& a, int64_t p, int64_t b, int64_t e) {
+  return a.part2 != nullptr && p % kPieces2 == 0 && p * kPiece >= b &&
+         (p + kPieces2) * kPiece <= e;
+}
+
 // The sum of the run [b, e): directly, or from its pieces' sums.
 template <bool HF32, int W, int U, int DEEP>
 __device__ __forceinline__ void run_sum(const GradArgs& a, int64_t b, int64_t e, int lanes, int k,
@@ -576,27 +597,30 @@ __device__ __forceinline__ void run_sum(const GradArgs& a, int64_t b, int64_t e,
     for (int u = 0; u < U; ++u) load_w<true, W>(a.part, (2 * p + 1) * a.H + h[u], acc[u]);
     ++p;
   }
-  for (; p + DEEP <= p1 + 1; p += DEEP) {
+  while (p <= p1) {
+    // The next DEEP rows, large or small.
     float v[DEEP][U][W];
 #pragma unroll
-    for (int d = 0; d < DEEP; ++d)
+    for (int d = 0; d < DEEP; ++d) {
+      if (p > p1) {
 #pragma unroll
-      for (int u = 0; u < U; ++u) load_w<true, W>(a.part, 2 * (p + d) * a.H + h[u], v[d][u]);
+        for (int u = 0; u < U; ++u)
+#pragma unroll
+          for (int q = 0; q < W; ++q) v[d][u][q] = 0.f;
+        continue;
+      }
+      const bool large = large_piece(a, p, b, e);
+      const float* row = large ? a.part2 + p / kPieces2 * a.H : a.part + 2 * p * a.H;
+#pragma unroll
+      for (int u = 0; u < U; ++u) load_w<true, W>(row, h[u], v[d][u]);
+      p += large ? kPieces2 : 1;
+    }
 #pragma unroll
     for (int d = 0; d < DEEP; ++d)
 #pragma unroll
       for (int u = 0; u < U; ++u)
 #pragma unroll
         for (int q = 0; q < W; ++q) acc[u][q] += v[d][u][q];
-  }
-  for (; p <= p1; ++p) {
-    float v[U][W];
-#pragma unroll
-    for (int u = 0; u < U; ++u) load_w<true, W>(a.part, 2 * p * a.H + h[u], v[u]);
-#pragma unroll
-    for (int u = 0; u < U; ++u)
-#pragma unroll
-      for (int q = 0; q < W; ++q) acc[u][q] += v[u][q];
   }
 }
 
@@ -664,6 +688,28 @@ __global__ void __launch_bounds__(256) embed_segments_kernel(GradArgs a) {
     add_rows<HF32, 4, 1, 16>(a, qe - tail, qe, 64, lane, hc, acc);
     if (on) store_part(a, 2 * piece + 1, h, acc[0]);
   }
+}
+
+// One large piece and column chunk a block, if it lies inside one run: the pieces'
+// sums in order, 16 in flight.
+__global__ void __launch_bounds__(256) embed_large_pieces_kernel(GradArgs a) {
+  const int64_t n = a.header[1];
+  const int64_t q = blockIdx.x / a.chunks, p0 = q * kPieces2;
+  const int64_t b = p0 * kPiece, e = b + kPieces2 * kPiece;
+  const int64_t h = ((int64_t)(blockIdx.x % a.chunks) * blockDim.x + threadIdx.x) * 4;
+  if (e > n || a.key[b] != a.key[e - 1] || h >= a.H) return;
+  float acc[4] = {};
+#pragma unroll
+  for (int c = 0; c < kPieces2; c += 16) {
+    float v[16][4];
+#pragma unroll
+    for (int d = 0; d < 16; ++d) load_w<true, 4>(a.part, 2 * (p0 + c + d) * a.H + h, v[d]);
+#pragma unroll
+    for (int d = 0; d < 16; ++d)
+#pragma unroll
+      for (int k = 0; k < 4; ++k) acc[k] += v[d][k];
+  }
+  *reinterpret_cast<ef32x4*>(a.part2 + q * a.H + h) = ef32x4{acc[0], acc[1], acc[2], acc[3]};
 }
 
 // Rows of a table gradient [Vs,H]: a block takes kGradRows consecutive rows, whole

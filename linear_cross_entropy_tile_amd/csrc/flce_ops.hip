@@ -249,7 +249,7 @@ flce_status_t sort_tokens(const TokenArgs& t, const EmbedPlan& p, void* ws, int3
   SortArgs a{};
   a.t = t;
   a.counts = reinterpret_cast<int32_t*>(wsp(ws, p.counts));
-  a.tiles = s.tiles;
+  a.pitch = s.pitch;
   a.bits = s.bits;
   for (int pass = 0; pass < s.passes; ++pass) {
     a.shift = pass * s.bits;
@@ -261,7 +261,8 @@ flce_status_t sort_tokens(const TokenArgs& t, const EmbedPlan& p, void* ws, int3
       embed_sort_count_kernel<<<(int)s.tiles, 256, 0, st>>>(a);
     }));
     FLCE_TRY(launch(K_EMBED_SORT, st, [&] {
-      embed_sort_scan_kernel<<<(nd + 3) / 4, 256, 0, st>>>(a.counts, s.tiles, nd, totals);
+      embed_sort_scan_kernel<<<(nd + 3) / 4, 256, 0, st>>>(a.counts, s.tiles, s.pitch, nd,
+                                                           totals);
     }));
     FLCE_TRY(launch(K_EMBED_SORT, st, [&] {
       embed_sort_move_kernel<<<(int)s.tiles, 64 * kSortMoveWaves, 0, st>>>(a, totals);
@@ -355,9 +356,10 @@ flce_status_t flce_embedding_forward(const void* weight, const int64_t* tokens, 
                     (unsigned)ceil_div(blocks, kGatherGridY));
     return launch(K_EMBED_GATHER, st, [&] { embed_gather_cols_kernel<<<grid, 256, 0, st>>>(a); });
   }
-  // One more block counts the tokens of a small batch beside the copy; in a
-  // large one every block counts its own.
-  a.count_block = N <= kCountBlockTokens ? 1 : 0;
+  // One more block, the first, counts the invalid tokens beside the copy, which takes
+  // longer while the batch is small or the rows are long; otherwise every wave
+  // counts its own into a cleared header, a launch more (4 us).
+  a.count_block = N <= kCountBlockTokens || H >= kCountBlockHidden ? 1 : 0;
   if (a.count_block == 0) FLCE_TRY(clear_header(a.t, st));
   a.lanes = row_lanes(H);
   const dim3 grid((unsigned)(ceil_div(N, 4 * (64 / a.lanes)) + a.count_block),
@@ -407,6 +409,13 @@ flce_status_t flce_embedding_backward(const void* grad_hidden, const int64_t* to
     else
       embed_segments_kernel<false><<<(unsigned)blocks, threads, 0, st>>>(a);
   }));
+  const int64_t large = p.large_pieces;
+  if (large > 0) {
+    a.part2 = reinterpret_cast<float*>(wsp(workspace, p.part2));
+    FLCE_TRY(launch(K_EMBED_SEGMENTS, st, [&] {
+      embed_large_pieces_kernel<<<(unsigned)(large * a.chunks), threads, 0, st>>>(a);
+    }));
+  }
   return launch(K_EMBED_GRAD, st, [&] {
     switch ((hf ? 4 : 0) + (gf ? 2 : 0) + (acc ? 1 : 0)) {
       case 0: launch_grad<false, false, false>(a, opt->layout, st); break;

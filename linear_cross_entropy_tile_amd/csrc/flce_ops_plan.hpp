@@ -135,16 +135,19 @@ inline bool aligned_to(const void* p, size_t a) { return ((uintptr_t)p & (a - 1)
 // ---- embedding --------------------------------------------------------------------
 
 constexpr int kPiece = 32;                    // sorted positions a piece; longer runs are split
+// Batches sorted by digits sum this many consecutive pieces of one run once more
+// (a launch of 4 us; a run of 10 % of 2^21 tokens has 6500 pieces).
+constexpr int kPieces2 = 32;
 constexpr int kStrip = 64;                    // rows (ids) a block of the gradient takes
 constexpr int64_t kRankTokens = 16384;        // tokens sorted by counting every place
-constexpr int kSortTile = 4096;               // tokens a block of the larger sort takes
+constexpr int kSortTile = 1024;               // tokens a block of the larger sort takes
 constexpr int kMaxDigitBits = 11;
 
 // The sort: keys are the token's row in the slice, or Vs for a token that takes
 // no part, so that these come last.
 struct SortPlan {
   int passes, bits;     // digit passes of `bits` bits each
-  int64_t tiles;        // blocks of the larger sort
+  int64_t tiles, pitch; // blocks of the larger sort, and their counts' row length
   bool by_rank;
 };
 inline SortPlan make_sort_plan(int64_t N, int64_t Vs) {
@@ -155,6 +158,7 @@ inline SortPlan make_sort_plan(int64_t N, int64_t Vs) {
   s.passes = (total + kMaxDigitBits - 1) / kMaxDigitBits;
   s.bits = (total + s.passes - 1) / s.passes;
   s.tiles = ceil_div(N, kSortTile);
+  s.pitch = ceil_div(s.tiles, 4) * 4;
   return s;
 }
 
@@ -164,13 +168,21 @@ struct EmbedPlan {
   size_t key, perm, key2, perm2, counts, totals;  // sort
   size_t strips;        // backward: first sorted position of every strip, [strips + 1]
   size_t part;          // backward: sums of split runs, [2 * pieces, H] fp32
+  int64_t large_pieces; // and of whole groups of kPieces2 pieces, [large_pieces, H]
+  size_t part2;
   size_t f_total, b_total;
 };
 
-// Lookups of up to this many tokens from a table count them in one block.
+// Lookups from a table of up to this many tokens, or of rows this long, count the
+// invalid tokens in one block: it takes 0.8 ns a token, the copy 1.6 ns or more a
+// token from this row length on.
 constexpr int64_t kCountBlockTokens = 8192;
-// Lookups of fewer tokens from an [H,V] weight gather in token order.
-constexpr int64_t kGatherSorted = 512;
+constexpr int64_t kCountBlockHidden = 2048;
+// Lookups of fewer tokens from an [H,V] weight gather in token order: a sort and a
+// sorted gather of 2048 tokens took 37 us (frequent ids) and 102 us (all different)
+// at H = 2304, V = 256000, the gather alone 34 and 104; of 4096, 61 and 165 against
+// 63 and 201; of 1024, 19 and 59 against 17 and 55.
+constexpr int64_t kGatherSorted = 2048;
 
 inline EmbedPlan make_embed_plan(int64_t N, int64_t H, int64_t Vs, int layout) {
   EmbedPlan p{};
@@ -186,12 +198,14 @@ inline EmbedPlan make_embed_plan(int64_t N, int64_t H, int64_t Vs, int layout) {
   if (!p.sort.by_rank) {
     take(p.key2, 4 * (size_t)N);
     take(p.perm2, 4 * (size_t)N);
-    take(p.counts, 4 * ((size_t)p.sort.tiles << p.sort.bits));
+    take(p.counts, 4 * ((size_t)p.sort.pitch << p.sort.bits));
     take(p.totals, (size_t)4 << p.sort.bits);
   }
   p.f_total = p.sorted ? off : kHeaderBytes;
   take(p.strips, 4 * ((size_t)ceil_div(Vs, kStrip) + 1));
   take(p.part, 4 * 2 * (size_t)ceil_div(N, kPiece) * (size_t)H);
+  p.large_pieces = p.sort.by_rank ? 0 : N / (kPiece * kPieces2);
+  take(p.part2, 4 * (size_t)p.large_pieces * (size_t)H);
   p.b_total = off;
   return p;
 }

@@ -46,7 +46,8 @@ FORWARD = [(0, 8, 5, "all"), (1, 8, 1, "all"), (1, 2304, 1001, "all"), (31, 72, 
            (300, 64, 999, "holes"), (511, 200, 640, "all"), (512, 200, 641, "holes"),
            (1025, 136, 4096, "hot"), (4100, 64, 777, "holes"), (9000, 40, 5000, "hot"),
            (16384, 8, 70000, "all"), (20001, 24, 300, "holes"), (33000, 16, 300000, "holes"),
-           (700, 4104, 513, "holes")]
+           (700, 4104, 513, "holes"), (2047, 136, 600, "hot"), (2048, 136, 601, "holes"),
+           (3000, 72, 4000, "all")]
 
 
 @pytest.mark.parametrize("layout", ["hv", "vh"])
@@ -86,7 +87,7 @@ BACKWARD = [(0, 8, 5, "all"), (1, 8, 1, "all"), (33, 16, 1, "same"), (32, 16, 1,
             (31, 72, 7, "holes"), (64, 8, 3, "same"), (65, 136, 130, "same"),
             (300, 192, 1001, "holes"), (1025, 136, 192, "hot"), (3000, 64, 65, "hot"),
             (9000, 40, 5000, "hot"), (16385, 8, 700, "holes"), (40000, 16, 70001, "hot"),
-            (520, 4104, 72, "hot"), (2048, 264, 8, "same")]
+            (520, 4104, 72, "hot"), (2048, 264, 8, "same"), (30000, 24, 9, "same"), (50000, 16, 40, "hot")]
 
 
 def _check_grad(got, tok, g, V, scale, layout, dtype, base=None):
@@ -197,7 +198,7 @@ def test_slices_make_the_whole(layout):
 
 
 @pytest.mark.parametrize("layout", ["hv", "vh"])
-@pytest.mark.parametrize("N", [40, 700, 17000])
+@pytest.mark.parametrize("N", [40, 2500, 17000])
 def test_captured_calls_replay(layout, N):
     """Two captured calls that share a workspace, replayed with other inputs
     and eager work between."""
