@@ -285,6 +285,8 @@ struct LossArgs {
   int64_t items;                // sequences, or pairs
   int64_t tiles;
   int rows;                     // of 64 tokens a tile: 1 or kLossRows
+  int deferred;                 // blocks whose totals the gradients kernel adds up; 0: the
+                                // batch is finished before it
   typename Loss::Share* parts;    // [B + tiles]
   typename Loss::Share* seq_sum;  // [B]
   typename Loss::Total* totals;   // [blocks of the sequences kernel]
@@ -424,12 +426,16 @@ struct PolicyLoss {
     tot.inv += v.inv;
     tot.bad += v.bad;
   }
+  // The batch's factor, from its counts.
+  __device__ static double factor(const LossArgs<PolicyLoss>& a, int n, int c, int bad) {
+    double k = 1.0;
+    if (a.in.reduction == FLCE_REDUCTION_MEAN) k = n > 0 ? 1.0 / n : 0.0;
+    if (a.in.reduction == FLCE_REDUCTION_SEQUENCE_MEAN) k = c > 0 ? 1.0 / c : 0.0;
+    return bad != 0 ? __builtin_nan("") : k;
+  }
   __device__ static void finish(const LossArgs<PolicyLoss>& a, const Total& v) {
     const In& in = a.in;
-    double k = 1.0;
-    if (in.reduction == FLCE_REDUCTION_MEAN) k = v.n > 0 ? 1.0 / v.n : 0.0;
-    if (in.reduction == FLCE_REDUCTION_SEQUENCE_MEAN) k = v.c > 0 ? 1.0 / v.c : 0.0;
-    if (v.bad != 0) k = __builtin_nan("");
+    const double k = factor(a, v.n, v.c, v.bad);
     a.state[2 * a.B] = k;
     a.state[2 * a.B + 1] = 0.0;
     float* s = a.out.stats;
@@ -446,10 +452,10 @@ struct PolicyLoss {
     s[6] = (float)v.n;
     s[7] = (float)v.c;
   }
-  // Upstream gradient times the batch's factor.
-  __device__ static double grad_scale(const LossArgs<PolicyLoss>& a) {
-    const double g = a.out.grad_loss != nullptr ? (double)a.out.grad_loss[0] : 1.0;
-    return g * a.state[2 * a.B];
+  __device__ static double state_factor(const LossArgs<PolicyLoss>& a) { return a.state[2 * a.B]; }
+  // The reduced loss's upstream gradient.
+  __device__ static double upstream(const LossArgs<PolicyLoss>& a) {
+    return a.out.grad_loss != nullptr ? (double)a.out.grad_loss[0] : 1.0;
   }
   __device__ static void grad(const LossArgs<PolicyLoss>& a, const Raw& r, double scale, int64_t t,
                               int64_t s) {
@@ -550,17 +556,21 @@ struct PreferenceLoss {
     tot.inv += c.inv + r.inv;
     tot.bad += c.bad + r.bad;
   }
+  __device__ static double factor(const LossArgs<PreferenceLoss>&, int, int, int bad) {
+    return bad != 0 ? __builtin_nan("") : 1.0;
+  }
   __device__ static void finish(const LossArgs<PreferenceLoss>& a, const Total& v) {
-    a.state[a.B] = v.bad != 0 ? __builtin_nan("") : 1.0;
+    a.state[a.B] = factor(a, v.n, v.c, v.bad);
     if (a.in.reduction != FLCE_REDUCTION_NONE) {
       const double k = a.in.reduction == FLCE_REDUCTION_MEAN && a.items > 0
                            ? 1.0 / (double)a.items : 1.0;
       a.out.loss[0] = (float)(k * v.x[0]);
     }
   }
-  __device__ static double grad_scale(const LossArgs<PreferenceLoss>& a) {
+  __device__ static double state_factor(const LossArgs<PreferenceLoss>& a) { return a.state[a.B]; }
+  __device__ static double upstream(const LossArgs<PreferenceLoss>& a) {
     const bool one = a.in.reduction != FLCE_REDUCTION_NONE && a.out.grad_loss != nullptr;
-    return (one ? (double)a.out.grad_loss[0] : 1.0) * a.state[a.B];
+    return one ? (double)a.out.grad_loss[0] : 1.0;
   }
   __device__ static void grad(const LossArgs<PreferenceLoss>& a, const Raw&, double scale,
                               int64_t t, int64_t s) {
@@ -752,6 +762,24 @@ __device__ __forceinline__ void finish_batch(const LossArgs<Loss>& a,
   }
 }
 
+// The batch's factor for the gradients, in every lane: from the state, or from the
+// counts of the blocks that step 2 left unadded (at most 64, one a lane).
+template <class Loss>
+__device__ __forceinline__ double batch_factor(const LossArgs<Loss>& a) {
+  if (a.deferred == 0) return Loss::state_factor(a);
+  const int lane = threadIdx.x & 63;
+  int n = 0, c = 0, bad = 0;
+  if (lane < a.deferred) {
+    n = a.totals[lane].n;
+    c = a.totals[lane].c;
+    bad = a.totals[lane].bad;
+  }
+  n = __builtin_amdgcn_readlane(wave_sum_dpp(n), 63);
+  c = __builtin_amdgcn_readlane(wave_sum_dpp(c), 63);
+  bad = __builtin_amdgcn_readlane(wave_sum_dpp(bad), 63);
+  return Loss::factor(a, n, c, bad);
+}
+
 // Step 3, one wave, one tile.
 template <class Loss, int ROWS>
 __device__ __forceinline__ void tile_grads(const LossArgs<Loss>& a, int64_t tile) {
@@ -760,7 +788,7 @@ __device__ __forceinline__ void tile_grads(const LossArgs<Loss>& a, int64_t tile
   TileRows<Loss, ROWS, Loss::kGradReads> in;
   in.load(a, t0);
   const TileSeqs r = tile_sequences(a.cu, a.B, a.N, t0, t1);
-  const double scale = Loss::grad_scale(a);
+  const double scale = Loss::upstream(a) * batch_factor(a);
 #pragma unroll
   for (int j = 0; j < ROWS; ++j) {
     const int tl = j * 64 + (threadIdx.x & 63);
@@ -779,8 +807,20 @@ __global__ void __launch_bounds__(64 * kLossWaves) loss_parts_kernel(LossArgs<Lo
   if (tile < a.tiles) tile_parts<Loss, ROWS>(a, tile);
 }
 
-// A block takes `per` items; the block that is done last adds up the blocks'
-// totals, in block order, and finishes the batch.
+// Adds up the totals of `blocks` blocks, in block order, and finishes the batch.
+template <class Loss>
+__device__ __forceinline__ void finish_blocks(const LossArgs<Loss>& a, int blocks,
+                                              typename Loss::Total* sh) {
+  typename Loss::Total t;
+  t.clear();
+  for (int b = threadIdx.x; b < blocks; b += blockDim.x) t.add(a.totals[b]);
+  t = block_total(t, (int)(blockDim.x >> 6), sh);
+  finish_batch(a, t);
+}
+
+// A block takes `per` items. With several blocks the one that is done last finishes
+// the batch, or the next kernel if that is there: passing on what other blocks
+// wrote within a launch costs 5 us of fences and round trips.
 template <class Loss>
 __global__ void __launch_bounds__(kSeqThreads) loss_sequences_kernel(LossArgs<Loss> a,
                                                                      int64_t per) {
@@ -791,6 +831,10 @@ __global__ void __launch_bounds__(kSeqThreads) loss_sequences_kernel(LossArgs<Lo
   const int64_t i1 = a.items - i0 < per ? a.items : i0 + per;
   Total t = sum_sequences(a, i0, i1);
   if (gridDim.x > 1) {
+    if (a.deferred != 0) {
+      if (threadIdx.x == 0) a.totals[blockIdx.x] = t;
+      return;
+    }
     if (threadIdx.x == 0) {
       a.totals[blockIdx.x] = t;
       __threadfence();
@@ -801,17 +845,18 @@ __global__ void __launch_bounds__(kSeqThreads) loss_sequences_kernel(LossArgs<Lo
     __syncthreads();
     if (last == 0) return;
     __threadfence();
-    t.clear();
-    for (int b = threadIdx.x; b < (int)gridDim.x; b += blockDim.x) t.add(a.totals[b]);
-    t = block_total(t, (int)(blockDim.x >> 6), sh);
+    finish_blocks(a, (int)gridDim.x, sh);
+    return;
   }
   finish_batch(a, t);
 }
 
 template <class Loss, int ROWS>
 __global__ void __launch_bounds__(64 * kLossWaves) loss_grads_kernel(LossArgs<Loss> a) {
+  __shared__ typename Loss::Total sh[kLossWaves];
   const int64_t tile = (int64_t)blockIdx.x * kLossWaves + (threadIdx.x >> 6);
   if (tile < a.tiles) tile_grads<Loss, ROWS>(a, tile);
+  if (a.deferred != 0 && blockIdx.x == 0) finish_blocks(a, a.deferred, sh);
 }
 
 // All three steps in one block, for small batches; the steps exchange their sums

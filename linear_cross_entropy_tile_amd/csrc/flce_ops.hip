@@ -56,6 +56,9 @@ flce_status_t run_loss(LossArgs<Loss>& a, const LossPlan& p, bool grads, void* w
     });
   }
   if (a.state == nullptr) a.state = reinterpret_cast<double*>(wsp(workspace, p.state));
+  // What the sequences kernel's blocks found is added up by the gradients kernel if
+  // there is one and a lane a block suffices.
+  a.deferred = grads && a.tiles > 0 && p.seq_blocks > 1 && p.seq_blocks <= 64 ? p.seq_blocks : 0;
   // At least one block, which readies the header for the next kernel.
   const int grid = (int)ceil_div(a.tiles > 0 ? a.tiles : 1, kLossWaves);
   FLCE_TRY(launch(K_LOSS_PARTS, st, [&] {

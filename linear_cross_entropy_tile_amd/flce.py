@@ -835,34 +835,34 @@ def embedding_backward(grad_hidden, tokens, vocab_size: int, layout: str = "hv",
     return grad_weight
 
 
-def _token_arrays(labels, cu_seqlens, arrays):
-    """Checks int64 [N] labels, int64 cu_seqlens (or None) and the fp32 arrays
-    ((name, tensor, size); None tensors skipped); returns the device."""
-    f32 = _torch().float32
-    dev = labels.device
-    if cu_seqlens is not None:
-        _check_devices(dev, ("cu_seqlens", cu_seqlens))
-    for name, t, size in arrays:
-        if t is None:
-            continue
-        _require(t, f32, 1, name)
-        if t.numel() != size:
-            raise ValueError(f"{name} must have {size} element(s)")
-        if t.device != dev:
-            raise ValueError(f"{name} must be on {dev}, got {t.device}")
-    return dev
+def _check_vector(t, dtype, size, index, name) -> None:
+    """``t`` must be a contiguous 1-d tensor of ``size`` elements on device
+    ``index`` (these calls are made once a step on small batches, where the
+    checks count)."""
+    try:
+        if (t.dtype is dtype and t.is_cuda and t.dim() == 1 and t.numel() == size
+                and t.is_contiguous() and t.get_device() == index):
+            return
+    except AttributeError:
+        pass
+    _require(t, dtype, 1, name)
+    if t.numel() != size:
+        raise ValueError(f"{name} must have {size} element(s)")
+    raise ValueError(f"{name} must be on cuda:{index}, got {t.device}")
 
 
 def _sequences(labels, cu_seqlens):
-    """(N, number of sequences) after checking both tensors."""
+    """(device, N, number of sequences) after checking both tensors."""
     torch = _torch()
     _require(labels, torch.int64, 1, "labels")
+    dev = labels.device
     if cu_seqlens is None:
-        return labels.shape[0], 1
+        return dev, labels.numel(), 1
     _require(cu_seqlens, torch.int64, 1, "cu_seqlens")
-    if cu_seqlens.shape[0] < 2:
+    _check_devices(dev, ("cu_seqlens", cu_seqlens))
+    if cu_seqlens.numel() < 2:
         raise ValueError("cu_seqlens must have one element more than there are sequences")
-    return labels.shape[0], cu_seqlens.shape[0] - 1
+    return dev, labels.numel(), cu_seqlens.numel() - 1
 
 
 def _policy_options(clip_low=0.2, clip_high=0.2, dual_clip=0.0, kl_coef=0.0, kl_estimator="k3",
@@ -880,19 +880,21 @@ def _policy_options(clip_low=0.2, clip_high=0.2, dual_clip=0.0, kl_coef=0.0, kl_
 def _policy_check(opt, logprob, labels, old_logprob, advantages, entropy, ref_logprob, cu_seqlens,
                   grad_loss):
     """(device, N, B) of a policy call, after checking its tensors."""
-    N, B = _sequences(labels, cu_seqlens)
-    for name, t in (("logprob", logprob), ("old_logprob", old_logprob),
-                    ("advantages", advantages)):
-        if t is None:
-            raise ValueError(f"{name} is required")
+    dev, N, B = _sequences(labels, cu_seqlens)
+    f32, index = _torch().float32, dev.index
     if opt.kl_coef != 0.0 and ref_logprob is None:
         raise ValueError("kl_coef needs ref_logprob")
     if opt.level == 1 and (cu_seqlens is None or not opt.advantages_per_sequence):
         raise ValueError("level 'sequence' needs cu_seqlens and advantages_per_sequence")
-    dev = _token_arrays(labels, cu_seqlens, (
-        ("logprob", logprob, N), ("old_logprob", old_logprob, N),
-        ("advantages", advantages, B if opt.advantages_per_sequence else N),
-        ("ref_logprob", ref_logprob, N), ("entropy", entropy, N), ("grad_loss", grad_loss, 1)))
+    _check_vector(logprob, f32, N, index, "logprob")
+    _check_vector(old_logprob, f32, N, index, "old_logprob")
+    _check_vector(advantages, f32, B if opt.advantages_per_sequence else N, index, "advantages")
+    if ref_logprob is not None:
+        _check_vector(ref_logprob, f32, N, index, "ref_logprob")
+    if entropy is not None:
+        _check_vector(entropy, f32, N, index, "entropy")
+    if grad_loss is not None:
+        _check_vector(grad_loss, f32, 1, index, "grad_loss")
     return dev, N, B
 
 
@@ -1002,14 +1004,18 @@ def _preference_check(opt, labels, cu_seqlens, grad_loss, arrays):
     (name, fp32 [N] tensor or None))."""
     if cu_seqlens is None:
         raise ValueError("cu_seqlens is required")
-    N, B = _sequences(labels, cu_seqlens)
+    dev, N, B = _sequences(labels, cu_seqlens)
     if B % 2 != 0:
         raise ValueError("cu_seqlens must hold an even number of sequences: the chosen ones, "
                          "then the rejected ones")
     P = B // 2
-    want = P if opt.reduction == FLCE_REDUCTION_NONE else 1
-    dev = _token_arrays(labels, cu_seqlens, [(name, t, N) for name, t in arrays]
-                        + [("grad_loss", grad_loss, want)])
+    f32, index = _torch().float32, dev.index
+    for name, t in arrays:
+        if t is not None:
+            _check_vector(t, f32, N, index, name)
+    if grad_loss is not None:
+        _check_vector(grad_loss, f32, P if opt.reduction == FLCE_REDUCTION_NONE else 1, index,
+                      "grad_loss")
     return dev, N, P
 
 

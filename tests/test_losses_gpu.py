@@ -48,6 +48,7 @@ LENGTHS = {
     "large_singles": ([1, 2, 0, 1] * 2600, 0, 3),
     "one_large": ([30000], 0, 0),
     "skewed": ([1] * 600 + [16000] + [2] * 300, 0, 0),
+    "many": ([1, 0] * 33500, 0, 0),
 }
 
 

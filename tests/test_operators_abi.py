@@ -149,8 +149,8 @@ def test_preference_rejects_outputs(which, kw, code):
 def test_workspace_sizes():
     opt = flce.FlceEmbeddingOptions(-100, 1.0, 1, 0, 0, 0)
     f, b = flce.flce_embedding_workspace_size(8192, 2304, 256000, opt)
-    # sorted keys and positions; row starts and the split runs' fp32 rows.
-    assert f >= 8 * 8192 and b >= f + 4 * 256001 + 8 * 256 * 2304
+    # sorted keys and positions; strip starts and the split runs' fp32 rows.
+    assert f >= 8 * 8192 and b >= f + 4 * 4001 + 8 * 256 * 2304
     assert flce.flce_embedding_workspace_size(0, 8, 1, opt)[0] >= 256
     assert flce.flce_policy_workspace_size(0, 1) >= 256
     assert flce.flce_policy_workspace_size(1 << 21, 1 << 21) >= 48 * 2 * (1 << 21)
