@@ -476,21 +476,20 @@ __global__ void __launch_bounds__(256) embed_gather_rows_kernel(GatherArgs a) {
 // hidden values; lane (t, g) gathers 8 values of token t down the rows 8 g .. and
 // stores them as 16 bytes, 128 contiguous bytes a token.
 constexpr int kGatherTokens = 32;  // tokens a block
-constexpr int kGatherGridY = 32768;
 
 __global__ void __launch_bounds__(256) embed_gather_cols_kernel(GatherArgs a) {
   __shared__ int sh[4];
-  if (a.count_block != 0 && blockIdx.y == gridDim.y - 1) {
-    if (blockIdx.x == 0) count_tokens(a.t, sh);
+  if (a.count_block != 0 && blockIdx.x >= gridDim.x - 8) {
+    if (blockIdx.x == gridDim.x - 8 && blockIdx.y == 0) count_tokens(a.t, sh);
     return;
   }
   const int lane = threadIdx.x & 63;
   // Blocks go to the 8 XCDs in turn, each with an L2 of its own. grid.x is a multiple
   // of 8, so a chunk of 64 rows of the weight stays with one XCD, and the tokens of
-  // a line, neighbours in the sorted order, find it in that L2.
-  const int64_t blk = (int64_t)blockIdx.z * kGatherGridY + blockIdx.y;
-  const int64_t i = blk * kGatherTokens + (threadIdx.x >> 6) * 8 + (lane & 7);
-  const int64_t h = (int64_t)blockIdx.x * 64 + (lane >> 3) * 8;
+  // a line, neighbours in the sorted order, find it in that L2; a chunk's tokens run
+  // one after another, within the same 64 rows' pages.
+  const int64_t i = (int64_t)(blockIdx.x >> 3) * kGatherTokens + (threadIdx.x >> 6) * 8 + (lane & 7);
+  const int64_t h = ((int64_t)blockIdx.y * 8 + (blockIdx.x & 7)) * 64 + (lane >> 3) * 8;
   if (i >= a.t.N || h >= a.H) return;
   bool bad;
   const int32_t key = a.key != nullptr ? a.key[i] : token_key(a.t, a.t.tokens[i], bad);
@@ -804,21 +803,27 @@ __global__ void __launch_bounds__(256) embed_grad_cols_kernel(GradArgs a) {
     // Added to what is there, -0 changes nothing, the sign of a zero included.
     for (int i = tid; i < kStripH * kPitch; i += 256) tile[i] = ACC ? (T)-0.f : (T)0;
     __syncthreads();
+    // The columns with a run, in order.
     const int lane = tid & 63;
-    const uint64_t mask = __builtin_amdgcn_ballot_w64(st[lane] < st[lane + 1]);
-    nu = __popcll(mask);
-    if (tid < 64 && ((mask >> lane) & 1) != 0) used[lanes_below(mask)] = (uint8_t)lane;
+#pragma unroll
+    for (int c = 0; c < kStrip; c += 64) {
+      const uint64_t mask = __builtin_amdgcn_ballot_w64(st[c + lane] < st[c + lane + 1]);
+      if (tid < 64 && ((mask >> lane) & 1) != 0)
+        used[nu + lanes_below(mask)] = (uint8_t)(c + lane);
+      nu += __popcll(mask);
+    }
     __syncthreads();
   }
   const int64_t h0 = (int64_t)blockIdx.y * kStripH;
   const int nh = a.H - h0 < kStripH ? (int)(a.H - h0) : kStripH;
   if (any) {
-    const int k = tid & 15, hl = k * 8;
-    for (int u = tid >> 4; u < nu; u += 16) {
+    constexpr int kLanes = kStripH / 8;  // lanes a run
+    const int k = tid % kLanes, hl = k * 8;
+    for (int u = tid / kLanes; u < nu; u += 256 / kLanes) {
       const int r = used[u];
       const int64_t h[1] = {hl < nh ? h0 + hl : a.H - 8};
       float sum[1][8];
-      run_sum<HF32, 8, 1, 4>(a, st[r], st[r + 1], 16, k, h, sum);
+      run_sum<HF32, 8, 1, 4>(a, st[r], st[r + 1], kLanes, k, h, sum);
       float acc[8];
 #pragma unroll
       for (int c = 0; c < 8; ++c) acc[c] = sum[0][c] * a.scale;
@@ -863,9 +868,9 @@ __global__ void __launch_bounds__(256) embed_grad_cols_kernel(GradArgs a) {
       }
     }
   } else {
-    const int c = tid & 63;
+    const int c = tid % kStrip;
     if (c < nv) {
-      for (int r = tid >> 6; r < nh; r += 4) {
+      for (int r = tid / kStrip; r < nh; r += 256 / kStrip) {
         const int64_t at = (h0 + r) * a.Vs + v0 + c;
         const T v = any ? tile[r * kPitch + c] : (T)0;
         if constexpr (GF32) {

@@ -351,12 +351,10 @@ flce_status_t flce_embedding_forward(const void* weight, const int64_t* tokens, 
       a.key = key;
       a.perm = perm;
     } else {
-      a.count_block = 1;  // one more block row, whose first block counts the tokens
+      a.count_block = 1;  // eight more blocks, the first of which counts
     }
     const int64_t blocks = ceil_div(N, kGatherTokens) + a.count_block;
-    const dim3 grid((unsigned)(ceil_div(H, 64 * 8) * 8),
-                    (unsigned)(blocks < kGatherGridY ? blocks : kGatherGridY),
-                    (unsigned)ceil_div(blocks, kGatherGridY));
+    const dim3 grid((unsigned)(8 * blocks), (unsigned)ceil_div(H, 64 * 8));
     return launch(K_EMBED_GATHER, st, [&] { embed_gather_cols_kernel<<<grid, 256, 0, st>>>(a); });
   }
   // One more block, the first, counts the invalid tokens beside the copy, which takes
