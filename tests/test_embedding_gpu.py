@@ -176,6 +176,28 @@ def test_gradients_of_infinite_rows_stay_in_their_column(layout):
 
 
 @pytest.mark.parametrize("layout", ["hv", "vh"])
+@pytest.mark.parametrize("N", [3000, 17000])
+def test_largest_vocabulary(layout, N):
+    """Ids up to the library's limit, through both sorts."""
+    V, H = (1 << 22) - 256, 8
+    g = torch.Generator(device="cuda")
+    g.manual_seed(1)
+    t = torch.randint(0, V, (N,), generator=g, device=G.dev())
+    t[:50] = V - 1
+    t[50:60] = 0
+    w = torch.randn(*((H, V) if layout == "hv" else (V, H)), generator=g, device=G.dev(),
+                    dtype=torch.bfloat16)
+    out = flce.embedding(w, t, layout=layout)["hidden"]
+    rows = w[:, t].t() if layout == "hv" else w[t]
+    assert torch.equal(out, rows)
+    # Whole numbers: their sums are exact in any order.
+    gr = torch.randint(-8, 9, (N, H), generator=g, device=G.dev()).float()
+    got = flce.embedding_backward(gr, t, V, layout=layout, grad_dtype="f32")
+    want = torch.zeros(V, H, device=G.dev()).index_add_(0, t, gr)
+    assert torch.equal(got, want.t() if layout == "hv" else want)
+
+
+@pytest.mark.parametrize("layout", ["hv", "vh"])
 def test_slices_make_the_whole(layout):
     rng = np.random.default_rng(7)
     N, H, V, cut = 900, 40, 203, 96
