@@ -24,12 +24,16 @@ namespace flce {
 constexpr int kLossTile = 256;        // tokens a wave takes at most
 constexpr int kLossRows = kLossTile / 64;
 constexpr int kLossWaves = 4;         // waves a block, parts and gradients kernels
-constexpr int kSmallWaves = 8;        // waves of the one-block kernel
+constexpr int kSmallWaves = 16;       // waves of the one-block kernel
 constexpr int kSeqThreads = 1024;     // threads a block, sequences kernel
 constexpr int64_t kMaxSeqBlocks = 512;
-// Batches up to these sizes take the one-block kernel.
-constexpr int64_t kSmallTokens = 4096;
-constexpr int64_t kSmallSequences = 1024;
+// Batches up to these sizes take the one-block kernel, at most two rounds of its 16
+// waves. Policy loss with gradients, kernels back to back: 512 tokens 7.8 us against
+// 11.2 in three launches, 1024 9.5 against 11.7; by itself, as such batches mostly
+// run, each launch has 3 to 5 us more (cold caches) and 2.5 us on the host. With
+// more tokens or sequences one block is too slow: 4000 tokens 33 us against 14.
+constexpr int64_t kSmallTokens = 2048;
+constexpr int64_t kSmallSequences = 256;
 constexpr int64_t kMaxSequences = (int64_t)1 << 21;
 
 // Workspace: header, shares [B + tiles], sequence sums [B], block totals, and

@@ -757,6 +757,11 @@ def _workspace(workspace, nbytes, dev):
     return torch.empty(max(nbytes, 256), dtype=torch.uint8, device=dev)
 
 
+@functools.lru_cache(maxsize=256)
+def _embedding_bytes(N, H, V, layout):
+    return flce_embedding_workspace_size(N, H, V, FlceEmbeddingOptions(0, 1.0, layout, 0, 0, 0))
+
+
 def _require_grad_dtype(t, name):
     torch = _torch()
     if not isinstance(t, torch.Tensor) or t.dtype not in (torch.bfloat16, torch.float32):
@@ -785,7 +790,7 @@ def embedding(weight, tokens, layout: str = "hv", scale: float = 1.0, ignore_ind
     N = tokens.shape[0]
     opt = FlceEmbeddingOptions(int(ignore_index), float(scale), lay, FLCE_GRAD_BF16,
                                FLCE_GRAD_BF16, 0)
-    nbytes, _ = flce_embedding_workspace_size(N, H, V, opt)
+    nbytes, _ = _embedding_bytes(N, H, V, lay)
     workspace = _workspace(workspace, nbytes, dev)
     hidden = torch.empty((N, H), dtype=torch.bfloat16, device=dev)
     _call(dev, "flce_embedding_forward", weight.data_ptr(), tokens.data_ptr(), N, H, V,
@@ -824,7 +829,7 @@ def embedding_backward(grad_hidden, tokens, vocab_size: int, layout: str = "hv",
             raise ValueError(f"grad_weight must be {list(shape)}")
     opt = FlceEmbeddingOptions(int(ignore_index), float(scale), lay, hdt, gdt,
                                1 if accumulate else 0)
-    _, nbytes = flce_embedding_workspace_size(N, H, V, opt)
+    _, nbytes = _embedding_bytes(N, H, V, lay)
     workspace = _workspace(workspace, nbytes, dev)
     if not accumulate:
         grad_weight = torch.empty(shape, device=dev, dtype=torch.float32 if gdt == FLCE_GRAD_F32

@@ -33,14 +33,19 @@ def _cu(lens, start=0):
 
 
 # Sequence lengths: empty ones, single tokens, tile borders (256), many in one
-# tile, one over many tiles, beyond the one-block kernel (8192), beyond one
-# block of sequences (4096); padding in front of and behind the sequences.
+# tile, one over many tiles, up to and beyond the one-block kernel (2048 tokens, 256
+# sequences), beyond one block of sequences, beyond 64 of them; padding in front of
+# and behind the sequences.
 LENGTHS = {
     "one": ([1], 0, 0),
     "empty": ([0, 0], 0, 0),
     "empty_between": ([0, 5, 0, 0, 250, 1, 0, 256, 0], 0, 0),
     "tile_borders": ([256, 255, 1, 257, 512, 1], 0, 0),
     "padded": ([60, 3, 200], 7, 40),
+    "small_mixed": ([1, 2, 0, 70, 1, 1, 64, 3, 0, 0, 90] * 4, 5, 9),
+    "small_singles": ([1] * 255 + [0], 1, 2),
+    "small_limit": ([2000], 10, 38),
+    "small_beyond": ([1700, 349], 0, 0),
     "singles": ([1] * 700, 3, 5),
     "long": ([5000], 0, 0),
     "ragged": ([900, 1, 33, 2500, 0, 700, 64], 0, 100),
@@ -281,7 +286,7 @@ def test_preference_extremes():
             assert np.all(np.abs(got - w) <= 2.0 ** -23 * np.abs(w) + 2.0 ** -148), (cfg, k)
 
 
-@pytest.mark.parametrize("name", ["ragged", "large"])
+@pytest.mark.parametrize("name", ["small_mixed", "ragged", "large"])
 def test_captured_calls_replay(name):
     """Captured policy and preference steps that share a workspace, replayed
     with other inputs and eager work between."""
@@ -330,7 +335,7 @@ def test_captured_calls_replay(name):
 
 
 def test_streams_match_alone():
-    xs = [_up(_inputs(n, 4)) for n in ("ragged", "large")]
+    xs = [_up(_inputs(n, 4)) for n in ("small_mixed", "large")]
 
     def step(x):
         args, kw = _policy_call(x, POLICY[1])
