@@ -19,8 +19,13 @@
 // keeps its digits at small x, and sums over 2^21 tokens lose nothing. Each
 // output is rounded once, to fp32.
 //
-// What bounds them: below some 10^5 tokens the launches (hence one launch for
-// everything in small batches, three otherwise); at 2^21 tokens the bytes.
+// What bounds them: below some 10^5 tokens the launches and each kernel's chain of
+// dependent loads (hence one launch for everything in small batches, three
+// otherwise); at 2^21 tokens the bytes, read twice because the batch's divisor is
+// not known before the last token, and the float64 exponentials. Measured on an
+// MI355X, policy loss with k3 KL, entropy and gradients: 413 tokens 8.1 us, 32768
+// tokens 14.4 us, 2.07 M tokens 50 us (75 MB of distinct inputs and outputs); pairs
+// without a reference, 2.07 M tokens, 24 us (33 MB).
 #pragma once
 
 #include <hip/hip_runtime.h>
@@ -608,7 +613,9 @@ struct TileRows {
 // wave once a sequence. With more, each row is scanned with the sequences as
 // segments, the open segment carried to the next row, and the lane with a
 // sequence's last token in the tile has its share. No LDS either way, so the
-// occupancy is the registers'.
+// occupancy is the registers'; token terms in LDS and sums over them took 36 us where
+// this takes 24 (policy loss, 2.07 M tokens in 1000 sequences: 58 MB, 2.4 TB/s).
+// 32768 tokens take 4.5 us.
 template <class Loss, int ROWS>
 __device__ __forceinline__ void tile_parts(const LossArgs<Loss>& a, int64_t tile) {
   using Token = typename Loss::Token;
@@ -691,7 +698,7 @@ __device__ __forceinline__ SeqParts seq_parts(const int64_t* cu, int64_t N, int 
 }
 
 // Step 2, one block, items [i0, i1): adds up the sequences' shares, then the
-// items. Groups of lanes take a sequence each, sized by the average number of
+// items (5.7 us for 1000 sequences in 16 blocks; 45 us in one block). Groups of lanes take a sequence each, sized by the average number of
 // shares; a sequence with far more than that is added by the whole block.
 template <class Loss>
 __device__ __forceinline__ typename Loss::Total sum_sequences(const LossArgs<Loss>& a, int64_t i0,
@@ -780,7 +787,8 @@ __device__ __forceinline__ double batch_factor(const LossArgs<Loss>& a) {
   return Loss::factor(a, n, c, bad);
 }
 
-// Step 3, one wave, one tile.
+// Step 3, one wave, one tile: the inputs again, now out of the MALL for most batches
+// (policy loss, 2.07 M tokens: 75 MB in 19 us, 3.9 TB/s).
 template <class Loss, int ROWS>
 __device__ __forceinline__ void tile_grads(const LossArgs<Loss>& a, int64_t tile) {
   const int64_t t0 = tile * (ROWS * 64);
@@ -860,7 +868,8 @@ __global__ void __launch_bounds__(64 * kLossWaves) loss_grads_kernel(LossArgs<Lo
 }
 
 // All three steps in one block, for small batches; the steps exchange their sums
-// through LDS.
+// through LDS. Bound by latency: 8.1 us for 413 tokens, half of it the loads and
+// exponentials of the two token steps.
 template <class Loss, bool GRADS>
 __global__ void __launch_bounds__(64 * kSmallWaves) loss_small_kernel(LossArgs<Loss> a) {
   __shared__ typename Loss::Share parts[kSmallSequences + kSmallTokens / 64];
