@@ -491,8 +491,8 @@ flce_status_t flce_policy_loss_forward(const float* logprob, const float* entrop
                                        const float* advantages, const int64_t* labels,
                                        const int64_t* cu_seqlens, int64_t N, int64_t B, int64_t V,
                                        const flce_policy_options_t* opt, float* loss,
-                                       float* stats, double* seq_state, void* workspace, size_t workspace_bytes,
-                                       void* stream);
+                                       float* stats, double* seq_state, void* workspace,
+                                       size_t workspace_bytes, void* stream);
 
 /* grad_logprob, and unless NULL grad_entropy (device fp32 [N]), of
  * grad_loss[0] * loss (device fp32 [1]; NULL means 1), from the inputs of the
@@ -570,9 +570,11 @@ flce_status_t flce_preference_loss_forward_backward(
     float* chosen_reward, float* rejected_reward, float* grad_logprob, void* workspace,
     size_t workspace_bytes, void* stream);
 
-/* Reads the status word that the last call with this workspace left, after synchronising `stream`. *invalid_labels (may be NULL)
- * receives the number of labels that were neither ignore_index nor in [0, V);
- * returns FLCE_ERR_INVALID_LABEL if that number is not 0, else FLCE_OK. */
+/* Reads the status word that the last call with this workspace left, after
+ * synchronising `stream`. *invalid_labels (may be NULL) receives the number of
+ * labels (embedding: tokens) that were neither ignore_index nor in [0, V), or of
+ * bad sequence offsets (losses); returns FLCE_ERR_INVALID_LABEL if that number is
+ * not 0, else FLCE_OK. */
 flce_status_t flce_get_status(const void* workspace, int64_t* invalid_labels, void* stream);
 
 /* Static English text for a status code. */

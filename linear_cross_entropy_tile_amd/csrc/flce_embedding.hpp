@@ -353,8 +353,8 @@ __global__ void __launch_bounds__(256) embed_sort_scan_kernel(int32_t* counts, i
   if (lane == 0) totals[d] = run;
 }
 
-__global__ void __launch_bounds__(64 * kSortMoveWaves) embed_sort_move_kernel(SortArgs a,
-                                                                              const int32_t* totals) {
+__global__ void __launch_bounds__(64 * kSortMoveWaves)
+embed_sort_move_kernel(SortArgs a, const int32_t* totals) {
   __shared__ uint16_t cnt[kSortMoveWaves][1 << kMaxDigitBits];
   __shared__ int base[1 << kMaxDigitBits];
   __shared__ int sh[kSortMoveWaves];
@@ -495,7 +495,8 @@ __global__ void __launch_bounds__(256) embed_gather_cols_kernel(GatherArgs a) {
   // of 8, so a chunk of 64 rows of the weight stays with one XCD, and the tokens of
   // a line, neighbours in the sorted order, find it in that L2; a chunk's tokens run
   // one after another, within the same 64 rows' pages.
-  const int64_t i = (int64_t)(blockIdx.x >> 3) * kGatherTokens + (threadIdx.x >> 6) * 8 + (lane & 7);
+  const int64_t i0 = (int64_t)(blockIdx.x >> 3) * kGatherTokens;
+  const int64_t i = i0 + (threadIdx.x >> 6) * 8 + (lane & 7);
   const int64_t h = ((int64_t)blockIdx.y * 8 + (blockIdx.x & 7)) * 64 + (lane >> 3) * 8;
   if (i >= a.t.N || h >= a.H) return;
   bool bad;

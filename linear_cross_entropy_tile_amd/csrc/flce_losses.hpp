@@ -142,8 +142,6 @@ __device__ __forceinline__ bool label_valid(int64_t y, int64_t ignore_index, int
 
 // ---- wave and block sums --------------------------------------------------------
 
-__device__ __forceinline__ double shfl_down_f64(double v, int d) { return __shfl_down(v, d, 64); }
-
 // The counts of one tile's tokens in one word (at most kLossTile = 256 each).
 constexpr int kCountValid = 1, kCountClipped = 1 << 10, kCountInvalid = 1 << 20;
 
@@ -698,8 +696,9 @@ __device__ __forceinline__ SeqParts seq_parts(const int64_t* cu, int64_t N, int 
 }
 
 // Step 2, one block, items [i0, i1): adds up the sequences' shares, then the
-// items (5.7 us for 1000 sequences in 16 blocks; 45 us in one block). Groups of lanes take a sequence each, sized by the average number of
-// shares; a sequence with far more than that is added by the whole block.
+// items (5.7 us for 1000 sequences in 16 blocks; 45 us in one block). Groups of
+// lanes take a sequence each, sized by the average number of shares; a sequence
+// with far more than that is added by the whole block.
 template <class Loss>
 __device__ __forceinline__ typename Loss::Total sum_sequences(const LossArgs<Loss>& a, int64_t i0,
                                                               int64_t i1) {

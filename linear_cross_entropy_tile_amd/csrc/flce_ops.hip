@@ -17,7 +17,8 @@ namespace {
 
 using namespace flce;
 
-static_assert(sizeof(PolicyLoss::Share) == sum_bytes(4) && sizeof(PolicyLoss::Total) == sum_bytes(5) &&
+static_assert(sizeof(PolicyLoss::Share) == sum_bytes(4) &&
+                  sizeof(PolicyLoss::Total) == sum_bytes(5) &&
                   sizeof(PreferenceLoss::Share) == sum_bytes(1) &&
                   sizeof(PreferenceLoss::Total) == sum_bytes(1),
               "workspace layout");
@@ -136,9 +137,9 @@ flce_status_t policy_impl(const float* logprob, const float* entropy, const floa
   if (stats == nullptr || workspace == nullptr) return FLCE_ERR_NULL_POINTER;
   if (opt->entropy_coef != 0.0 && N > 0 && entropy == nullptr) return FLCE_ERR_NULL_POINTER;
   if (grads && N > 0 && grad_logprob == nullptr) return FLCE_ERR_NULL_POINTER;
-  if (!aligned_to(entropy, 4) || !aligned_to(loss, 4) || !aligned_to(stats, 4) || !aligned_to(state, 8) ||
-      !aligned_to(grad_loss, 4) || !aligned_to(grad_logprob, 4) || !aligned_to(grad_entropy, 4) ||
-      !aligned16(workspace))
+  if (!aligned_to(entropy, 4) || !aligned_to(loss, 4) || !aligned_to(stats, 4) ||
+      !aligned_to(state, 8) || !aligned_to(grad_loss, 4) || !aligned_to(grad_logprob, 4) ||
+      !aligned_to(grad_entropy, 4) || !aligned16(workspace))
     return FLCE_ERR_MISALIGNED;
   const LossPlan p = policy_plan(N, B);
   if (workspace_bytes < p.total) return FLCE_ERR_WORKSPACE_TOO_SMALL;
@@ -448,8 +449,8 @@ flce_status_t flce_policy_loss_forward(const float* logprob, const float* entrop
                                        void* stream) {
   if (seq_state == nullptr) return FLCE_ERR_NULL_POINTER;
   return policy_impl(logprob, entropy, old_logprob, ref_logprob, advantages, labels, cu_seqlens,
-                     N, B, V, opt, nullptr, loss, stats, seq_state, false, nullptr, nullptr, workspace,
-                     workspace_bytes, stream);
+                     N, B, V, opt, nullptr, loss, stats, seq_state, false, nullptr, nullptr,
+                     workspace, workspace_bytes, stream);
 }
 
 flce_status_t flce_policy_loss_backward(const float* logprob, const float* old_logprob,
@@ -485,8 +486,8 @@ flce_status_t flce_policy_loss_forward_backward(
     float* grad_logprob, float* grad_entropy, void* workspace, size_t workspace_bytes,
     void* stream) {
   return policy_impl(logprob, entropy, old_logprob, ref_logprob, advantages, labels, cu_seqlens,
-                     N, B, V, opt, grad_loss, loss, stats, nullptr, true, grad_logprob, grad_entropy,
-                     workspace, workspace_bytes, stream);
+                     N, B, V, opt, grad_loss, loss, stats, nullptr, true, grad_logprob,
+                     grad_entropy, workspace, workspace_bytes, stream);
 }
 
 // ---- preference loss ------------------------------------------------------------------

@@ -218,7 +218,8 @@ inline flce_status_t check_embedding(int64_t N, int64_t H, int64_t Vs, int64_t v
                                      int64_t V_total, const flce_embedding_options_t* o) {
   const flce_status_t s = check_shape(N, H, Vs);
   if (s != FLCE_OK) return s;
-  if (V_total < 1 || V_total > kMaxV || v_begin < 0 || v_begin + Vs > V_total)
+  if (V_total < 1 || V_total > kMaxV || v_begin < 0 || Vs > V_total ||
+      v_begin > V_total - Vs)
     return FLCE_ERR_BAD_SHAPE;
   if (o == nullptr) return FLCE_ERR_NULL_POINTER;
   if (!std::isfinite(o->scale) || !std::isfinite((float)o->scale)) return FLCE_ERR_BAD_OPTION;

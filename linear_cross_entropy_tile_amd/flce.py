@@ -348,8 +348,8 @@ def flce_policy_loss_forward(logprob, entropy, old_logprob, ref_logprob, advanta
                              cu_seqlens, N, B, V, opt, loss, stats, seq_state, workspace,
                              workspace_bytes, stream):
     _check(lib().flce_policy_loss_forward(logprob, entropy, old_logprob, ref_logprob, advantages,
-                                          labels, cu_seqlens, N, B, V, ctypes.byref(opt), loss, stats,
-                                          seq_state, workspace, workspace_bytes, stream),
+                                          labels, cu_seqlens, N, B, V, ctypes.byref(opt), loss,
+                                          stats, seq_state, workspace, workspace_bytes, stream),
            "flce_policy_loss_forward")
 
 

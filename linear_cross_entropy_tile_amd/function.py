@@ -143,6 +143,7 @@ def policy_loss(logprob, labels, old_logprob, advantages, entropy=None, ref_logp
     not differentiable). Differentiable with respect to logprob and entropy,
     e.g. the outputs of ``linear_cross_entropy(..., reduction="none")``;
     old_logprob, ref_logprob and advantages are constants."""
+    flce._policy_options(**options)  # refuses what the backward could not take
     return PolicyLoss.apply(logprob, entropy, labels, old_logprob, advantages, ref_logprob,
                             cu_seqlens, options)
 
@@ -180,4 +181,5 @@ def preference_loss(logprob, labels, cu_seqlens, ref_logprob=None, **options):
     reduction "none", and the rewards [P] of the two sides (not
     differentiable). Differentiable with respect to logprob; ref_logprob is a
     constant."""
+    flce._preference_options(**options)  # refuses what the backward could not take
     return PreferenceLoss.apply(logprob, labels, cu_seqlens, ref_logprob, options)

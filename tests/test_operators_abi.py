@@ -5,7 +5,7 @@ import ctypes
 import pytest
 import torch
 
-from linear_cross_entropy_tile_amd import flce
+from linear_cross_entropy_tile_amd import flce, function
 
 A = 0x1000
 BIG = 1 << 40
@@ -27,6 +27,7 @@ def _embed(fn="forward", **kw):
     (dict(x=None), 1), (dict(tokens=None), 1), (dict(out=None), 1), (dict(ws=None), 1),
     (dict(N=-1), 2), (dict(N=(1 << 21) + 1), 2), (dict(H=0), 2), (dict(V=0), 2),
     (dict(V=(1 << 22)), 2), (dict(vb=-1), 2), (dict(vb=1), 2), (dict(vt=9), 2),
+    (dict(vb=(1 << 63) - 1), 2), (dict(vb=(1 << 63) - 5), 2),
     (dict(vt=1 << 23), 2),
     (dict(H=12), 4), (dict(x=A + 8), 4), (dict(out=A + 4), 4), (dict(ws=A + 8), 4),
     (dict(tokens=A + 4), 4), (dict(wsb=16), 5),
@@ -180,6 +181,10 @@ def test_wrappers_reject_host_tensors_and_options():
         flce.policy_loss_forward_backward(x, t, x, x, kl_estimator="k4")
     with pytest.raises(TypeError):
         flce.policy_loss(x, t, x, x, clip=0.2)
+    # The autograd functions keep no workspace for their backward.
+    for fn, args in ((function.policy_loss, (x, t, x, x)), (function.preference_loss, (x, t, t))):
+        with pytest.raises(TypeError, match="workspace"):
+            fn(*args, workspace=x)
     with pytest.raises(ValueError, match="kind must be one of"):
         flce.preference_loss(x, t, t, kind="margin")
     with pytest.raises(ValueError, match="logprob must be a CUDA"):
