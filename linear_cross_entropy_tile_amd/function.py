@@ -12,6 +12,13 @@ and the losses of RL and preference tuning on the head's per-token outputs.
 Marshalling only: the forward calls flce_forward through ``flce.forward``
 and keeps the per-token lse and entropy; the backward hands the upstream
 gradients of the two outputs to flce_backward through ``flce.backward``.
+
+Under graph capture: torch adds a leaf's gradient on the stream on which the
+leaf's accumulating node was made, and that node lives as long as any graph of
+the leaf. A captured backward over a leaf of which an eager graph still lives
+would reach out of the capture, which ends the process; ``embedding``,
+``policy_loss`` and ``preference_loss`` refuse the call while an eager result of
+this module on the same leaf lives (drop it first, or capture on its stream).
 """
 from __future__ import annotations
 
@@ -23,6 +30,32 @@ from . import flce
 
 __all__ = ["LinearCrossEntropy", "linear_cross_entropy", "Embedding", "embedding",
            "PolicyLoss", "policy_loss", "PreferenceLoss", "preference_loss"]
+
+
+def _leaves(tensors):
+    return [t for t in tensors if isinstance(t, torch.Tensor) and t.is_cuda and t.is_leaf
+            and t.requires_grad] if torch.is_grad_enabled() else []
+
+
+def _refuse_captured_leaves(*tensors):
+    """Raises if a graph is captured while a leaf among the tensors belongs to a
+    live graph that this module made on another stream."""
+    for t in _leaves(tensors):
+        if torch.cuda.is_current_stream_capturing():
+            made = torch.autograd.graph.get_gradient_edge(t).node.metadata.get("flce_stream")
+            if made not in (None, torch.cuda.current_stream(t.device).cuda_stream):
+                raise RuntimeError(
+                    "an eager result of this leaf is still alive: its backward cannot be "
+                    "captured on another stream; drop the result first, capture on its stream, "
+                    "or use torch.no_grad() for the forward alone")
+
+
+def _note_leaves(*tensors):
+    """Notes the stream of a new graph on its leaves' accumulating nodes (kept
+    alive by the graph, and with them the note)."""
+    for t in _leaves(tensors):
+        torch.autograd.graph.get_gradient_edge(t).node.metadata.setdefault(
+            "flce_stream", torch.cuda.current_stream(t.device).cuda_stream)
 
 
 class LinearCrossEntropy(torch.autograd.Function):
@@ -73,8 +106,10 @@ def linear_cross_entropy(hidden, weight, labels, reduction="mean", ignore_index=
     class_weight[labels[t]] in the reductions; the mean then divides by the
     weight sum of the non-ignored tokens. Differentiable with respect to
     hidden and weight (gradients in bf16)."""
-    return LinearCrossEntropy.apply(hidden, weight, labels, reduction, ignore_index, softcap,
-                                    class_weight, entropy_reduction)
+    out = LinearCrossEntropy.apply(hidden, weight, labels, reduction, ignore_index, softcap,
+                                   class_weight, entropy_reduction)
+    _note_leaves(hidden, weight)
+    return out
 
 
 class Embedding(torch.autograd.Function):
@@ -104,7 +139,10 @@ def embedding(weight, tokens, layout="hv", scale=1.0, ignore_index=-100):
     bf16: the head's [H,V] (layout "hv", tied embeddings) or a table [V,H]
     ("vh"). Zero rows at ignore_index and at ids outside the vocabulary.
     Differentiable with respect to weight (gradient in bf16)."""
-    return Embedding.apply(weight, tokens, layout, scale, ignore_index)
+    _refuse_captured_leaves(weight)
+    hidden = Embedding.apply(weight, tokens, layout, scale, ignore_index)
+    _note_leaves(weight)
+    return hidden
 
 
 class PolicyLoss(torch.autograd.Function):
@@ -144,8 +182,11 @@ def policy_loss(logprob, labels, old_logprob, advantages, entropy=None, ref_logp
     e.g. the outputs of ``linear_cross_entropy(..., reduction="none")``;
     old_logprob, ref_logprob and advantages are constants."""
     flce._policy_options(**options)  # refuses what the backward could not take
-    return PolicyLoss.apply(logprob, entropy, labels, old_logprob, advantages, ref_logprob,
-                            cu_seqlens, options)
+    _refuse_captured_leaves(logprob, entropy)
+    out = PolicyLoss.apply(logprob, entropy, labels, old_logprob, advantages, ref_logprob,
+                           cu_seqlens, options)
+    _note_leaves(logprob, entropy)
+    return out
 
 
 class PreferenceLoss(torch.autograd.Function):
@@ -182,4 +223,7 @@ def preference_loss(logprob, labels, cu_seqlens, ref_logprob=None, **options):
     differentiable). Differentiable with respect to logprob; ref_logprob is a
     constant."""
     flce._preference_options(**options)  # refuses what the backward could not take
-    return PreferenceLoss.apply(logprob, labels, cu_seqlens, ref_logprob, options)
+    _refuse_captured_leaves(logprob)
+    out = PreferenceLoss.apply(logprob, labels, cu_seqlens, ref_logprob, options)
+    _note_leaves(logprob)
+    return out

@@ -98,3 +98,97 @@ def test_tied_step(loss, how):
         gw = wp.grad
     assert abs(got_loss.item() - want_loss) <= 2.0 ** -6 * max(1.0, abs(want_loss))
     assert _rel(gw.float().cpu().numpy(), dw) <= 2.0 ** -6
+
+
+def _autograd_step(weight, tok, lab, old, adv, cu):
+    hidden = torch.tanh(function.embedding(weight, tok, scale=SCALE))
+    lp, ent = function.linear_cross_entropy(hidden, weight, lab, reduction="none")
+    loss, stats = function.policy_loss(lp, lab, old, adv, entropy=ent, cu_seqlens=cu,
+                                       entropy_coef=0.01, advantages_per_sequence=True)
+    pref, _, _ = function.preference_loss(lp, lab, cu)
+    return loss + pref, stats
+
+
+def _step_tensors():
+    rng, w, _, tok, lab = _step_inputs()
+    dev = G.dev()
+    old = torch.from_numpy((-rng.exponential(1.0, N) - 3).astype(np.float32)).to(dev)
+    adv = torch.from_numpy(rng.normal(size=len(CU) - 1).astype(np.float32)).to(dev)
+    return (w.to(dev), torch.from_numpy(tok).to(dev), torch.from_numpy(lab).to(dev), old, adv,
+            torch.tensor(CU, device=dev))
+
+
+def test_captured_autograd_step_replays():
+    """Forward and backward through autograd in a captured graph, over a leaf
+    that no eager graph holds, replayed with other inputs and eager work
+    between; against the same step run eagerly on another leaf."""
+    w, tok, lab, old, adv, cu = _step_tensors()
+
+    def eager():
+        leaf = w.clone().requires_grad_(True)
+        total, stats = _autograd_step(leaf, tok, lab, old, adv, cu)
+        total.backward()
+        return [total.detach().clone(), stats.clone(), leaf.grad.clone()]
+
+    eager()  # loads what the step needs before the capture
+    torch.cuda.synchronize()
+    leaf = w.clone().requires_grad_(True)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        total, stats = _autograd_step(leaf, tok, lab, old, adv, cu)
+        total.backward()
+    got = [total.detach(), stats, leaf.grad]
+    for rep in range(3):
+        tok.random_(0, V)
+        w.normal_(0.0, 0.2)
+        with torch.no_grad():
+            leaf.copy_(w)
+        want = eager()
+        for x in got:
+            x.fill_(7.0)
+        graph.replay()
+        torch.cuda.synchronize()
+        for x, y in zip(got, want):
+            assert torch.equal(x, y)
+
+
+def test_capture_over_a_live_eager_graph_is_refused(monkeypatch):
+    """While an eager result lives, a call under capture on another stream is
+    refused for the same leaf, by every operator; not for another leaf, on the
+    result's own stream, without gradients, or once the result is dropped.
+    Nothing is captured here: the query is answered in its place."""
+    w, tok, lab, old, adv, cu = _step_tensors()
+    weight, lp = w.requires_grad_(True), old.clone().requires_grad_(True)
+    calls = {
+        "embedding": lambda: function.embedding(weight, tok),
+        "policy": lambda: function.policy_loss(lp, lab, old, adv, cu_seqlens=cu,
+                                               advantages_per_sequence=True)[0],
+        "preference": lambda: function.preference_loss(lp, lab, cu)[0],
+    }
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+
+    def captured(call):
+        with monkeypatch.context() as m, torch.cuda.stream(side):
+            m.setattr(torch.cuda, "is_current_stream_capturing", lambda: True)
+            return call()
+
+    head = lambda: function.linear_cross_entropy(  # noqa: E731
+        torch.zeros(N, H, dtype=torch.bfloat16, device=w.device), weight, lab)[0]
+    for name, made in (("embedding", calls["embedding"]), ("embedding", head),
+                       ("policy", calls["policy"]), ("preference", calls["policy"]),
+                       ("policy", calls["preference"])):
+        call = calls[name]
+        alive = made()
+        with pytest.raises(RuntimeError, match="still alive"):
+            captured(call)
+        with torch.no_grad():
+            captured(call)
+        with monkeypatch.context() as m:
+            m.setattr(torch.cuda, "is_current_stream_capturing", lambda: True)
+            call()
+        other = "embedding" if name != "embedding" else "policy"
+        captured(calls[other])
+        del alive
+        captured(call)
+    torch.cuda.synchronize()
