@@ -43,7 +43,7 @@ def _refuse_captured_leaves(*tensors):
     for t in _leaves(tensors):
         if torch.cuda.is_current_stream_capturing():
             made = torch.autograd.graph.get_gradient_edge(t).node.metadata.get("flce_stream")
-            if made not in (None, torch.cuda.current_stream(t.device).cuda_stream):
+            if made not in (None, torch._C._cuda_getCurrentRawStream(t.device.index)):
                 raise RuntimeError(
                     "an eager result of this leaf is still alive: its backward cannot be "
                     "captured on another stream; drop the result first, capture on its stream, "
@@ -55,7 +55,7 @@ def _note_leaves(*tensors):
     alive by the graph, and with them the note)."""
     for t in _leaves(tensors):
         torch.autograd.graph.get_gradient_edge(t).node.metadata.setdefault(
-            "flce_stream", torch.cuda.current_stream(t.device).cuda_stream)
+            "flce_stream", torch._C._cuda_getCurrentRawStream(t.device.index))
 
 
 class LinearCrossEntropy(torch.autograd.Function):
