@@ -198,6 +198,61 @@ def test_largest_vocabulary(layout, N):
 
 
 @pytest.mark.parametrize("layout", ["hv", "vh"])
+def test_weights_of_more_than_2_32_values(layout):
+    """Offsets into the weight and its gradient that pass 32 bits. Every value of
+    the gradient is written: the memory it gets held NaN before."""
+    V, H, N = (1 << 22) - 256, 1032, 300
+    assert V * H > 1 << 32
+    shape = (H, V) if layout == "hv" else (V, H)
+    g = torch.Generator(device="cuda")
+    g.manual_seed(2)
+    w = torch.empty(shape, device=G.dev(), dtype=torch.bfloat16).normal_(generator=g)
+    t = torch.randint(0, V, (N,), generator=g, device=G.dev())
+    t[::3] = V - 1 - torch.arange(100, device=G.dev()) // 4
+    out = flce.embedding(w, t, layout=layout)["hidden"]
+    for i, v in enumerate(t.tolist()):
+        assert torch.equal(out[i], w[:, v] if layout == "hv" else w[v]), (i, v)
+    w.fill_(float("nan"))
+    del w
+    gr = torch.randint(-8, 9, (N, H), generator=g, device=G.dev()).to(torch.bfloat16)
+    got = flce.embedding_backward(gr, t, V, layout=layout)
+    ids = sorted(set(t.tolist()))
+    for v in ids:  # sums of whole numbers below 2^8: exact, also in bf16
+        row = got[:, v] if layout == "hv" else got[v]
+        assert torch.equal(row.float(), gr.float()[t == v].sum(0)), v
+        row.zero_()
+    assert not bool(torch.any(got))
+
+
+@pytest.mark.parametrize("layout", ["hv", "vh"])
+def test_hidden_states_of_more_than_2_32_values(layout):
+    """The same for the hidden states and their gradient, at the largest batch."""
+    V, H, N = 1000, 2056, 1 << 21
+    assert N * H > 1 << 32
+    g = torch.Generator(device="cuda")
+    g.manual_seed(3)
+    dev = G.dev()
+    w = torch.randn((H, V) if layout == "hv" else (V, H), generator=g, device=dev,
+                    dtype=torch.bfloat16)
+    t = torch.randint(0, V, (N,), generator=g, device=dev)
+    out = flce.embedding(w, t, layout=layout)["hidden"]
+    table = w.t().contiguous() if layout == "hv" else w
+    for i in range(0, N, 1 << 16):
+        assert torch.equal(out[i:i + (1 << 16)], table[t[i:i + (1 << 16)]]), i
+    del out
+    # Row i, column h holds i % 7 + h % 3: sums are whole numbers below 2^24, exact.
+    a = (torch.arange(N, device=dev) % 7).to(torch.bfloat16)
+    b = (torch.arange(H, device=dev) % 3).to(torch.bfloat16)
+    gr = a[:, None] + b[None, :]
+    got = flce.embedding_backward(gr, t, V, layout=layout, grad_dtype="f32")
+    tc = t.cpu().numpy()
+    sums = np.bincount(tc, weights=np.arange(N) % 7, minlength=V)
+    want = sums[:, None] + np.bincount(tc, minlength=V)[:, None] * (np.arange(H) % 3)[None, :]
+    got = (got.t() if layout == "hv" else got).cpu().numpy().astype(np.float64)
+    assert np.array_equal(got, want)
+
+
+@pytest.mark.parametrize("layout", ["hv", "vh"])
 def test_slices_make_the_whole(layout):
     rng = np.random.default_rng(7)
     N, H, V, cut = 900, 40, 203, 96
