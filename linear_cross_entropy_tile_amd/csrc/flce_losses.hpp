@@ -746,6 +746,7 @@ __device__ __forceinline__ typename Loss::Total sum_sequences(const LossArgs<Los
         v.clear();
         for (int64_t q = threadIdx.x; q < p.count; q += blockDim.x) v.add(a.parts[s + p.p0 + q]);
         v = block_total(v, (int)(blockDim.x >> 6), sh_share);
+        v.bad = 0;  // its own offsets are good; shares that no tile wrote hold anything
         if (threadIdx.x == 0) a.seq_sum[s] = v;
       }
     }
