@@ -441,8 +441,8 @@ flce_status_t flce_embedding_backward(const void* grad_hidden, const int64_t* to
  * Every per-token term is computed, and every sum accumulated, in float64 in a
  * fixed order; outputs are rounded once to fp32.
  * A sequence whose offsets decrease or leave [0, N] makes the reduced loss, the
- * statistics and every valid token's gradient NaN, and (preference) its pair's
- * outputs; the results of the other sequences are then unspecified. The status
+ * statistics and the gradient of every token with a valid label NaN, and
+ * (preference) its pair's outputs; the results of the other sequences are then unspecified. The status
  * word counts such sequences or, when there are none, the labels of sequences
  * that are neither ignore_index nor in [0, V). */
 enum { FLCE_REDUCTION_SEQUENCE_MEAN = 3 };  /* flce_policy_loss_* only */

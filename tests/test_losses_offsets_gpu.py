@@ -96,3 +96,42 @@ def test_preference_counts_bad_sequences(name, fill):
         assert _status(ws) == bad.sum()
         assert bool(torch.isnan(out["loss"]).all()) or red == "none"
         assert bool(torch.isnan(out["pair_loss"][torch.from_numpy(bad[:P] | bad[P:])]).all())
+
+
+@pytest.mark.parametrize("cfg", POLICY, ids=range(len(POLICY)))
+@pytest.mark.parametrize("name", BATCHES)
+def test_policy_gradients_are_nan_at_every_valid_token(name, cfg):
+    """Also at tokens that the broken offsets place in no sequence."""
+    x, bad, valid = _inputs(name)
+    args, kw = _policy(x, cfg)
+    both = flce.policy_loss_forward_backward(*args, entropy=x["entropy"], **kw)
+    assert _nan_where_valid(both["grad_logprob"], valid)
+    assert _nan_where_valid(both["grad_entropy"], valid)
+    out = flce.policy_loss(*args, entropy=x["entropy"], **kw)
+    for g in flce.policy_loss_backward(*args, out["seq_state"], **kw):
+        assert _nan_where_valid(g, valid)
+
+
+@pytest.mark.parametrize("reduction", ["mean", "none"])
+@pytest.mark.parametrize("name", BATCHES)
+def test_preference_gradients_are_nan_at_every_valid_token(name, reduction):
+    x, bad, valid = _inputs(name)
+    args, kw = (x["logprob"], x["labels"], x["cu"]), dict(reduction=reduction, vocab_size=V)
+    both = flce.preference_loss_forward_backward(*args, **kw)
+    assert _nan_where_valid(both["grad_logprob"], valid)
+    out = flce.preference_loss(*args, **kw)
+    assert _nan_where_valid(flce.preference_loss_backward(*args[1:], out["seq_state"], **kw), valid)
+
+
+def test_nan_upstream_gradient_is_no_bad_offset():
+    """A NaN gradient of the loss reaches the tokens of the sequences only."""
+    cu = torch.tensor([2, 5, 9], device=G.dev())
+    x = -torch.rand(12, device=G.dev())
+    lab = torch.zeros(12, dtype=torch.int64, device=G.dev())
+    inside = np.zeros(12, bool)
+    inside[2:9] = True
+    g = torch.full((1,), float("nan"), device=G.dev())
+    out = flce.policy_loss_forward_backward(x, lab, x - 0.1, x + 3.0, grad_loss=g, cu_seqlens=cu)
+    assert _nan_where_valid(out["grad_logprob"], inside)
+    out = flce.preference_loss_forward_backward(x, lab, cu, grad_loss=g)
+    assert _nan_where_valid(out["grad_logprob"], inside)
