@@ -452,8 +452,9 @@ struct PolicyLoss {
     s[3] = (float)(k * v.x[3]);
     s[4] = (float)(k * v.x[4]);
     s[5] = (float)(0.0 - k * v.x[0]);
-    s[6] = (float)v.n;
-    s[7] = (float)v.c;
+    // The counts are of shares that are undefined after bad offsets.
+    s[6] = v.bad != 0 ? __builtin_nanf("") : (float)v.n;
+    s[7] = v.bad != 0 ? __builtin_nanf("") : (float)v.c;
   }
   __device__ static double state_factor(const LossArgs<PolicyLoss>& a) { return a.state[2 * a.B]; }
   // The reduced loss's upstream gradient.

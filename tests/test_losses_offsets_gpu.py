@@ -135,3 +135,12 @@ def test_nan_upstream_gradient_is_no_bad_offset():
     assert _nan_where_valid(out["grad_logprob"], inside)
     out = flce.preference_loss_forward_backward(x, lab, cu, grad_loss=g)
     assert _nan_where_valid(out["grad_logprob"], inside)
+
+
+@pytest.mark.parametrize("name", BATCHES)
+def test_policy_statistics_are_all_nan(name):
+    """The two counts among them: they add up shares that may be undefined."""
+    x, bad, valid = _inputs(name)
+    args, kw = _policy(x, POLICY[0])
+    assert bool(torch.isnan(flce.policy_loss(*args, **kw)["stats"]).all())
+    assert bool(torch.isnan(flce.policy_loss_forward_backward(*args, **kw)["stats"]).all())
