@@ -527,7 +527,10 @@ struct PreferenceLoss {
     const Share c = a.seq_sum[i], r = a.seq_sum[P + i];
     const double ic = in.normalize && c.n > 0 ? 1.0 / c.n : 1.0;
     const double ir = in.normalize && r.n > 0 ? 1.0 / r.n : 1.0;
-    const double rc = c.x[0] * ic, rr = r.x[0] * ir;
+    // Bad offsets on either side take the whole pair.
+    const bool bad = c.bad != 0 || r.bad != 0;
+    const double rc = bad ? __builtin_nan("") : c.x[0] * ic;
+    const double rr = bad ? __builtin_nan("") : r.x[0] * ir;
     const double diff = rc - rr;
     double loss, slope;  // slope: derivative by diff
     if (in.kind == FLCE_PREFERENCE_IPO) {

@@ -144,3 +144,17 @@ def test_policy_statistics_are_all_nan(name):
     args, kw = _policy(x, POLICY[0])
     assert bool(torch.isnan(flce.policy_loss(*args, **kw)["stats"]).all())
     assert bool(torch.isnan(flce.policy_loss_forward_backward(*args, **kw)["stats"]).all())
+
+
+@pytest.mark.parametrize("kind", ["sigmoid", "hinge", "ipo"])
+@pytest.mark.parametrize("name", BATCHES)
+def test_preference_outputs_of_a_bad_pair_are_nan(name, kind):
+    """Both rewards and the loss of a pair, whichever side's offsets are bad."""
+    x, bad, valid = _inputs(name)
+    P = bad.size // 2
+    pair = torch.from_numpy(bad[:P] | bad[P:])
+    for norm in (False, True):
+        out = flce.preference_loss(x["logprob"], x["labels"], x["cu"], kind=kind,
+                                   length_normalize=norm, vocab_size=V)
+        for k in ("pair_loss", "chosen_reward", "rejected_reward"):
+            assert bool(torch.isnan(out[k].cpu()[pair]).all()), k
