@@ -462,6 +462,7 @@ __global__ void __launch_bounds__(256) embed_gather_rows_kernel(GatherArgs a) {
   const int64_t h0 = ((int64_t)blockIdx.y * kGatherLoads * a.lanes + k) * 8;
   const uint16_t* src = a.weight + (int64_t)key * a.H;
   uint16_t* dst = a.out + i * a.H;
+  const float scale = key < a.t.Vs ? a.scale : 1.f;  // zero rows are +0 for every scale
   eu32x4 v[kGatherLoads];
 #pragma unroll
   for (int j = 0; j < kGatherLoads; ++j) {
@@ -472,7 +473,7 @@ __global__ void __launch_bounds__(256) embed_gather_rows_kernel(GatherArgs a) {
 #pragma unroll
   for (int j = 0; j < kGatherLoads; ++j) {
     const int64_t h = h0 + (int64_t)j * a.lanes * 8;
-    if (h < a.H) stream(reinterpret_cast<eu32x4*>(dst + h), scaled8(v[j], a.scale));
+    if (h < a.H) stream(reinterpret_cast<eu32x4*>(dst + h), scaled8(v[j], scale));
   }
 }
 
