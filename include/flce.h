@@ -403,7 +403,7 @@ typedef struct flce_embedding_options {
   int grad_dtype;        /* FLCE_GRAD_BF16 or FLCE_GRAD_F32: type of grad_weight */
   int accumulate;        /* 0: grad_weight is written whole (zero for unused ids);
                           * 1: the gradient is added to what grad_weight holds, e.g. the head's
-                          * grad_weight of a tied matrix (only used ids are touched) */
+                          * grad_weight of a tied matrix (ids without a token are not written) */
 } flce_embedding_options_t;
 
 /* Workspace bytes of the two calls for Vs ids (host only; either out-pointer

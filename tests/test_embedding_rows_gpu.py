@@ -30,3 +30,39 @@ def test_zero_rows_are_positive_zeros(N, H, scale, layout):
     rows = w[torch.from_numpy(tok - v_begin)[on]]
     want = (rows.float() * scale).to(torch.bfloat16)
     assert torch.equal(got[on], want.view(torch.int16))
+
+
+@pytest.mark.parametrize("layout", ["hv", "vh"])
+@pytest.mark.parametrize("V", [1, 70, 72, 203, 640])
+@pytest.mark.parametrize("hidden", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+def test_accumulation_stores_to_used_ids_only(V, hidden, dtype, layout):
+    """Ids that no token has hold signalling NaN: any arithmetic on their values,
+    and so any store but one of the same bits, would change them. Used ids alone,
+    in pairs, in whole groups of eight, and at the borders of the strips of 64."""
+    H, N = 264, 500
+    rng = np.random.default_rng(V)
+    used = np.zeros(V, bool)
+    used[::11] = True
+    used[[i for i in (8, 9, 62, 63, 64, 65, 127, 128) if i < V]] = True
+    used[16:24] = True
+    used[V - 1] = True
+    if V > 400:
+        used[192:256] = True
+        used[320:384] = False
+    ids = np.nonzero(used)[0]
+    tok = np.concatenate([ids, rng.choice(ids, N)])
+    tok[1::7] = -100
+    used = np.isin(np.arange(V), tok)
+    view, signal = ((torch.int16, 0x7F81) if dtype == torch.bfloat16 else (torch.int32, 0x7F800001))
+    base = torch.from_numpy(rng.integers(-8, 9, (V, H)).astype(np.float32)).to(dtype)
+    base.view(view)[torch.from_numpy(~used)] = signal
+    g = torch.from_numpy(rng.integers(-2, 3, (tok.size, H)).astype(np.float32)).to(hidden)
+    acc = (base if layout == "vh" else base.t().contiguous()).to(G.dev())
+    flce.embedding_backward(g.to(G.dev()), torch.from_numpy(tok).to(G.dev()), V, layout=layout,
+                            grad_weight=acc)
+    got = (acc if layout == "vh" else acc.t().contiguous()).cpu()
+    want = base.clone()
+    for v in np.nonzero(used)[0]:  # whole numbers below 2^8 in every partial sum: exact
+        want[v] += g[torch.from_numpy(tok == v)].float().sum(0).to(dtype)
+    assert torch.equal(got.view(view), want.view(view))
