@@ -128,9 +128,11 @@ class Embedding(torch.autograd.Function):
     @once_differentiable
     def backward(ctx, grad_hidden):
         tokens, = ctx.saved_tensors
-        gw = flce.embedding_backward(grad_hidden.contiguous(), tokens, ctx.vocab_size,
-                                     layout=ctx.layout, scale=ctx.scale,
-                                     ignore_index=ctx.ignore_index)
+        grad_hidden = grad_hidden.contiguous()
+        if grad_hidden.data_ptr() % 16 != 0:  # a view into another tensor's gradient
+            grad_hidden = grad_hidden.clone()
+        gw = flce.embedding_backward(grad_hidden, tokens, ctx.vocab_size, layout=ctx.layout,
+                                     scale=ctx.scale, ignore_index=ctx.ignore_index)
         return gw, None, None, None, None
 
 
