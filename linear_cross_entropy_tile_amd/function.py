@@ -15,10 +15,12 @@ gradients of the two outputs to flce_backward through ``flce.backward``.
 
 Under graph capture: torch adds a leaf's gradient on the stream on which the
 leaf's accumulating node was made, and that node lives as long as any graph of
-the leaf. A captured backward over a leaf of which an eager graph still lives
-would reach out of the capture, which ends the process; ``embedding``,
-``policy_loss`` and ``preference_loss`` refuse the call while an eager result of
-this module on the same leaf lives (drop it first, or capture on its stream).
+the leaf. A stream made for the work joins a capture through events, so a result
+of a warm-up on a side stream may still be bound. The default stream cannot join
+one: a captured backward over a leaf that an eager graph made there still holds
+would reach out of the capture, which ends the process. ``embedding``,
+``policy_loss`` and ``preference_loss`` refuse the call while such a result of
+this module on the same leaf lives (drop it first).
 """
 from __future__ import annotations
 
@@ -37,17 +39,23 @@ def _leaves(tensors):
             and t.requires_grad] if torch.is_grad_enabled() else []
 
 
+_DEFAULT_STREAM = 0  # raw handle
+
+
 def _refuse_captured_leaves(*tensors):
     """Raises if a graph is captured while a leaf among the tensors belongs to a
-    live graph that this module made on another stream."""
-    for t in _leaves(tensors):
-        if torch.cuda.is_current_stream_capturing():
-            made = torch.autograd.graph.get_gradient_edge(t).node.metadata.get("flce_stream")
-            if made not in (None, torch._C._cuda_getCurrentRawStream(t.device.index)):
-                raise RuntimeError(
-                    "an eager result of this leaf is still alive: its backward cannot be "
-                    "captured on another stream; drop the result first, capture on its stream, "
-                    "or use torch.no_grad() for the forward alone")
+    live graph that this module made on the default stream."""
+    leaves = _leaves(tensors)
+    if not leaves or not torch.cuda.is_current_stream_capturing():
+        return
+    for t in leaves:
+        made = torch.autograd.graph.get_gradient_edge(t).node.metadata.get("flce_stream")
+        if (made == _DEFAULT_STREAM
+                and torch._C._cuda_getCurrentRawStream(t.device.index) != _DEFAULT_STREAM):
+            raise RuntimeError(
+                "an eager result of this leaf is still alive on the default stream: a backward "
+                "over it cannot be captured; drop the result first, make it on a side stream, "
+                "or use torch.no_grad() for the forward alone")
 
 
 def _note_leaves(*tensors):

@@ -3,6 +3,7 @@ import pytest
 import torch
 
 import gpu_helpers as G
+import test_tied_step_gpu as T
 from linear_cross_entropy_tile_amd import flce, function
 
 pytestmark = pytest.mark.gpu
@@ -25,3 +26,79 @@ def test_embedding_takes_a_gradient_at_any_address(layout):
     out = torch.cat([head, function.embedding(leaf, tok, layout=layout).reshape(-1)])
     out.backward(up)
     assert torch.equal(leaf.grad, want)
+
+
+def _captured(monkeypatch, stream, call):
+    """The call as it would run under a capture on the stream; nothing is
+    captured, the query is answered in its place."""
+    with monkeypatch.context() as m, torch.cuda.stream(stream):
+        m.setattr(torch.cuda, "is_current_stream_capturing", lambda: True)
+        return call()
+
+
+def _calls(weight, lp, tok, lab, old, adv, cu):
+    return {"embedding": lambda: function.embedding(weight, tok),
+            "policy": lambda: function.policy_loss(lp, lab, old, adv, cu_seqlens=cu,
+                                                   advantages_per_sequence=True)[0],
+            "preference": lambda: function.preference_loss(lp, lab, cu)[0]}
+
+
+@pytest.mark.parametrize("name", ["embedding", "policy", "preference"])
+def test_results_of_a_side_stream_do_not_stop_a_capture(name, monkeypatch):
+    """A warm-up on a side stream whose result is still bound: a gradient that is
+    added on that stream joins the capture through events, and is not refused.
+    One that belongs to the default stream, which no capture can join, is."""
+    w, tok, lab, old, adv, cu = T._step_tensors()
+    weight, lp = w.requires_grad_(True), old.clone().requires_grad_(True)
+    call = _calls(weight, lp, tok, lab, old, adv, cu)[name]
+    warm, side = torch.cuda.Stream(), torch.cuda.Stream()
+    for s in (warm, side):
+        s.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(warm):
+        alive = call()
+    again = call()  # on the default stream, over the node that the side stream made
+    _captured(monkeypatch, side, call)
+    del alive, again
+    alive = call()
+    with pytest.raises(RuntimeError, match="still alive"):
+        _captured(monkeypatch, side, call)
+    del alive
+    torch.cuda.synchronize()
+
+
+def test_captured_step_with_its_warm_up_still_bound():
+    """The usual order: a warm-up on a side stream, its loss still in a variable,
+    then forward and backward captured over the same leaf, and replayed with
+    other inputs and eager work between."""
+    w, tok, lab, old, adv, cu = T._step_tensors()
+    leaf = w.clone().requires_grad_(True)
+    warm = torch.cuda.Stream()
+    warm.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(warm):
+        bound, _ = T._autograd_step(leaf, tok, lab, old, adv, cu)
+        bound.backward()
+    torch.cuda.current_stream().wait_stream(warm)
+    torch.cuda.synchronize()
+    leaf.grad = None
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        total, stats = T._autograd_step(leaf, tok, lab, old, adv, cu)
+        total.backward()
+    got = [total.detach(), stats, leaf.grad]
+    for rep in range(3):
+        tok.random_(0, T.V)
+        w.normal_(0.0, 0.2)
+        with torch.no_grad():
+            leaf.copy_(w)
+        other = w.clone().requires_grad_(True)
+        t, s = T._autograd_step(other, tok, lab, old, adv, cu)
+        t.backward()
+        want = [t.detach().clone(), s.clone(), other.grad.clone()]
+        del t, s
+        for x in got:
+            x.fill_(7.0)
+        graph.replay()
+        torch.cuda.synchronize()
+        for x, y in zip(got, want):
+            assert torch.equal(x, y)
+    assert bool(torch.isfinite(bound))
