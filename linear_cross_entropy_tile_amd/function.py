@@ -18,9 +18,10 @@ leaf's accumulating node was made, and that node lives as long as any graph of
 the leaf. A stream made for the work joins a capture through events, so a result
 of a warm-up on a side stream may still be bound. The default stream cannot join
 one: a captured backward over a leaf that an eager graph made there still holds
-would reach out of the capture, which ends the process. ``embedding``,
-``policy_loss`` and ``preference_loss`` refuse the call while such a result of
-this module on the same leaf lives (drop it first).
+would reach out of the capture, which ends the process. While such a result of
+this module on the same leaf lives (drop it first), ``embedding``,
+``policy_loss`` and ``preference_loss`` refuse the call, and the backward of
+``linear_cross_entropy`` raises.
 """
 from __future__ import annotations
 
@@ -34,24 +35,25 @@ __all__ = ["LinearCrossEntropy", "linear_cross_entropy", "Embedding", "embedding
            "PolicyLoss", "policy_loss", "PreferenceLoss", "preference_loss"]
 
 
-def _leaves(tensors):
-    return [t for t in tensors if isinstance(t, torch.Tensor) and t.is_cuda and t.is_leaf
-            and t.requires_grad] if torch.is_grad_enabled() else []
+def _accumulators(tensors):
+    """The accumulating nodes of the leaves among the tensors."""
+    return [torch.autograd.graph.get_gradient_edge(t).node for t in tensors
+            if isinstance(t, torch.Tensor) and t.is_cuda and t.is_leaf and t.requires_grad
+            ] if torch.is_grad_enabled() else []
 
 
 _DEFAULT_STREAM = 0  # raw handle
 
 
-def _refuse_captured_leaves(*tensors):
-    """Raises if a graph is captured while a leaf among the tensors belongs to a
-    live graph that this module made on the default stream."""
-    leaves = _leaves(tensors)
-    if not leaves or not torch.cuda.is_current_stream_capturing():
+def _refuse_captured(nodes):
+    """Raises if a graph is captured while an accumulating node among the nodes
+    belongs to a live graph that this module made on the default stream."""
+    if not nodes or not torch.cuda.is_current_stream_capturing():
         return
-    for t in leaves:
-        made = torch.autograd.graph.get_gradient_edge(t).node.metadata.get("flce_stream")
-        if (made == _DEFAULT_STREAM
-                and torch._C._cuda_getCurrentRawStream(t.device.index) != _DEFAULT_STREAM):
+    for node in nodes:
+        if (node.metadata.get("flce_stream") == _DEFAULT_STREAM
+                and torch._C._cuda_getCurrentRawStream(node.variable.device.index)
+                != _DEFAULT_STREAM):
             raise RuntimeError(
                 "an eager result of this leaf is still alive on the default stream: a backward "
                 "over it cannot be captured; drop the result first, make it on a side stream, "
@@ -61,9 +63,17 @@ def _refuse_captured_leaves(*tensors):
 def _note_leaves(*tensors):
     """Notes the stream of a new graph on its leaves' accumulating nodes (kept
     alive by the graph, and with them the note)."""
-    for t in _leaves(tensors):
-        torch.autograd.graph.get_gradient_edge(t).node.metadata.setdefault(
-            "flce_stream", torch._C._cuda_getCurrentRawStream(t.device.index))
+    for node in _accumulators(tensors):
+        node.metadata.setdefault("flce_stream", torch._C._cuda_getCurrentRawStream(
+            node.variable.device.index))
+
+
+def _reached(node):
+    """Whether the running backward pass goes on to the accumulating node."""
+    try:
+        return torch._C._will_engine_execute_node(node)
+    except RuntimeError:  # of torch.autograd.grad, which asks for this leaf
+        return True
 
 
 class LinearCrossEntropy(torch.autograd.Function):
@@ -87,6 +97,9 @@ class LinearCrossEntropy(torch.autograd.Function):
 
     @staticmethod
     def backward(ctx, grad_logprob, grad_entropy):
+        # Of hidden and weight; a captured forward alone is always allowed.
+        _refuse_captured([node for node, _ in ctx.next_functions[:2]
+                          if hasattr(node, "variable") and _reached(node)])
         hidden, weight, labels, lse, entropy = ctx.saved_tensors
         n = hidden.shape[0]
 
@@ -149,7 +162,7 @@ def embedding(weight, tokens, layout="hv", scale=1.0, ignore_index=-100):
     bf16: the head's [H,V] (layout "hv", tied embeddings) or a table [V,H]
     ("vh"). Zero rows at ignore_index and at ids outside the vocabulary.
     Differentiable with respect to weight (gradient in bf16)."""
-    _refuse_captured_leaves(weight)
+    _refuse_captured(_accumulators([weight]))
     hidden = Embedding.apply(weight, tokens, layout, scale, ignore_index)
     _note_leaves(weight)
     return hidden
@@ -192,7 +205,7 @@ def policy_loss(logprob, labels, old_logprob, advantages, entropy=None, ref_logp
     e.g. the outputs of ``linear_cross_entropy(..., reduction="none")``;
     old_logprob, ref_logprob and advantages are constants."""
     flce._policy_options(**options)  # refuses what the backward could not take
-    _refuse_captured_leaves(logprob, entropy)
+    _refuse_captured(_accumulators([logprob, entropy]))
     out = PolicyLoss.apply(logprob, entropy, labels, old_logprob, advantages, ref_logprob,
                            cu_seqlens, options)
     _note_leaves(logprob, entropy)
@@ -233,7 +246,7 @@ def preference_loss(logprob, labels, cu_seqlens, ref_logprob=None, **options):
     differentiable). Differentiable with respect to logprob; ref_logprob is a
     constant."""
     flce._preference_options(**options)  # refuses what the backward could not take
-    _refuse_captured_leaves(logprob)
+    _refuse_captured(_accumulators([logprob]))
     out = PreferenceLoss.apply(logprob, labels, cu_seqlens, ref_logprob, options)
     _note_leaves(logprob)
     return out

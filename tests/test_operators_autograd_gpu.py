@@ -102,3 +102,37 @@ def test_captured_step_with_its_warm_up_still_bound():
         for x, y in zip(got, want):
             assert torch.equal(x, y)
     assert bool(torch.isfinite(bound))
+
+
+@pytest.mark.parametrize("holder", ["head", "embedding"])
+def test_captured_backward_of_the_head_is_refused_over_a_live_graph(holder, monkeypatch):
+    """The head's captured backward over a leaf that a result of the default
+    stream holds; its captured forward alone is not refused, nor a backward that
+    needs no gradient of that leaf, nor one after the result is dropped."""
+    w, tok, lab, old, adv, cu = T._step_tensors()
+    weight = w.requires_grad_(True)
+    hidden = torch.randn(T.N, T.H, device=w.device).to(torch.bfloat16)
+    h = hidden.clone().requires_grad_(True)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+
+    def eager():
+        if holder == "embedding":
+            return function.embedding(weight, tok)
+        return function.linear_cross_entropy(hidden, weight, lab)[0]
+
+    alive = eager()
+    lp, ent = _captured(monkeypatch, side,
+                        lambda: function.linear_cross_entropy(h, weight, lab))
+    with pytest.raises(RuntimeError, match="still alive"):
+        _captured(monkeypatch, side, lambda: (lp + ent).backward(retain_graph=True))
+    with pytest.raises(RuntimeError, match="still alive"):
+        _captured(monkeypatch, side, lambda: torch.autograd.grad(lp, [weight], retain_graph=True))
+    _captured(monkeypatch, side, lambda: torch.autograd.grad(lp, [h], retain_graph=True))
+    with torch.cuda.stream(side):
+        (lp + ent).backward()  # not captured: allowed
+    assert weight.grad is not None and h.grad is not None
+    del alive, lp, ent
+    _captured(monkeypatch, side,
+              lambda: function.linear_cross_entropy(h.detach(), weight, lab)[0].backward())
+    torch.cuda.synchronize()
