@@ -21,7 +21,9 @@ one: a captured backward over a leaf that an eager graph made there still holds
 would reach out of the capture, which ends the process. While such a result of
 this module on the same leaf lives (drop it first), ``embedding``,
 ``policy_loss`` and ``preference_loss`` refuse the call, and the backward of
-``linear_cross_entropy`` raises.
+``linear_cross_entropy`` raises. Seen are leaves among the arguments and leaves
+that an argument is a cast, view or multiple of; not seen are leaves further
+back in the graph, and results that other operators made on a leaf first.
 """
 from __future__ import annotations
 
@@ -35,21 +37,35 @@ __all__ = ["LinearCrossEntropy", "linear_cross_entropy", "Embedding", "embedding
            "PolicyLoss", "policy_loss", "PreferenceLoss", "preference_loss"]
 
 
+def _accumulator(node):
+    """The accumulating node of a leaf: the node itself, or the one behind it where
+    up to eight operations of one input each (casts, views, scalings) lie between;
+    else None."""
+    for _ in range(9):
+        if hasattr(node, "variable"):
+            return node
+        behind = [n for n, _ in node.next_functions if n is not None]
+        if len(behind) != 1:
+            break
+        node = behind[0]
+    return None
+
+
 def _accumulators(tensors):
-    """The accumulating nodes of the leaves among the tensors."""
-    return [torch.autograd.graph.get_gradient_edge(t).node for t in tensors
-            if isinstance(t, torch.Tensor) and t.is_cuda and t.is_leaf and t.requires_grad
-            ] if torch.is_grad_enabled() else []
+    """The accumulating nodes of the leaves that the tensors are or are cast from."""
+    if not torch.is_grad_enabled():
+        return []
+    nodes = [_accumulator(torch.autograd.graph.get_gradient_edge(t).node) for t in tensors
+             if isinstance(t, torch.Tensor) and t.is_cuda and t.requires_grad]
+    return [node for node in nodes if node is not None]
 
 
 _DEFAULT_STREAM = 0  # raw handle
 
 
 def _refuse_captured(nodes):
-    """Raises if a graph is captured while an accumulating node among the nodes
-    belongs to a live graph that this module made on the default stream."""
-    if not nodes or not torch.cuda.is_current_stream_capturing():
-        return
+    """Under capture: raises if an accumulating node among the nodes belongs to a
+    live graph that this module made on the default stream."""
     for node in nodes:
         if (node.metadata.get("flce_stream") == _DEFAULT_STREAM
                 and torch._C._cuda_getCurrentRawStream(node.variable.device.index)
@@ -58,6 +74,11 @@ def _refuse_captured(nodes):
                 "an eager result of this leaf is still alive on the default stream: a backward "
                 "over it cannot be captured; drop the result first, make it on a side stream, "
                 "or use torch.no_grad() for the forward alone")
+
+
+def _refuse_captured_leaves(*tensors):
+    if getattr(tensors[0], "is_cuda", False) and torch.cuda.is_current_stream_capturing():
+        _refuse_captured(_accumulators(tensors))
 
 
 def _note_leaves(*tensors):
@@ -97,9 +118,10 @@ class LinearCrossEntropy(torch.autograd.Function):
 
     @staticmethod
     def backward(ctx, grad_logprob, grad_entropy):
-        # Of hidden and weight; a captured forward alone is always allowed.
-        _refuse_captured([node for node, _ in ctx.next_functions[:2]
-                          if hasattr(node, "variable") and _reached(node)])
+        if torch.cuda.is_current_stream_capturing():
+            # Of hidden and weight; a captured forward alone is always allowed.
+            leaves = [_accumulator(node) for node, _ in ctx.next_functions[:2] if node is not None]
+            _refuse_captured([node for node in leaves if node is not None and _reached(node)])
         hidden, weight, labels, lse, entropy = ctx.saved_tensors
         n = hidden.shape[0]
 
@@ -162,7 +184,7 @@ def embedding(weight, tokens, layout="hv", scale=1.0, ignore_index=-100):
     bf16: the head's [H,V] (layout "hv", tied embeddings) or a table [V,H]
     ("vh"). Zero rows at ignore_index and at ids outside the vocabulary.
     Differentiable with respect to weight (gradient in bf16)."""
-    _refuse_captured(_accumulators([weight]))
+    _refuse_captured_leaves(weight)
     hidden = Embedding.apply(weight, tokens, layout, scale, ignore_index)
     _note_leaves(weight)
     return hidden
@@ -205,7 +227,7 @@ def policy_loss(logprob, labels, old_logprob, advantages, entropy=None, ref_logp
     e.g. the outputs of ``linear_cross_entropy(..., reduction="none")``;
     old_logprob, ref_logprob and advantages are constants."""
     flce._policy_options(**options)  # refuses what the backward could not take
-    _refuse_captured(_accumulators([logprob, entropy]))
+    _refuse_captured_leaves(logprob, entropy)
     out = PolicyLoss.apply(logprob, entropy, labels, old_logprob, advantages, ref_logprob,
                            cu_seqlens, options)
     _note_leaves(logprob, entropy)
@@ -246,7 +268,7 @@ def preference_loss(logprob, labels, cu_seqlens, ref_logprob=None, **options):
     differentiable). Differentiable with respect to logprob; ref_logprob is a
     constant."""
     flce._preference_options(**options)  # refuses what the backward could not take
-    _refuse_captured(_accumulators([logprob]))
+    _refuse_captured_leaves(logprob)
     out = PreferenceLoss.apply(logprob, labels, cu_seqlens, ref_logprob, options)
     _note_leaves(logprob)
     return out

@@ -136,3 +136,44 @@ def test_captured_backward_of_the_head_is_refused_over_a_live_graph(holder, monk
     _captured(monkeypatch, side,
               lambda: function.linear_cross_entropy(h.detach(), weight, lab)[0].backward())
     torch.cuda.synchronize()
+
+
+def test_leaves_behind_casts_and_views_are_seen(monkeypatch):
+    """A master weight in fp32, cast (and transposed) for the call, has the
+    gradient's node of a leaf as much as a direct argument."""
+    w, tok, lab, old, adv, cu = T._step_tensors()
+    master = w.float().requires_grad_(True)
+    wide = old.double().requires_grad_(True)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    hidden = torch.randn(T.N, T.H, device=w.device).to(torch.bfloat16)
+
+    def embed():
+        return function.embedding(master.to(torch.bfloat16), tok)
+
+    def table():
+        return function.embedding((2.0 * master).to(torch.bfloat16).t().contiguous(), tok,
+                                  layout="vh")
+
+    def head():
+        return function.linear_cross_entropy(hidden, master.to(torch.bfloat16), lab)[0]
+
+    def policy():
+        return function.policy_loss(wide.float().view(-1), lab, old, adv, cu_seqlens=cu,
+                                    advantages_per_sequence=True)[0]
+
+    def preference():
+        return function.preference_loss(wide.float(), lab, cu)[0]
+
+    for made, call in ((embed, table), (head, embed), (policy, preference), (preference, policy)):
+        alive = made()
+        with pytest.raises(RuntimeError, match="still alive"):
+            _captured(monkeypatch, side, call)
+        del alive
+        _captured(monkeypatch, side, call)
+    alive = table()
+    with pytest.raises(RuntimeError, match="still alive"):
+        _captured(monkeypatch, side, lambda: head().backward())
+    del alive
+    _captured(monkeypatch, side, lambda: head().backward())
+    torch.cuda.synchronize()
