@@ -580,7 +580,10 @@ flce_status_t flce_get_status(const void* workspace, int64_t* invalid_labels, vo
 /* Static English text for a status code. */
 const char* flce_status_string(flce_status_t status);
 
-/* Library version, major*10000 + minor*100 + patch. */
+/* Library version, major*10000 + minor*100 + patch. It changes with the layout of
+ * an existing structure or the meaning of an existing call. Entry points added
+ * beside these, such as the embedding and the losses after version 212, leave it:
+ * a program that loads the library at run time looks for their symbols. */
 int flce_version(void);
 
 /* Measurement hooks. When enabled, every kernel the library launches is
