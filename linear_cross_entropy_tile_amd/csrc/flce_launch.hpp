@@ -49,6 +49,15 @@ struct Profiler {
     if (hipEventCreate(&e) != hipSuccess) return nullptr;
     return e;
   }
+  // Back into the pool; destroyed when there is no memory for that.
+  void give(hipEvent_t e) {
+    if (e == nullptr) return;
+    try {
+      pool.push_back(e);
+    } catch (...) {
+      (void)hipEventDestroy(e);
+    }
+  }
   void drain() {
     for (auto& p : pending) {
       float t = 0.f;
@@ -56,8 +65,8 @@ struct Profiler {
         launches[p.kind] += 1;
         ms[p.kind] += t;
       }
-      pool.push_back(p.a);
-      pool.push_back(p.b);
+      give(p.a);
+      give(p.b);
     }
     pending.clear();
   }
@@ -67,7 +76,8 @@ inline Profiler& prof() {
   return *p;
 }
 
-// Launches through `fn` on `st`, bracketed by events when timing is on.
+// Launches through `fn` on `st`, bracketed by events when timing is on. A sample
+// that there is no memory for is dropped: no exception leaves the C entry points.
 template <class F>
 flce_status_t launch(int kind, hipStream_t st, F fn) {
   Profiler& P = prof();
@@ -80,13 +90,22 @@ flce_status_t launch(int kind, hipStream_t st, F fn) {
     if (a != nullptr) (void)hipEventRecord(a, st);
   }
   fn();
-  if (hipGetLastError() != hipSuccess) return FLCE_ERR_HIP;
-  if (timed && a != nullptr && b != nullptr) {
-    (void)hipEventRecord(b, st);
+  const bool ok = hipGetLastError() == hipSuccess;
+  if (timed) {
+    bool kept = ok && a != nullptr && b != nullptr;
+    if (kept) (void)hipEventRecord(b, st);
     std::lock_guard<std::mutex> g(P.mu);
-    P.pending.push_back({kind, a, b});
+    try {
+      if (kept) P.pending.push_back({kind, a, b});
+    } catch (...) {
+      kept = false;
+    }
+    if (!kept) {
+      P.give(a);
+      P.give(b);
+    }
   }
-  return FLCE_OK;
+  return ok ? FLCE_OK : FLCE_ERR_HIP;
 }
 
 #define FLCE_TRY(x)                    \
