@@ -101,17 +101,18 @@ def _code_only(text: str) -> str:
     return " ".join(text.split())
 
 
-# The sources of the head's kernels, plan and launches; the other operators'
-# sources do not change its traffic.
-HEAD_SOURCES = ("flce_api.hip", "flce_gemm.hpp", "flce_kernels.hpp", "flce_layout.hpp",
-                "flce_plan.hpp")
+# The sources of the head's kernels, plan and launches, relative to the root; the other
+# operators' sources do not change its traffic.
+CSRC = "linear_cross_entropy_tile_amd/csrc/"
+HEAD_SOURCES = (CSRC + "flce_api.hip", CSRC + "flce_gemm.hpp", CSRC + "flce_kernels.hpp",
+                CSRC + "flce_launch.hpp", CSRC + "flce_layout.hpp", CSRC + "flce_plan.hpp",
+                "include/flce.h")
 
 
 def kernel_source_hash() -> str:
     """SHA-256 over the code (comments and blank space dropped) of the head's
     kernel and boundary sources, in a fixed order."""
-    csrc = os.path.join(ROOT, "linear_cross_entropy_tile_amd", "csrc")
-    files = [os.path.join(csrc, f) for f in HEAD_SOURCES]
+    files = [os.path.join(ROOT, f) for f in HEAD_SOURCES]
     h = hashlib.sha256()
     for f in files:
         h.update(os.path.basename(f).encode())
