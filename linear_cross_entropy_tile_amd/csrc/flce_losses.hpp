@@ -461,11 +461,10 @@ struct PolicyLoss {
   __device__ static double upstream(const LossArgs<PolicyLoss>& a) {
     return a.out.grad_loss != nullptr ? (double)a.out.grad_loss[0] : 1.0;
   }
-  // Gradients of token t of sequence s; of one that takes no part (s < 0): none.
   __device__ static void grad(const LossArgs<PolicyLoss>& a, const Raw& r, double scale, int64_t t,
-                              int64_t s, float none) {
+                              int64_t s) {
     const In& in = a.in;
-    float glp = none, gent = none;
+    float glp = 0.f, gent = 0.f;
     if (s >= 0) {
       double df, f;
       if (in.by_sequence) {
@@ -581,8 +580,8 @@ struct PreferenceLoss {
     return one ? (double)a.out.grad_loss[0] : 1.0;
   }
   __device__ static void grad(const LossArgs<PreferenceLoss>& a, const Raw&, double scale,
-                              int64_t t, int64_t s, float none) {
-    double g = none;
+                              int64_t t, int64_t s) {
+    double g = 0.0;
     if (s >= 0) {
       g = scale * a.state[s];
       if (a.in.reduction == FLCE_REDUCTION_NONE && a.out.grad_loss != nullptr)
@@ -801,20 +800,20 @@ __device__ __forceinline__ void tile_grads(const LossArgs<Loss>& a, int64_t tile
   TileRows<Loss, ROWS, Loss::kGradReads> in;
   in.load(a, t0);
   const TileSeqs r = tile_sequences(a.cu, a.B, a.N, t0, t1);
-  // The factor is NaN after bad offsets, and only then. Tokens may lie in no
-  // sequence there, yet every one with a valid label has a NaN gradient.
   const double factor = batch_factor(a);
   const double scale = Loss::upstream(a) * factor;
-  const float lost = factor != factor ? __builtin_nanf("") : 0.f;
+  // The factor is NaN after bad offsets, and only then. A valid token may lie in no
+  // sequence there; it goes with the first, and so has a NaN gradient as all others.
+  const int64_t none = factor != factor ? 0 : -1;
 #pragma unroll
   for (int j = 0; j < ROWS; ++j) {
     const int tl = j * 64 + (threadIdx.x & 63);
     const int rank = token_rank(a.cu, r, t0, tl);
     const int64_t t = t0 + tl;
     if (t >= a.N) continue;
-    const bool valid = label_valid(in.y[j], a.ignore_index, a.V);
-    Loss::grad(a, in.raw[j], scale, t, valid && rank >= 0 ? r.s0 + rank : -1,
-               valid ? lost : 0.f);
+    const int64_t s = rank >= 0 ? r.s0 + rank : none;
+    const bool valid = s >= 0 && label_valid(in.y[j], a.ignore_index, a.V);
+    Loss::grad(a, in.raw[j], scale, t, valid ? s : -1);
   }
 }
 
