@@ -593,8 +593,10 @@ struct PreferenceLoss {
 
 // ---- the three steps ----------------------------------------------------------------
 
-// A tile's inputs, lane l having the tokens t0 + 64 j + l; all loads are issued at
-// once.
+// A tile's inputs, lane l having the tokens t0 + 64 j + l. The loads are not all in
+// flight at once: those of an optional input sit in branches that wait for it (in the
+// policy loss two waits a row, reference and entropy, before the offsets are asked
+// for), and a token-level advantage is loaded with the token's terms.
 template <class Loss, int ROWS, bool READ>
 struct TileRows {
   typename Loss::Raw raw[ROWS];
@@ -616,8 +618,8 @@ struct TileRows {
 // segments, the open segment carried to the next row, and the lane with a
 // sequence's last token in the tile has its share. No LDS either way, so the
 // occupancy is the registers'; token terms in LDS and sums over them took 36 us where
-// this takes 24 (policy loss, 2.07 M tokens in 1000 sequences: 58 MB, 2.4 TB/s).
-// 32768 tokens take 4.5 us.
+// this takes 24 (policy loss, 2.07 M tokens in 1000 sequences: 58 MB, 2.4 TB/s), which
+// its chain of loads and waits bounds rather than the memory. 32768 tokens take 4.6 us.
 template <class Loss, int ROWS>
 __device__ __forceinline__ void tile_parts(const LossArgs<Loss>& a, int64_t tile) {
   using Token = typename Loss::Token;
