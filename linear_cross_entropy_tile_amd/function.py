@@ -38,12 +38,12 @@ __all__ = ["LinearCrossEntropy", "linear_cross_entropy", "Embedding", "embedding
 
 
 def _accumulator(node):
-    """The accumulating node of a leaf: the node itself, or the one behind it where
-    up to eight operations of one input each (casts, views, scalings) lie between;
-    else None."""
+    """The accumulating node of a leaf on a GPU: the node itself, or the one behind it
+    where up to eight operations of one input each (casts, views, scalings) lie
+    between; else None."""
     for _ in range(9):
-        if hasattr(node, "variable"):
-            return node
+        if node.name() == "torch::autograd::AccumulateGrad":
+            return node if node.variable.is_cuda else None
         behind = [n for n, _ in node.next_functions if n is not None]
         if len(behind) != 1:
             break

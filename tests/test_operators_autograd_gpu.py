@@ -177,3 +177,36 @@ def test_leaves_behind_casts_and_views_are_seen(monkeypatch):
     del alive
     _captured(monkeypatch, side, lambda: head().backward())
     torch.cuda.synchronize()
+
+
+class _Halved(torch.autograd.Function):
+    """A function of the caller's with an attribute of its own on the node."""
+
+    @staticmethod
+    def forward(ctx, x):
+        ctx.variable = "its own"
+        return 0.5 * x
+
+    @staticmethod
+    def backward(ctx, g):
+        return 0.5 * g
+
+
+def test_leaves_on_the_host_and_nodes_of_other_functions():
+    """A leaf in host memory that the argument is copied from, and a node of
+    another function in between."""
+    w, tok, lab, old, adv, cu = T._step_tensors()
+    host = w.float().cpu().requires_grad_(True)
+    out = function.embedding(host.to(w.device, torch.bfloat16), tok)
+    out.backward(torch.ones_like(out))
+    ones = torch.ones_like(out)
+    want = flce.embedding_backward(ones, tok, T.V)
+    assert torch.equal(host.grad, want.float().cpu())
+    lp = old.cpu().requires_grad_(True)
+    for halved in (lp.to(w.device) * 0.5, _Halved.apply(lp.to(w.device)),
+                   _Halved.apply(old.clone().requires_grad_(True))):
+        loss, _ = function.policy_loss(halved, lab, old, adv, cu_seqlens=cu,
+                                       advantages_per_sequence=True)
+        loss.backward()
+        function.preference_loss(halved.detach().requires_grad_(True), lab, cu)[0].backward()
+    assert bool(torch.isfinite(lp.grad).all())
