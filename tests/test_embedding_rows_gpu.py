@@ -66,3 +66,33 @@ def test_accumulation_stores_to_used_ids_only(V, hidden, dtype, layout):
     for v in np.nonzero(used)[0]:  # whole numbers below 2^8 in every partial sum: exact
         want[v] += g[torch.from_numpy(tok == v)].float().sum(0).to(dtype)
     assert torch.equal(got.view(view), want.view(view))
+
+
+@pytest.mark.parametrize("layout", ["hv", "vh"])
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+def test_two_streams_add_to_neighbouring_ids(dtype, layout):
+    """Two batches without a common id, alternating within every strip and every
+    group of 16 bytes, added on two streams at once to one tensor."""
+    N, H, V = 20000, 512, 4000
+    dev = G.dev()
+    gen = torch.Generator(device="cuda")
+    gen.manual_seed(5)
+    base = torch.randint(-8, 9, (V, H) if layout == "vh" else (H, V), generator=gen, device=dev)
+    acc = base.to(dtype)
+    toks = [2 * torch.randint(0, V // 2, (N,), generator=gen, device=dev) + k for k in (0, 1)]
+    ups = [torch.randint(-1, 2, (N, H), generator=gen, device=dev).to(torch.bfloat16)
+           for _ in toks]
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    for s in streams:
+        s.wait_stream(torch.cuda.current_stream())
+    for s, tok, up in zip(streams, toks, ups):
+        with torch.cuda.stream(s):
+            flce.embedding_backward(up, tok, V, layout=layout, grad_weight=acc)
+    for s in streams:
+        torch.cuda.current_stream().wait_stream(s)
+    want = torch.zeros(V, H, device=dev)
+    for tok, up in zip(toks, ups):  # whole numbers far below 2^8: exact
+        want.index_add_(0, tok, up.float())
+    want = base + (want if layout == "vh" else want.t())
+    assert want.abs().max() < 256
+    assert torch.equal(acc.float(), want)
