@@ -97,7 +97,8 @@ typedef enum {
   FLCE_ERR_INVALID_LABEL = 8,     /* reported only by flce_get_status */
   FLCE_ERR_BAD_OPTION = 9,        /* z_loss_scale negative or not finite, unknown grad_dtype,
                                    * class_weight under NONE, entropy_per_token not 0 or 1; an
-                                   * embedding, policy or preference option outside its range */
+                                   * embedding, policy, preference, process or AdamW option
+                                   * outside its range */
   FLCE_ERR_TOO_LARGE = 10         /* flce_forward_noalloc: the shape needs more scratch than
                                    * FLCE_NOALLOC_SCRATCH_BYTES */
 } flce_status_t;
@@ -570,9 +571,199 @@ flce_status_t flce_preference_loss_forward_backward(
     float* chosen_reward, float* rejected_reward, float* grad_logprob, void* workspace,
     size_t workspace_bytes, void* stream);
 
+/* ---- Logits to sample from --------------------------------------------------------
+ * The head's logits for a few rows, e.g. the last positions of the sequences that
+ * are being generated:
+ *   z_iv = cap(sum_h hidden[i,h] weight[h,v] + bias[v]),
+ *   cap(z) = c * tanh(z / c) if softcap c > 0, else z.
+ * The products are summed in fp32 in a fixed order and rounded once to the
+ * output's type. For many tokens there is flce_forward, which never writes the
+ * logits: N <= 1024 here. */
+
+/* Workspace bytes (host only). */
+flce_status_t flce_logits_workspace_size(int64_t N, int64_t H, int64_t V, size_t* bytes);
+
+/* hidden device bf16 [N,H], weight device bf16 [H,V], both 16-byte aligned (H a
+ * multiple of 8, V any size); bias device fp32 [V] or NULL; out device [N,V] of
+ * out_dtype (FLCE_GRAD_BF16 or FLCE_GRAD_F32), row i from element i * ld_out on
+ * (ld_out >= V), aligned to its elements. */
+flce_status_t flce_logits(const void* hidden, const void* weight, const float* bias, int64_t N,
+                          int64_t H, int64_t V, float softcap, int out_dtype, void* out,
+                          int64_t ld_out, void* workspace, size_t workspace_bytes, void* stream);
+
+/* ---- Penalties, biases and masks on logits ------------------------------------------
+ * What a sampler does to a row of logits before it draws a token. Row i has a
+ * history of tokens, the first prompt_lengths[i] of which are its prompt and the
+ * others generated. With n(v) the occurrences of id v among the generated ones,
+ * a logit x of id v becomes, in this order,
+ *   x > 0 ? x / r : x * r          if v is anywhere in the history (repetition r)
+ *   x - frequency * n(v), then x - presence if n(v) > 0
+ *   x + bias[v] + the sum of the row's listed biases of v (in the list's order)
+ *   x / temperature                (not if the temperature is 0: such a row is for
+ *                                   its largest value)
+ *   -inf                           if the row's mask does not allow v, whatever x is
+ * in fp32, where the divisions are products with the fp32 reciprocal, and is
+ * rounded once to the output's type. Each row also gets, of the logits as they are
+ * returned,
+ *   lse      logsumexp (-inf if nothing is allowed), so that out[t] - lse is the
+ *            log-probability with which token t is drawn (the policy loss's
+ *            old_logprob);
+ *   entropy  lse - sum p x (0 if nothing is allowed, NaN if lse is not finite
+ *            otherwise);
+ *   greedy   the first id of the largest value (the first NaN, if there is one; -1
+ *            if nothing is allowed). */
+typedef struct flce_process_options {
+  int64_t ignore_index;    /* token id of a history or of listed biases to pass over */
+  /* History: tokens device int64. Packed (tokens_stride 0): row i is tokens
+   * [offsets[i], offsets[i+1]) of the tokens_size ones (offsets [N+1], within
+   * [0, tokens_size] and not decreasing). Padded (tokens_stride > 0, N * tokens_stride
+   * <= tokens_size): row i is the first offsets[i] tokens (in [0, tokens_stride]) from
+   * i * tokens_stride on (offsets [N]). Both NULL: no history. */
+  const int64_t* tokens;
+  int64_t tokens_size, tokens_stride;
+  const int64_t* offsets;
+  const int64_t* prompt_lengths;  /* [N], cut to the history; NULL: 0 */
+  /* Device fp32 [N], or NULL for the value of all rows below. */
+  const float* repetition;
+  const float* presence;
+  const float* frequency;
+  const float* temperatures;
+  double repetition_penalty;      /* > 0, 1: off */
+  double presence_penalty;        /* 0: off */
+  double frequency_penalty;       /* 0: off */
+  double temperature;             /* >= 0, 1: off */
+  const float* bias;              /* device fp32 [V] (bias_stride 0) or [N, bias_stride], or NULL */
+  int64_t bias_stride;
+  /* Listed biases: row i's are the pairs [bias_offsets[i], bias_offsets[i+1]) of the
+   * bias_count ones, or NULL. */
+  const int64_t* bias_tokens;
+  const float* bias_values;
+  int64_t bias_count;
+  const int64_t* bias_offsets;    /* [N+1], within [0, bias_count] and not decreasing */
+  const int32_t* allowed;         /* device bits: id v of a row is allowed if bit v % 32 of word v / 32
+                                   * is set; one row for all (allowed_stride 0) or rows of
+                                   * allowed_stride words; NULL: all allowed */
+  int64_t allowed_stride;
+  int logits_dtype, out_dtype;    /* FLCE_GRAD_BF16 or FLCE_GRAD_F32 */
+} flce_process_options_t;
+
+/* Workspace bytes of the two calls (host only). */
+flce_status_t flce_process_workspace_size(int64_t N, int64_t V, size_t* bytes);
+
+/* logits device [N,V] of logits_dtype, row i from element i * ld on (ld >= V); out
+ * likewise of out_dtype and ld_out (it may be logits itself, of the same type and
+ * ld); lse and entropy device fp32 [N], greedy device int64 [N], each or NULL. All
+ * aligned to their elements. Tokens of a history (if there is a penalty) or of listed
+ * biases that are neither ignore_index nor in [0, V) are passed over and counted in the
+ * status word. A row whose offsets are bad (see above) counts there as one, and its
+ * outputs are NaN and -1. */
+flce_status_t flce_process_logits(const void* logits, int64_t ld, int64_t N, int64_t V,
+                                  const flce_process_options_t* opt, void* out, int64_t ld_out,
+                                  float* lse, float* entropy, int64_t* greedy, void* workspace,
+                                  size_t workspace_bytes, void* stream);
+
+/* Upstream gradients of a forward's outputs, each NULL for zero: of the returned logits
+ * (type out_dtype, rows of ld_grad_out), of lse and of entropy (device fp32 [N]). The
+ * latter two need what the forward returned: out (rows of ld_out), lse and, for
+ * grad_entropy, entropy. */
+typedef struct flce_process_grads {
+  const void* grad_out;
+  int64_t ld_grad_out;
+  const float* grad_lse;
+  const float* grad_entropy;
+  const void* out;
+  int64_t ld_out;
+  const float* lse;
+  const float* entropy;
+} flce_process_grads_t;
+
+/* grad_logits device [N,V] (type logits_dtype, rows of ld_grad) = what a logit is
+ * multiplied by (r where x <= 0 and 1 / r where x > 0 for seen ids, then
+ * 1 / temperature; 0 where the mask does not allow it) times
+ *   grad_out + p (grad_lse - grad_entropy (x' - lse + entropy)),  p = exp(x' - lse)
+ * with x' the returned logit (no second term where p is 0); NaN in rows of bad
+ * offsets. logits and opt are those that went into the forward, whose output must not
+ * have been written over them. grad_logits may be grad_out itself, of the same type
+ * and ld. Listed and dense biases play no part and are not looked at. */
+flce_status_t flce_process_logits_backward(const flce_process_grads_t* grads, const void* logits,
+                                           int64_t ld, int64_t N, int64_t V,
+                                           const flce_process_options_t* opt, void* grad_logits,
+                                           int64_t ld_grad, void* workspace,
+                                           size_t workspace_bytes, void* stream);
+
+/* ---- Norm of the gradients and AdamW --------------------------------------------------
+ * The update that ends a training step, over many tensors in a few launches, with
+ * the step's count, the clip factor and (optionally) the learning rate on the
+ * device, so that a captured step stays right when it is replayed. The arrays of
+ * pointers and sizes are host memory, read before the call returns. */
+
+/* Workspace bytes of flce_grad_norm (host only): sizes[i] values in tensor i. */
+flce_status_t flce_grad_norm_workspace_size(const int64_t* sizes, int64_t count, size_t* bytes);
+
+/* norm (device fp32 [1]) = sqrt(sum of squares) over all values of the count tensors
+ * (device, type dtypes[i], aligned to their elements), summed in float64 in a fixed
+ * order. scale (device fp32 [1], or NULL) = min(1, max_norm / norm), 1 if max_norm is
+ * 0, and NaN if the norm is not finite. */
+flce_status_t flce_grad_norm(const void* const* grads, const int64_t* sizes, const int* dtypes,
+                             int64_t count, double max_norm, float* norm, float* scale,
+                             void* workspace, size_t workspace_bytes, void* stream);
+
+enum { FLCE_STATE_F32 = 0, FLCE_STATE_8BIT = 1 };
+enum { FLCE_ROUND_NEAREST = 0, FLCE_ROUND_STOCHASTIC = 1 };
+
+/* The tensors of an update: host arrays of `count` entries. Tensor i has sizes[i]
+ * values, its pointers are device pointers aligned to their elements; sizes of 0 are
+ * passed over. With FLCE_STATE_8BIT the states are e4m3 codes (OCP: the largest is 448)
+ * in blocks of 256 values from the tensor's start on, and exp_avg_scales and
+ * exp_avg_sq_scales (fp32, one a block) what a code is multiplied by; exp_avg_sqs then
+ * holds the root of the second moment. */
+typedef struct flce_adamw_list {
+  int64_t count;
+  const int64_t* sizes;
+  void* const* params;           /* of param_dtypes; written */
+  const void* const* grads;      /* of grad_dtypes */
+  void* const* masters;          /* fp32 copies that the update is made on (a parameter then is
+                                  * its copy rounded to the nearest); NULL, or NULL entries, for
+                                  * none; bf16 parameters only */
+  void* const* exp_avgs;         /* fp32 or codes */
+  void* const* exp_avg_sqs;
+  void* const* exp_avg_scales;   /* 8-bit states only */
+  void* const* exp_avg_sq_scales;
+  const int* param_dtypes;       /* FLCE_GRAD_BF16 or FLCE_GRAD_F32 */
+  const int* grad_dtypes;
+} flce_adamw_list_t;
+
+typedef struct flce_adamw_options {
+  double lr;               /* finite */
+  double beta1, beta2;     /* in [0, 1) */
+  double eps;              /* >= 0 */
+  double weight_decay;     /* finite */
+  int state_dtype;         /* FLCE_STATE_* */
+  int rounding;            /* FLCE_ROUND_*: of bf16 weights without a master copy, and of codes */
+  uint64_t seed;           /* of stochastic rounding */
+} flce_adamw_options_t;
+
+/* Workspace bytes of flce_adamw_step (host only). */
+size_t flce_adamw_workspace_size(void);
+
+/* With t = step[0] + 1 (step device int64 [1], then set to t), s = grad_scale[0]
+ * (device fp32 [1]; NULL: 1) and lr = lr_device[0] (device fp32 [1]; NULL: opt->lr),
+ * for every value in fp32:
+ *   g = s grad,  m = beta1 m + (1 - beta1) g,  v = beta2 v + (1 - beta2) g^2,
+ *   p = (1 - lr weight_decay) p - lr / (1 - beta1^t) m / (sqrt(v) / sqrt(1 - beta2^t) + eps).
+ * If s is not finite (an overflow in the backward), nothing is changed, step among
+ * it. In 8-bit states a block's scale is its largest magnitude a times 1 / 448 and
+ * its codes are those of the values times 448 (1 / a) (all 0 if a is below 2^-100), in
+ * fp32; a second moment above 0 has a code above 0.
+ * Stochastic rounding goes up with the probability of the part cut off, by 16 bits
+ * of a hash of the seed, t, the tensor's index and the value's. */
+flce_status_t flce_adamw_step(const flce_adamw_list_t* list, const flce_adamw_options_t* opt,
+                              const float* lr_device, const float* grad_scale, int64_t* step,
+                              void* workspace, size_t workspace_bytes, void* stream);
+
 /* Reads the status word that the last call with this workspace left, after
  * synchronising `stream`. *invalid_labels (may be NULL) receives the number of
- * labels (embedding: tokens) that were neither ignore_index nor in [0, V), or of
+ * labels (embedding, processing of logits: tokens) that were neither ignore_index nor in [0, V), or of
  * bad sequence offsets (losses); returns FLCE_ERR_INVALID_LABEL if that number is
  * not 0, else FLCE_OK. */
 flce_status_t flce_get_status(const void* workspace, int64_t* invalid_labels, void* stream);

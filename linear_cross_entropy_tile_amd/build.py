@@ -8,7 +8,8 @@ import subprocess
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
 LIB = os.path.join(PKG, "libflce.so")
-SOURCES = [os.path.join(PKG, "csrc", "flce_api.hip"), os.path.join(PKG, "csrc", "flce_ops.hip")]
+SOURCES = [os.path.join(PKG, "csrc", name)
+           for name in ("flce_api.hip", "flce_ops.hip", "flce_step.hip")]
 HEADERS = [os.path.join(ROOT, "include", "flce.h"),
            os.path.join(PKG, "csrc", "flce_layout.hpp"),
            os.path.join(PKG, "csrc", "flce_plan.hpp"),
@@ -17,7 +18,12 @@ HEADERS = [os.path.join(ROOT, "include", "flce.h"),
            os.path.join(PKG, "csrc", "flce_launch.hpp"),
            os.path.join(PKG, "csrc", "flce_ops_plan.hpp"),
            os.path.join(PKG, "csrc", "flce_losses.hpp"),
-           os.path.join(PKG, "csrc", "flce_embedding.hpp")]
+           os.path.join(PKG, "csrc", "flce_embedding.hpp"),
+           os.path.join(PKG, "csrc", "flce_vector.hpp"),
+           os.path.join(PKG, "csrc", "flce_step_plan.hpp"),
+           os.path.join(PKG, "csrc", "flce_logits.hpp"),
+           os.path.join(PKG, "csrc", "flce_process.hpp"),
+           os.path.join(PKG, "csrc", "flce_adamw.hpp")]
 
 # Packed fp32 VALU forms are switched off for all device code.
 HIPCC_FLAGS = ["--offload-arch=gfx950", "-O3", "-std=c++17", "-shared", "-fPIC",

@@ -30,33 +30,9 @@
 #include <type_traits>
 
 #include "flce_ops_plan.hpp"
+#include "flce_vector.hpp"
 
 namespace flce {
-
-typedef uint32_t eu32x4 __attribute__((ext_vector_type(4)));
-typedef float ef32x4 __attribute__((ext_vector_type(4)));
-typedef __bf16 ebf16x2 __attribute__((ext_vector_type(2)));
-typedef float ef32x2 __attribute__((ext_vector_type(2)));
-
-__device__ __forceinline__ float bf16_lo(uint32_t w) { return __builtin_bit_cast(float, w << 16); }
-__device__ __forceinline__ float bf16_hi(uint32_t w) {
-  return __builtin_bit_cast(float, w & 0xFFFF0000u);
-}
-// Two floats to a bf16 pair, nearest even.
-__device__ __forceinline__ uint32_t bf16_pair(float lo, float hi) {
-  return __builtin_bit_cast(uint32_t, __builtin_convertvector((ef32x2{lo, hi}), ebf16x2));
-}
-__device__ __forceinline__ void unpack8(const eu32x4& w, float (&v)[8]) {
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    v[2 * i] = bf16_lo(w[i]);
-    v[2 * i + 1] = bf16_hi(w[i]);
-  }
-}
-__device__ __forceinline__ eu32x4 pack8(const float (&v)[8]) {
-  return eu32x4{bf16_pair(v[0], v[1]), bf16_pair(v[2], v[3]), bf16_pair(v[4], v[5]),
-                bf16_pair(v[6], v[7])};
-}
 
 // W = 4 or 8 consecutive values of an array of bf16 or fp32, aligned to their
 // bytes or to 16.

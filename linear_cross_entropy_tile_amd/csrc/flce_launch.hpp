@@ -20,13 +20,15 @@ enum Kind {
   K_FWD_PREP, K_FWD_TILE, K_FWD_COMBINE, K_FWD_REDUCE, K_BWD_PREP, K_BWD_DLOGITS, K_BWD_DX,
   K_BWD_DW, K_DW_REDUCE, K_FILL, K_PACK_WEIGHT, K_PACK_HIDDEN, K_DX_FINALIZE, K_FUSED_TILE,
   K_FUSED_DLOGITS, K_BWD_DXDW, K_EMBED_SORT, K_EMBED_GATHER, K_EMBED_SEGMENTS, K_EMBED_GRAD,
-  K_LOSS_PARTS, K_LOSS_SEQUENCES, K_LOSS_GRADS, K_LOSS_SMALL, K_NUM
+  K_LOSS_PARTS, K_LOSS_SEQUENCES, K_LOSS_GRADS, K_LOSS_SMALL, K_LOGITS, K_PROCESS, K_PROCESS_ROWS,
+  K_PROCESS_GRAD, K_GRAD_NORM, K_ADAMW, K_NUM
 };
 inline const char* const kKindNames[K_NUM] = {
     "fwd_prep", "fwd_tile", "fwd_combine", "fwd_reduce", "bwd_prep", "bwd_dlogits", "bwd_dx",
     "bwd_dw", "dw_reduce", "fill_zero", "pack_weight", "pack_hidden", "dx_finalize", "fused_tile",
     "fused_dlogits", "bwd_dxdw", "embed_sort", "embed_gather", "embed_segments", "embed_grad",
-    "loss_parts", "loss_sequences", "loss_grads", "loss_small"};
+    "loss_parts", "loss_sequences", "loss_grads", "loss_small", "logits", "process",
+    "process_rows", "process_grad", "grad_norm", "adamw"};
 
 struct Pending {
   int kind;

@@ -21,6 +21,7 @@ missing or the device is not a GPU, calls raise.
 """
 from __future__ import annotations
 
+import array
 import ctypes
 import functools
 import os
@@ -44,6 +45,12 @@ __all__ = [
     "flce_preference_loss_forward_backward", "embedding", "embedding_backward", "policy_loss",
     "policy_loss_backward", "policy_loss_forward_backward", "preference_loss",
     "preference_loss_backward", "preference_loss_forward_backward",
+    "FLCE_STATE_F32", "FLCE_STATE_8BIT", "FLCE_ROUND_NEAREST", "FLCE_ROUND_STOCHASTIC",
+    "FlceProcessOptions", "FlceProcessGrads", "FlceAdamwList", "FlceAdamwOptions", "flce_logits_workspace_size",
+    "flce_logits", "flce_process_workspace_size", "flce_process_logits",
+    "flce_process_logits_backward", "flce_grad_norm_workspace_size", "flce_grad_norm",
+    "flce_adamw_workspace_size", "flce_adamw_step", "logits", "process_logits",
+    "process_logits_backward", "grad_norm", "adamw_state", "adamw_step",
 ]
 
 LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "libflce.so")
@@ -66,6 +73,12 @@ _KL_ESTIMATORS = {"k1": 0, "k2": 1, "k3": 2}
 _RATIO_LEVELS = {"token": 0, "sequence": 1}
 _PREFERENCE_KINDS = {"sigmoid": 0, "hinge": 1, "ipo": 2}
 MAX_VOCAB = (1 << 22) - 256
+FLCE_STATE_F32 = 0
+FLCE_STATE_8BIT = 1
+_STATE_DTYPES = {"f32": FLCE_STATE_F32, "8bit": FLCE_STATE_8BIT}
+FLCE_ROUND_NEAREST = 0
+FLCE_ROUND_STOCHASTIC = 1
+_ROUNDINGS = {"nearest": FLCE_ROUND_NEAREST, "stochastic": FLCE_ROUND_STOCHASTIC}
 
 STATUS_NAMES = {
     0: "FLCE_OK", 1: "FLCE_ERR_NULL_POINTER", 2: "FLCE_ERR_BAD_SHAPE",
@@ -106,6 +119,47 @@ class FlcePreferenceOptions(ctypes.Structure):
                 ("label_smoothing", ctypes.c_double), ("margin", ctypes.c_double),
                 ("kind", ctypes.c_int), ("length_normalize", ctypes.c_int),
                 ("reduction", ctypes.c_int)]
+
+
+
+class FlceProcessOptions(ctypes.Structure):
+    """flce_process_options_t."""
+    _fields_ = [("ignore_index", ctypes.c_int64), ("tokens", ctypes.c_void_p),
+                ("tokens_size", ctypes.c_int64), ("tokens_stride", ctypes.c_int64),
+                ("offsets", ctypes.c_void_p), ("prompt_lengths", ctypes.c_void_p),
+                ("repetition", ctypes.c_void_p), ("presence", ctypes.c_void_p),
+                ("frequency", ctypes.c_void_p), ("temperatures", ctypes.c_void_p),
+                ("repetition_penalty", ctypes.c_double), ("presence_penalty", ctypes.c_double),
+                ("frequency_penalty", ctypes.c_double), ("temperature", ctypes.c_double),
+                ("bias", ctypes.c_void_p), ("bias_stride", ctypes.c_int64),
+                ("bias_tokens", ctypes.c_void_p), ("bias_values", ctypes.c_void_p),
+                ("bias_count", ctypes.c_int64), ("bias_offsets", ctypes.c_void_p),
+                ("allowed", ctypes.c_void_p), ("allowed_stride", ctypes.c_int64),
+                ("logits_dtype", ctypes.c_int), ("out_dtype", ctypes.c_int)]
+
+
+class FlceProcessGrads(ctypes.Structure):
+    """flce_process_grads_t."""
+    _fields_ = [("grad_out", ctypes.c_void_p), ("ld_grad_out", ctypes.c_int64),
+                ("grad_lse", ctypes.c_void_p), ("grad_entropy", ctypes.c_void_p),
+                ("out", ctypes.c_void_p), ("ld_out", ctypes.c_int64), ("lse", ctypes.c_void_p),
+                ("entropy", ctypes.c_void_p)]
+
+
+class FlceAdamwList(ctypes.Structure):
+    """flce_adamw_list_t."""
+    _fields_ = [("count", ctypes.c_int64)] + [(name, ctypes.c_void_p) for name in (
+        "sizes", "params", "grads", "masters", "exp_avgs", "exp_avg_sqs", "exp_avg_scales",
+        "exp_avg_sq_scales", "param_dtypes", "grad_dtypes")]
+
+
+class FlceAdamwOptions(ctypes.Structure):
+    """flce_adamw_options_t."""
+    _fields_ = [("lr", ctypes.c_double), ("beta1", ctypes.c_double), ("beta2", ctypes.c_double),
+                ("eps", ctypes.c_double), ("weight_decay", ctypes.c_double),
+                ("state_dtype", ctypes.c_int), ("rounding", ctypes.c_int),
+                ("seed", ctypes.c_uint64)]
+
 
 # Every exported symbol with its (restype, argtypes).
 _P = ctypes.c_void_p
@@ -169,6 +223,25 @@ _SIG = {
     "flce_preference_loss_forward_backward": (ctypes.c_int, [_P] * 4 + [_I64] * 3
                                               + [ctypes.POINTER(FlcePreferenceOptions), _P, _P, _P,
                                                  _P, _P, _P, _P, ctypes.c_size_t, _P]),
+    "flce_logits_workspace_size": (ctypes.c_int, [_I64, _I64, _I64,
+                                                  ctypes.POINTER(ctypes.c_size_t)]),
+    "flce_logits": (ctypes.c_int, [_P, _P, _P, _I64, _I64, _I64, ctypes.c_float, ctypes.c_int, _P,
+                                   _I64, _P, ctypes.c_size_t, _P]),
+    "flce_process_workspace_size": (ctypes.c_int, [_I64, _I64, ctypes.POINTER(ctypes.c_size_t)]),
+    "flce_process_logits": (ctypes.c_int, [_P, _I64, _I64, _I64,
+                                           ctypes.POINTER(FlceProcessOptions), _P, _I64, _P, _P,
+                                           _P, _P, ctypes.c_size_t, _P]),
+    "flce_process_logits_backward": (ctypes.c_int, [ctypes.POINTER(FlceProcessGrads), _P, _I64,
+                                                    _I64, _I64,
+                                                    ctypes.POINTER(FlceProcessOptions), _P, _I64,
+                                                    _P, ctypes.c_size_t, _P]),
+    "flce_grad_norm_workspace_size": (ctypes.c_int, [_P, _I64, ctypes.POINTER(ctypes.c_size_t)]),
+    "flce_grad_norm": (ctypes.c_int, [_P, _P, _P, _I64, ctypes.c_double, _P, _P, _P,
+                                      ctypes.c_size_t, _P]),
+    "flce_adamw_workspace_size": (ctypes.c_size_t, []),
+    "flce_adamw_step": (ctypes.c_int, [ctypes.POINTER(FlceAdamwList),
+                                       ctypes.POINTER(FlceAdamwOptions), _P, _P, _P, _P,
+                                       ctypes.c_size_t, _P]),
     "flce_get_status": (ctypes.c_int, [_P, ctypes.POINTER(_I64), _P]),
     "flce_status_string": (ctypes.c_char_p, [ctypes.c_int]),
     "flce_version": (ctypes.c_int, []),
@@ -408,6 +481,65 @@ def flce_preference_loss_forward_backward(logprob, ref_logprob, labels, cu_seqle
                                                        rejected_reward, grad_logprob, workspace,
                                                        workspace_bytes, stream),
            "flce_preference_loss_forward_backward")
+
+
+def flce_logits_workspace_size(N: int, H: int, V: int) -> int:
+    b = ctypes.c_size_t(0)
+    _check(lib().flce_logits_workspace_size(N, H, V, ctypes.byref(b)),
+           "flce_logits_workspace_size")
+    return b.value
+
+
+def flce_logits(hidden, weight, bias, N, H, V, softcap, out_dtype, out, ld_out, workspace,
+                workspace_bytes, stream):
+    _check(lib().flce_logits(hidden, weight, bias, N, H, V, softcap, out_dtype, out, ld_out,
+                             workspace, workspace_bytes, stream), "flce_logits")
+
+
+def flce_process_workspace_size(N: int, V: int) -> int:
+    b = ctypes.c_size_t(0)
+    _check(lib().flce_process_workspace_size(N, V, ctypes.byref(b)),
+           "flce_process_workspace_size")
+    return b.value
+
+
+def flce_process_logits(logits, ld, N, V, opt, out, ld_out, lse, entropy, greedy, workspace,
+                        workspace_bytes, stream):
+    _check(lib().flce_process_logits(logits, ld, N, V, ctypes.byref(opt), out, ld_out, lse,
+                                     entropy, greedy, workspace, workspace_bytes, stream),
+           "flce_process_logits")
+
+
+def flce_process_logits_backward(grads, logits, ld, N, V, opt, grad_logits, ld_grad, workspace,
+                                 workspace_bytes, stream):
+    _check(lib().flce_process_logits_backward(ctypes.byref(grads), logits, ld, N, V,
+                                              ctypes.byref(opt), grad_logits, ld_grad, workspace,
+                                              workspace_bytes, stream),
+           "flce_process_logits_backward")
+
+
+def flce_grad_norm_workspace_size(sizes, count: int) -> int:
+    """sizes: a ctypes array of int64, or its address."""
+    b = ctypes.c_size_t(0)
+    _check(lib().flce_grad_norm_workspace_size(sizes, count, ctypes.byref(b)),
+           "flce_grad_norm_workspace_size")
+    return b.value
+
+
+def flce_grad_norm(grads, sizes, dtypes, count, max_norm, norm, scale, workspace, workspace_bytes,
+                   stream):
+    _check(lib().flce_grad_norm(grads, sizes, dtypes, count, max_norm, norm, scale, workspace,
+                                workspace_bytes, stream), "flce_grad_norm")
+
+
+def flce_adamw_workspace_size() -> int:
+    return lib().flce_adamw_workspace_size()
+
+
+def flce_adamw_step(tensors, opt, lr_device, grad_scale, step, workspace, workspace_bytes,
+                    stream):
+    _check(lib().flce_adamw_step(ctypes.byref(tensors), ctypes.byref(opt), lr_device, grad_scale,
+                                 step, workspace, workspace_bytes, stream), "flce_adamw_step")
 
 
 def flce_get_status(workspace, stream) -> int:
@@ -1107,3 +1239,420 @@ def preference_loss_forward_backward(logprob, labels, cu_seqlens, grad_loss=None
           workspace.numel())
     out.update(grad_logprob=glp, workspace=workspace)
     return out
+
+
+# ---- the two ends of a training step: logits to sample from, the update
+
+def _rows(t, dtypes, name):
+    """(N, V, row stride) of a 2-d tensor whose rows are dense; they may lie
+    apart, as in a slice of a wider tensor."""
+    torch = _torch()
+    if not isinstance(t, torch.Tensor) or t.device.type != "cuda":
+        raise ValueError(f"{name} must be a CUDA (HIP) tensor")
+    if t.dtype not in dtypes:
+        raise ValueError(f"{name} must be {' or '.join(map(str, dtypes))}, got {t.dtype}")
+    if t.dim() != 2 or (t.shape[1] > 1 and t.stride(1) != 1):
+        raise ValueError(f"{name} must be a 2-d tensor with dense rows")
+    N, V = t.shape
+    if N <= 1:
+        return N, V, V
+    if t.stride(0) < V:
+        raise ValueError(f"the rows of {name} must not overlap")
+    return N, V, t.stride(0)
+
+
+def _torch_dtype(code):
+    torch = _torch()
+    return torch.float32 if code == FLCE_GRAD_F32 else torch.bfloat16
+
+
+def _out_rows(out, N, V, dtype, dev, name="out"):
+    """(out or a new [N,V] tensor, row stride)."""
+    torch = _torch()
+    if out is None:
+        return torch.empty((N, V), dtype=dtype, device=dev), V
+    n, v, ld = _rows(out, (dtype,), name)
+    if (n, v) != (N, V):
+        raise ValueError(f"{name} must be [{N}, {V}]")
+    _check_devices(dev, (name, out))
+    return out, ld
+
+
+def logits(hidden, weight, bias=None, softcap: float = 0.0, out_dtype: str = "f32", out=None,
+           workspace=None) -> dict:
+    """{"logits": [N,V], "workspace"}: the head's logits of a few rows (at most
+    1024), e.g. the last positions of the sequences that are being generated.
+
+    hidden: bf16 [N,H]; weight: bf16 [H,V]; bias: fp32 [V] or None; softcap: 0
+    or less for none. The result is fp32 or (out_dtype "bf16") bf16; with out
+    (of that type, rows may lie apart) it is written there.
+    """
+    torch = _torch()
+    _require(hidden, torch.bfloat16, 2, "hidden")
+    _require(weight, torch.bfloat16, 2, "weight")
+    N, H = hidden.shape
+    if weight.shape[0] != H:
+        raise ValueError("shape mismatch between hidden [N,H] and weight [H,V]")
+    V = weight.shape[1]
+    dev = hidden.device
+    _check_devices(dev, ("weight", weight))
+    if bias is not None:
+        _check_vector(bias, torch.float32, V, dev.index, "bias")
+    odt = _choice(_GRAD_DTYPES, out_dtype, "out_dtype")
+    out, ld = _out_rows(out, N, V, _torch_dtype(odt), dev)
+    workspace = _workspace(workspace, _logits_bytes(N, H, V), dev)
+    _call(dev, "flce_logits", hidden.data_ptr(), weight.data_ptr(), _ptr(bias), N, H, V,
+          float(softcap), odt, out.data_ptr(), ld, workspace.data_ptr(), workspace.numel())
+    return {"logits": out, "workspace": workspace}
+
+
+_logits_bytes = functools.lru_cache(maxsize=256)(flce_logits_workspace_size)
+_process_bytes = functools.lru_cache(maxsize=256)(flce_process_workspace_size)
+
+
+def _process_options(x, out_dtype, tokens=None, cu_seqlens=None, lengths=None,
+                     prompt_lengths=None, repetition_penalty=1.0, presence_penalty=0.0,
+                     frequency_penalty=0.0, temperature=1.0, bias=None, bias_tokens=None,
+                     bias_values=None, bias_cu_seqlens=None, allowed=None, ignore_index=-100):
+    """(N, V, row stride, FlceProcessOptions) for logits x, after checking the
+    tensors."""
+    torch = _torch()
+    f32, i64 = torch.float32, torch.int64
+    N, V, ld = _rows(x, (torch.bfloat16, f32), "logits")
+    dev = x.device
+    index = dev.index
+    o = FlceProcessOptions()
+    o.ignore_index = int(ignore_index)
+    if tokens is None:
+        if cu_seqlens is not None or lengths is not None or prompt_lengths is not None:
+            raise ValueError("cu_seqlens, lengths and prompt_lengths need tokens")
+    else:
+        padded = isinstance(tokens, torch.Tensor) and tokens.dim() == 2
+        _require(tokens, i64, 2 if padded else 1, "tokens")
+        _check_devices(dev, ("tokens", tokens))
+        if padded:
+            if lengths is None or cu_seqlens is not None:
+                raise ValueError("tokens [N, L] need lengths [N] (and no cu_seqlens)")
+            if tokens.shape[0] != N:
+                raise ValueError(f"tokens must have {N} rows")
+            _check_vector(lengths, i64, N, index, "lengths")
+            offsets = lengths
+        else:
+            if cu_seqlens is None or lengths is not None:
+                raise ValueError("packed tokens need cu_seqlens [N+1] (and no lengths)")
+            _check_vector(cu_seqlens, i64, N + 1, index, "cu_seqlens")
+            offsets = cu_seqlens
+        if prompt_lengths is not None:
+            _check_vector(prompt_lengths, i64, N, index, "prompt_lengths")
+            o.prompt_lengths = prompt_lengths.data_ptr()
+        # Rows of no tokens have no address, nor do their lengths say anything.
+        if not padded or tokens.shape[1] > 0:
+            o.tokens = tokens.data_ptr() or offsets.data_ptr()
+            o.tokens_size = tokens.numel()
+            o.tokens_stride = tokens.shape[1] if padded else 0
+            o.offsets = offsets.data_ptr()
+    for value, array, scalar in ((repetition_penalty, "repetition", "repetition_penalty"),
+                                 (presence_penalty, "presence", "presence_penalty"),
+                                 (frequency_penalty, "frequency", "frequency_penalty"),
+                                 (temperature, "temperatures", "temperature")):
+        one = 1.0 if scalar in ("repetition_penalty", "temperature") else 0.0
+        if isinstance(value, torch.Tensor):
+            _check_vector(value, f32, N, index, scalar)
+            setattr(o, array, value.data_ptr())
+            setattr(o, scalar, one)
+        else:
+            setattr(o, scalar, float(value))
+    if bias is not None:
+        if isinstance(bias, torch.Tensor) and bias.dim() == 2:
+            n, v, stride = _rows(bias, (f32,), "bias")
+            if (n, v) != (N, V):
+                raise ValueError(f"bias must be [{V}] or [{N}, {V}]")
+            _check_devices(dev, ("bias", bias))
+            o.bias_stride = stride
+        else:
+            _check_vector(bias, f32, V, index, "bias")
+        o.bias = bias.data_ptr()
+    listed = (bias_tokens, bias_values, bias_cu_seqlens)
+    if any(t is not None for t in listed):
+        if any(t is None for t in listed):
+            raise ValueError("listed biases are bias_tokens, bias_values and bias_cu_seqlens")
+        _require(bias_tokens, i64, 1, "bias_tokens")
+        _check_devices(dev, ("bias_tokens", bias_tokens))
+        _check_vector(bias_values, f32, bias_tokens.numel(), index, "bias_values")
+        _check_vector(bias_cu_seqlens, i64, N + 1, index, "bias_cu_seqlens")
+        o.bias_tokens, o.bias_values = bias_tokens.data_ptr(), bias_values.data_ptr()
+        o.bias_count, o.bias_offsets = bias_tokens.numel(), bias_cu_seqlens.data_ptr()
+    if allowed is not None:
+        words = -(-V // 32)
+        if isinstance(allowed, torch.Tensor) and allowed.dim() == 2:
+            n, w, stride = _rows(allowed, (torch.int32,), "allowed")
+            if n != N or w < words:
+                raise ValueError(f"allowed must be [{words}] or [{N}, {words}]")
+            _check_devices(dev, ("allowed", allowed))
+            o.allowed_stride = stride
+        else:
+            _require(allowed, torch.int32, 1, "allowed")
+            if allowed.numel() < words:
+                raise ValueError(f"allowed must be [{words}] or [{N}, {words}]")
+            _check_devices(dev, ("allowed", allowed))
+        o.allowed = allowed.data_ptr()
+    o.logits_dtype = FLCE_GRAD_F32 if x.dtype == f32 else FLCE_GRAD_BF16
+    o.out_dtype = o.logits_dtype if out_dtype is None else _choice(_GRAD_DTYPES, out_dtype,
+                                                                   "out_dtype")
+    return N, V, ld, o
+
+
+def process_logits(logits, out_dtype=None, out=None, workspace=None, **options) -> dict:
+    """Penalties, biases, temperature and mask on logits (flce_process_logits):
+    {"logits": [N,V], "lse": fp32 [N], "entropy": fp32 [N], "greedy": int64 [N],
+    "workspace"}.
+
+    logits: bf16 or fp32 [N,V] (rows may lie apart), e.g. of ``logits``. The
+    result has their type or out_dtype ("f32" | "bf16"); out may be logits
+    itself. In row i a logit x of id v becomes
+      x / repetition if x > 0, else x * repetition   (v anywhere in the history)
+      x - frequency * n - (presence if n)            (n: v's count past the prompt)
+      x + bias[v] + the row's listed biases of v
+      x / temperature                                (0: unscaled)
+      -inf                                           (v not allowed)
+    in this order; lse, entropy and greedy (the first largest id, -1 if nothing
+    is allowed) are those of the returned row, so that logits[i, t] - lse[i] is
+    the log-probability with which token t is drawn.
+
+    Options: the rows' histories as tokens (int64, packed) with cu_seqlens
+    (int64 [N+1]), or as tokens [N, L] with lengths (int64 [N]); prompt_lengths
+    (int64 [N], None for 0); repetition_penalty = 1, presence_penalty = 0,
+    frequency_penalty = 0 and temperature = 1, numbers or fp32 [N]; bias (fp32
+    [V] or [N,V]); bias_tokens (int64 [K]), bias_values (fp32 [K]) and
+    bias_cu_seqlens (int64 [N+1]), a list of biases a row, of which those of one
+    id add up; allowed (int32 [V/32 rounded up], or [N, ...]: id v is allowed if
+    bit v % 32 of word v // 32 is set); ignore_index = -100. Tokens that are
+    neither ignore_index nor an id are passed over and counted
+    (flce_get_status on the workspace), in histories if there is a penalty. A
+    row whose offsets are bad counts as one, and its outputs are NaN and -1.
+    """
+    torch = _torch()
+    N, V, ld, opt = _process_options(logits, out_dtype, **options)
+    dev = logits.device
+    out, ld_out = _out_rows(out, N, V, _torch_dtype(opt.out_dtype), dev)
+    workspace = _workspace(workspace, _process_bytes(N, V), dev)
+    stats = torch.empty((2, N), dtype=torch.float32, device=dev)
+    greedy = torch.empty(N, dtype=torch.int64, device=dev)
+    lse, entropy = stats[0], stats[1]
+    _call(dev, "flce_process_logits", logits.data_ptr(), ld, N, V, opt, out.data_ptr(), ld_out,
+          lse.data_ptr(), entropy.data_ptr(), greedy.data_ptr(), workspace.data_ptr(),
+          workspace.numel())
+    return {"logits": out, "lse": lse, "entropy": entropy, "greedy": greedy,
+            "workspace": workspace}
+
+
+def process_logits_backward(grad_out, logits, processed=None, lse=None, entropy=None,
+                            grad_lse=None, grad_entropy=None, out_dtype=None, out=None,
+                            workspace=None, **options):
+    """Gradient [N,V] (type of logits) of ``process_logits`` with respect to the
+    logits, for the upstream gradients grad_out [N,V] of the returned logits
+    (None for zero) and grad_lse and grad_entropy (fp32 [N], None for zero) of
+    lse and entropy; the latter two need processed, lse and entropy, the
+    "logits", "lse" and "entropy" that the call returned. logits and options are
+    those of the call (logits as they were before it); without grad_out and
+    processed, out_dtype too. out may be grad_out itself, if the types agree."""
+    torch = _torch()
+    f32, both = torch.float32, (torch.bfloat16, torch.float32)
+    g = FlceProcessGrads()
+    for t in (grad_out, processed):
+        if isinstance(t, torch.Tensor) and t.dtype in both:
+            out_dtype = "f32" if t.dtype == f32 else "bf16"
+    N, V, ld, opt = _process_options(logits, out_dtype, **options)
+    dev = logits.device
+    for t, name, pointer, stride in ((grad_out, "grad_out", "grad_out", "ld_grad_out"),
+                                     (processed, "processed", "out", "ld_out")):
+        if t is not None:
+            n, v, rows = _rows(t, (_torch_dtype(opt.out_dtype),), name)
+            if (n, v) != (N, V):
+                raise ValueError(f"{name} must be [{N}, {V}]")
+            _check_devices(dev, (name, t))
+            setattr(g, pointer, t.data_ptr())
+            setattr(g, stride, rows)
+    for t, name in ((lse, "lse"), (entropy, "entropy"), (grad_lse, "grad_lse"),
+                    (grad_entropy, "grad_entropy")):
+        if t is not None:
+            _check_vector(t, f32, N, dev.index, name)
+            setattr(g, name, t.data_ptr())
+    if (grad_lse is not None or grad_entropy is not None) and (processed is None or lse is None):
+        raise ValueError("grad_lse and grad_entropy need processed and lse")
+    if grad_entropy is not None and entropy is None:
+        raise ValueError("grad_entropy needs entropy")
+    out, ld_grad = _out_rows(out, N, V, logits.dtype, dev)
+    workspace = _workspace(workspace, _process_bytes(N, V), dev)
+    _call(dev, "flce_process_logits_backward", g, logits.data_ptr(), ld, N, V, opt,
+          out.data_ptr(), ld_grad, workspace.data_ptr(), workspace.numel())
+    return out
+
+
+def _tensors(ts, dtypes, name, like=None, sizes=None):
+    """Checks a list of dense tensors of one device, of the types ``dtypes`` (a
+    set): (device, sizes, their types)."""
+    torch = _torch()
+    if not isinstance(ts, (list, tuple)):
+        raise ValueError(f"{name} must be a list of tensors")
+    if sizes is not None and len(ts) != len(sizes):
+        raise ValueError(f"{name} must have {len(sizes)} tensors, got {len(ts)}")
+    if len(ts) == 0:
+        return like, [], set()
+    T = torch.Tensor
+    try:  # lists are long and steps short: no loop of Python's own where all is well
+        numel = list(map(T.numel, ts))
+        kinds = {t.dtype for t in ts}
+        dev = like if like is not None else ts[0].device
+        if (kinds <= dtypes and all(map(T.is_contiguous, ts)) and dev.type == "cuda"
+                and set(map(T.get_device, ts)) == {dev.index}
+                and (sizes is None or numel == sizes)):
+            return dev, numel, kinds
+    except (TypeError, AttributeError):
+        pass
+    dev = like
+    for i, t in enumerate(ts):
+        if not isinstance(t, torch.Tensor) or t.device.type != "cuda":
+            raise ValueError(f"{name}[{i}] must be a CUDA (HIP) tensor")
+        if t.dtype not in dtypes:
+            raise ValueError(f"{name}[{i}] must be {' or '.join(sorted(map(str, dtypes)))}, "
+                             f"got {t.dtype}")
+        if not t.is_contiguous():
+            raise ValueError(f"{name}[{i}] must be contiguous")
+        if dev is None:
+            dev = t.device
+        if t.device != dev:
+            raise ValueError(f"{name}[{i}] must be on {dev}, got {t.device}")
+        if sizes is not None and t.numel() != sizes[i]:
+            raise ValueError(f"{name}[{i}] must have {sizes[i]} elements, got {t.numel()}")
+    raise ValueError(f"{name}: not a list of dense tensors")
+
+
+def _addresses(ts):
+    return array.array("Q", map(_torch().Tensor.data_ptr, ts))
+
+
+def _dtype_codes(ts, kinds):
+    """FLCE_GRAD_* of each tensor; kinds: their types."""
+    f32 = _torch().float32
+    if len(kinds) <= 1:
+        return array.array("i", [FLCE_GRAD_F32 if f32 in kinds else FLCE_GRAD_BF16]) * len(ts)
+    return array.array("i", [FLCE_GRAD_F32 if t.dtype is f32 else FLCE_GRAD_BF16 for t in ts])
+
+
+def grad_norm(grads, max_norm: float = 0.0, workspace=None) -> dict:
+    """{"norm": fp32 [1], "scale": fp32 [1], "workspace"}: the 2-norm over all
+    values of a list of dense bf16 or fp32 tensors (summed in float64), and the
+    factor min(1, max_norm / norm) that clips it (1 without max_norm, NaN if the
+    norm is not finite), for ``adamw_step``'s grad_scale. Both stay on the
+    device."""
+    torch = _torch()
+    dev, sizes, kinds = _tensors(grads, {torch.bfloat16, torch.float32}, "grads")
+    if dev is None:
+        raise ValueError("grads must have a tensor")
+    n = len(sizes)
+    pointers, csizes = _addresses(grads), array.array("q", sizes)
+    dtypes = _dtype_codes(grads, kinds)
+    psizes = csizes.buffer_info()[0]
+    workspace = _workspace(workspace, flce_grad_norm_workspace_size(psizes, n), dev)
+    both = torch.empty(2, dtype=torch.float32, device=dev)
+    norm, scale = both[:1], both[1:]
+    _call(dev, "flce_grad_norm", pointers.buffer_info()[0], psizes, dtypes.buffer_info()[0], n,
+          float(max_norm), norm.data_ptr(), scale.data_ptr(), workspace.data_ptr(),
+          workspace.numel())
+    return {"norm": norm, "scale": scale, "workspace": workspace}
+
+
+STATE_BLOCK = 256
+
+
+def adamw_state(params, state: str = "f32", master: bool = False) -> dict:
+    """The state of ``adamw_step`` for a list of dense bf16 or fp32 tensors:
+    step (int64 [1], 0) and, one tensor a parameter each, exp_avg and exp_avg_sq
+    of its shape (fp32, or under "8bit" torch.float8_e4m3fn codes, exp_avg_sq's
+    of the second moment's root), exp_avg_scale and exp_avg_sq_scale ("8bit":
+    fp32, one factor for each 256 values; None otherwise), all 0, and with
+    ``master`` master, an fp32 copy of each bf16 parameter (None for fp32 ones;
+    without it the whole list is None)."""
+    torch = _torch()
+    kind = _choice(_STATE_DTYPES, state, "state")
+    dev, sizes, _ = _tensors(params, {torch.bfloat16, torch.float32}, "params")
+    if dev is None:
+        raise ValueError("params must have a tensor")
+    dtype = torch.float32 if kind == FLCE_STATE_F32 else torch.float8_e4m3fn
+
+    def zeros():
+        return [torch.zeros(p.shape, dtype=dtype, device=dev) for p in params]
+
+    def scales():
+        return ([torch.zeros(-(-n // STATE_BLOCK), dtype=torch.float32, device=dev)
+                 for n in sizes] if kind == FLCE_STATE_8BIT else None)
+
+    return {"step": torch.zeros(1, dtype=torch.int64, device=dev),
+            "exp_avg": zeros(), "exp_avg_sq": zeros(),
+            "exp_avg_scale": scales(), "exp_avg_sq_scale": scales(),
+            "master": [p.detach().float() if p.dtype == torch.bfloat16 else None
+                       for p in params] if master else None}
+
+
+def adamw_step(params, grads, state, lr=1e-3, beta1: float = 0.9, beta2: float = 0.999,
+               eps: float = 1e-8, weight_decay: float = 0.01, grad_scale=None,
+               rounding: str = "nearest", seed: int = 0, workspace=None) -> None:
+    """One AdamW step over a list of tensors, in place (flce_adamw_step).
+
+    params and grads: dense bf16 or fp32 tensors of the same sizes, the types in
+    any mixture; state: of ``adamw_state``, updated in place, its step raised by
+    one. lr: a number, or fp32 [1] on the device (a captured step then follows
+    it). grad_scale: fp32 [1] that the gradients are multiplied by, e.g.
+    ``grad_norm``'s scale; if it is not finite, nothing is changed. Under
+    rounding "stochastic" bf16 parameters without a master copy and 8-bit states
+    are rounded up with the probability of the part cut off, by a hash of seed,
+    the step, the tensor's place in the list and the value's in the tensor.
+    """
+    torch = _torch()
+    f32 = torch.float32
+    both = {torch.bfloat16, f32}
+    dev, sizes, pkinds = _tensors(params, both, "params")
+    if dev is None:
+        raise ValueError("params must have a tensor")
+    gkinds = _tensors(grads, both, "grads", dev, sizes)[2]
+    m, v = state["exp_avg"], state["exp_avg_sq"]
+    ms, vs, master = state["exp_avg_scale"], state["exp_avg_sq_scale"], state["master"]
+    eight = ms is not None
+    sdt = {torch.float8_e4m3fn if eight else f32}
+    _tensors(m, sdt, "state exp_avg", dev, sizes)
+    _tensors(v, sdt, "state exp_avg_sq", dev, sizes)
+    lists = [array.array("q", sizes), _addresses(params), _addresses(grads), None, _addresses(m),
+             _addresses(v), None, None, _dtype_codes(params, pkinds), _dtype_codes(grads, gkinds)]
+    if eight:
+        blocks = [-(-n // STATE_BLOCK) for n in sizes]
+        _tensors(ms, {f32}, "state exp_avg_scale", dev, blocks)
+        _tensors(vs, {f32}, "state exp_avg_sq_scale", dev, blocks)
+        lists[6:8] = _addresses(ms), _addresses(vs)
+    if master is not None:
+        if len(master) != len(sizes):
+            raise ValueError(f"state master must have {len(sizes)} entries")
+        own = [(t, n) for t, n in zip(master, sizes) if t is not None]
+        _tensors([t for t, _ in own], {f32}, "state master", dev, [n for _, n in own])
+        if f32 in pkinds and any(t is not None and p.dtype == f32
+                                 for t, p in zip(master, params)):
+            raise ValueError("state master: fp32 parameters have no copy")
+        lists[3] = array.array("Q", [0 if t is None else t.data_ptr() for t in master])
+    step = state["step"]
+    _check_vector(step, torch.int64, 1, dev.index, "state step")
+    lr_device = None
+    if isinstance(lr, torch.Tensor):
+        _check_vector(lr, f32, 1, dev.index, "lr")
+        lr_device, lr = lr, 0.0
+    if grad_scale is not None:
+        _check_vector(grad_scale, f32, 1, dev.index, "grad_scale")
+    opt = FlceAdamwOptions(float(lr), float(beta1), float(beta2), float(eps),
+                           float(weight_decay), FLCE_STATE_8BIT if eight else FLCE_STATE_F32,
+                           _choice(_ROUNDINGS, rounding, "rounding"), int(seed) & (1 << 64) - 1)
+    table = FlceAdamwList(len(sizes), *[None if a is None else a.buffer_info()[0] for a in lists])
+    workspace = _workspace(workspace, _ADAMW_BYTES, dev)
+    _call(dev, "flce_adamw_step", table, opt, _ptr(lr_device), _ptr(grad_scale),
+          step.data_ptr(), workspace.data_ptr(), workspace.numel())
+
+
+_ADAMW_BYTES = 512  # flce_adamw_workspace_size()

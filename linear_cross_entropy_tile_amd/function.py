@@ -8,6 +8,8 @@ label (minus the cross-entropy), not the cross-entropy itself.
 ``embedding``, ``policy_loss`` and ``preference_loss`` are the operators
 beside the head in the same manner: the tied (or separate) embedding lookup,
 and the losses of RL and preference tuning on the head's per-token outputs.
+``process_logits`` is what a sampler does to logits, where a loss is taken on
+the distribution that it draws from.
 
 Marshalling only: the forward calls flce_forward through ``flce.forward``
 and keeps the per-token lse and entropy; the backward hands the upstream
@@ -20,7 +22,7 @@ of a warm-up on a side stream may still be bound. The default stream cannot join
 one: a captured backward over a leaf that an eager graph made there still holds
 would reach out of the capture, which ends the process. While such a result of
 this module on the same leaf lives (drop it first), ``embedding``,
-``policy_loss`` and ``preference_loss`` refuse the call, and the backward of
+``policy_loss``, ``preference_loss`` and ``process_logits`` refuse the call, and the backward of
 ``linear_cross_entropy`` raises. Seen are leaves among the arguments and leaves
 that an argument is a cast, view or multiple of; not seen are leaves further
 back in the graph, and results that other operators made on a leaf first.
@@ -34,7 +36,8 @@ from torch.autograd.function import once_differentiable
 from . import flce
 
 __all__ = ["LinearCrossEntropy", "linear_cross_entropy", "Embedding", "embedding",
-           "PolicyLoss", "policy_loss", "PreferenceLoss", "preference_loss"]
+           "PolicyLoss", "policy_loss", "PreferenceLoss", "preference_loss", "ProcessLogits",
+           "process_logits"]
 
 
 def _accumulator(node):
@@ -271,4 +274,57 @@ def preference_loss(logprob, labels, cu_seqlens, ref_logprob=None, **options):
     _refuse_captured_leaves(logprob)
     out = PreferenceLoss.apply(logprob, labels, cu_seqlens, ref_logprob, options)
     _note_leaves(logprob)
+    return out
+
+
+class ProcessLogits(torch.autograd.Function):
+    """(logits, lse, entropy, greedy) of the processed logits; see
+    ``process_logits``."""
+
+    @staticmethod
+    def forward(ctx, logits, out_dtype, options):
+        out = flce.process_logits(logits, out_dtype=out_dtype, **options)
+        ctx.save_for_backward(logits, out["logits"], out["lse"], out["entropy"],
+                              *[v for v in options.values() if isinstance(v, torch.Tensor)])
+        ctx.tensors = [k for k, v in options.items() if isinstance(v, torch.Tensor)]
+        ctx.options = {k: None if k in ctx.tensors else v for k, v in options.items()}
+        ctx.mark_non_differentiable(out["greedy"])
+        ctx.set_materialize_grads(False)
+        return out["logits"], out["lse"], out["entropy"], out["greedy"]
+
+    @staticmethod
+    @once_differentiable
+    def backward(ctx, grad_out, grad_lse, grad_entropy, _grad_greedy):
+        if grad_out is None and grad_lse is None and grad_entropy is None:
+            return None, None, None
+        logits, processed, lse, entropy, *tensors = ctx.saved_tensors
+        it = iter(tensors)
+        options = {k: next(it) if k in ctx.tensors else v for k, v in ctx.options.items()}
+        gl = flce.process_logits_backward(
+            None if grad_out is None else _dense_rows(grad_out), logits, processed=processed,
+            lse=lse, entropy=entropy,
+            grad_lse=None if grad_lse is None else grad_lse.contiguous(),
+            grad_entropy=None if grad_entropy is None else grad_entropy.contiguous(), **options)
+        return gl, None, None
+
+
+def _dense_rows(t):
+    """The 2-d tensor itself, or a copy of one with broadcast or strided rows."""
+    dense = t.shape[1] <= 1 or t.stride(1) == 1
+    return t if dense and (t.shape[0] <= 1 or t.stride(0) >= t.shape[1]) else t.contiguous()
+
+
+def process_logits(logits, out_dtype=None, **options):
+    """(logits, lse, entropy, greedy): ``flce.process_logits`` (same options) on
+    logits bf16 or fp32 [N,V]. The returned logits, lse and entropy are
+    differentiable with respect to logits, e.g. of a loss on
+    logits[i, token] - lse[i]; penalties, biases, masks and temperatures are
+    constants, and greedy has no gradient."""
+    for name in ("out", "workspace"):
+        if name in options:
+            raise ValueError(f"{name} belongs to flce.process_logits: the backward needs the "
+                             "logits and the result as they are")
+    _refuse_captured_leaves(logits)
+    out = ProcessLogits.apply(logits, out_dtype, options)
+    _note_leaves(logits)
     return out
