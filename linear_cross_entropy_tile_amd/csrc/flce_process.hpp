@@ -2,13 +2,13 @@
 // tokens of a row's history, biases, temperature and mask, with the logsumexp,
 // entropy and first largest id of the result, and the gradient.
 //
-// A row's ids are cut into slices, a block each. The block counts the history's
-// tokens that fall into its slice in LDS (integer atomics: the order does not
-// matter), adds up the slice's listed biases there in the list's order, and then
-// streams the slice once, eight ids a thread and step, keeping per thread the
-// running maximum m, s = sum exp(x - m), u = sum exp(x - m) (x - m) and the first
-// id of the maximum. The slices' states are merged by a wave a row in a second
-// launch. lse = m + ln s, entropy = ln s - u / s.
+// A row's ids are cut into slices, a block each, of which a thread holds eight
+// consecutive ids a step in registers. The logits are asked for first; while they
+// come, the block counts the history's tokens that fall into its slice in LDS
+// (integer atomics: the order does not matter) and adds up the slice's listed biases
+// there in the list's order. The values are formed and stored, and from the block's
+// maximum m come s = sum exp(x - m) and u = sum exp(x - m) (x - m). The slices' states
+// are merged by a wave a row in a second launch. lse = m + ln s, entropy = ln s - u / s.
 //
 // Contraction of a product and a sum into one rounding is off: the value of a
 // logit is the header's sequence of fp32 operations, whatever the compiler picks.
@@ -29,7 +29,7 @@ struct ProcArgs {
   int64_t ld, ld_out;
   int64_t N, V;
   int64_t row0;       // of the launch
-  int slice;
+  int slice;          // of the gradient; a multiple of kProcStep
   int64_t slices;
   flce_process_options_t o;
   float4* parts;      // [N, slices]: m, s, u, bits of the first id
@@ -103,15 +103,23 @@ __device__ __forceinline__ uint32_t mask_bits(const ProcArgs& a, int64_t row, in
   return p[base >> 3];
 }
 
-constexpr uint32_t kSeenPrompt = 0x80000000u;  // a count's flag: seen in the prompt
+// Counts of generated tokens in 16 bits, two ids a word, with a flag for those seen in
+// the prompt; rows of longer histories take 32 bits.
+constexpr uint32_t kSeenPrompt = 0x8000u, kSeenPromptWide = 0x80000000u;
+constexpr int64_t kLongHistory = 0x7FFF;
 
-// Counts the row's tokens of [lo, lo + n) into count (cleared by the caller);
-// COUNT: occurrences among the generated ones and kSeenPrompt, else bits. Returns
-// the thread's number of tokens that are no ids of the vocabulary.
-template <int HIST>
+// Counts the row's tokens of [lo, lo + n) into count (cleared by the caller): under
+// HIST_SEEN bits, under HIST_COUNT occurrences among the generated ones and the flag, a
+// word an id if WIDE. Returns the thread's number of tokens that are no ids of the
+// vocabulary.
+template <int HIST, bool WIDE>
 __device__ __forceinline__ int proc_history_slice(const ProcArgs& a, const ProcRow& r, int64_t lo,
                                                   int n, uint32_t* count) {
   constexpr int U = 8;
+  // Only a row's first slice counts what is no id, and the id to pass over is mostly
+  // none of the slice's: elsewhere a token costs a subtraction and a comparison.
+  const bool all = lo == 0;
+  const int64_t skip = a.o.ignore_index - lo;
   int invalid = 0;
   for (int64_t i0 = r.begin + threadIdx.x; i0 < r.end; i0 += U * kProcThreads) {
     int64_t t[U];
@@ -120,18 +128,24 @@ __device__ __forceinline__ int proc_history_slice(const ProcArgs& a, const ProcR
       const int64_t i = i0 + u * kProcThreads;
       t[u] = i < r.end ? a.o.tokens[i] : a.o.ignore_index;
     }
+    if (all) {
+#pragma unroll
+      for (int u = 0; u < U; ++u)
+        invalid += t[u] != a.o.ignore_index && (uint64_t)t[u] >= (uint64_t)a.V ? 1 : 0;
+    }
 #pragma unroll
     for (int u = 0; u < U; ++u) {
-      const int64_t x = t[u];
-      if (x == a.o.ignore_index) continue;
-      invalid += x < 0 || x >= a.V ? 1 : 0;
-      const int64_t d = x - lo;
-      if (d < 0 || d >= n || x >= a.V) continue;
+      const int64_t x = t[u] - lo;
+      if ((uint64_t)x >= (uint64_t)n || x == skip) continue;
+      const int d = (int)x;
       if constexpr (HIST == HIST_COUNT) {
-        if (i0 + u * kProcThreads < r.generated)
-          atomicOr(&count[d], kSeenPrompt);
+        const bool made = i0 + u * kProcThreads >= r.generated;
+        const int shift = WIDE ? 0 : 16 * (d & 1);
+        uint32_t* word = &count[WIDE ? d : d >> 1];
+        if (made)
+          atomicAdd(word, 1u << shift);
         else
-          atomicAdd(&count[d], 1u);
+          atomicOr(word, (WIDE ? kSeenPromptWide : kSeenPrompt) << shift);
       } else {
         atomicOr(&count[d >> 5], 1u << (d & 31));
       }
@@ -142,8 +156,9 @@ __device__ __forceinline__ int proc_history_slice(const ProcArgs& a, const ProcR
 
 // One wave adds the row's listed biases of [lo, lo + n) to sum (cleared by the
 // caller) in the list's order: of the lanes that have the same id, the first one
-// goes first. `tag` holds one word an id. Returns the lane's number of ids outside
-// the vocabulary.
+// goes first. `tag` holds kProcTags words; ids that share one wait for each other.
+// Returns the lane's number of ids outside the vocabulary.
+constexpr int kProcTags = 256;
 __device__ __forceinline__ int proc_bias_slice(const ProcArgs& a, const ProcRow& r, int64_t lo,
                                                int n, volatile float* sum, uint32_t* tag) {
   const int lane = threadIdx.x & 63;
@@ -161,11 +176,12 @@ __device__ __forceinline__ int proc_bias_slice(const ProcArgs& a, const ProcRow&
       if (on) value = a.o.bias_values[i];
     }
     while (__builtin_amdgcn_ballot_w64(on) != 0) {
-      if (on) tag[d] = 64u;
+      uint32_t* slot = &tag[d & (kProcTags - 1)];
+      if (on) *slot = 64u;
       __builtin_amdgcn_fence(__ATOMIC_SEQ_CST, "wavefront");
-      if (on) atomicMin(&tag[d], (uint32_t)lane);
+      if (on) atomicMin(slot, (uint32_t)lane);
       __builtin_amdgcn_fence(__ATOMIC_SEQ_CST, "wavefront");
-      if (on && *(volatile uint32_t*)&tag[d] == (uint32_t)lane) {
+      if (on && *(volatile uint32_t*)slot == (uint32_t)lane) {
         sum[d] = sum[d] + value;
         on = false;
       }
@@ -216,141 +232,303 @@ __device__ __forceinline__ ProcState proc_wave_merge(ProcState v) {
   return v;
 }
 
-// Adds eight values (the first `n`) of ids id0 .. to the thread's state, in ids'
-// order. NaN: s becomes NaN.
-__device__ __forceinline__ void proc_accumulate(ProcState& st, const float (&x)[8], int n, int id0) {
-  float top = -INFINITY;
+// A wave's result of `op` over its lanes, in all of them, in a fixed order: within the
+// rows of 16 lanes, then over the four rows.
+template <int CTRL>
+__device__ __forceinline__ float dpp_rotated(float v) {
+  return __builtin_bit_cast(
+      float, __builtin_amdgcn_update_dpp(0, __builtin_bit_cast(int, v), CTRL, 0xf, 0xf, false));
+}
+template <class Op>
+__device__ __forceinline__ float wave_all(float v, Op op) {
+  v = op(v, dpp_rotated<0x128>(v));  // row_ror:8
+  v = op(v, dpp_rotated<0x124>(v));
+  v = op(v, dpp_rotated<0x122>(v));
+  v = op(v, dpp_rotated<0x121>(v));
+  float r[4];
 #pragma unroll
-  for (int k = 0; k < 8; ++k) top = fmaxf(top, k < n ? x[k] : -INFINITY);
-  if (top > st.m) {
-    const float d = fmaxf(st.m - top, kMostNegative);
-    const float f = __builtin_amdgcn_exp2f(d * kLog2e);
-    st.u = f > 0.f ? f * (st.u + st.s * d) : 0.f;
-    st.s = f * st.s;
-    st.m = top;
-#pragma unroll
-    for (int k = 7; k >= 0; --k)
-      if (k < n && x[k] == top) st.id = id0 + k;
+  for (int i = 0; i < 4; ++i)
+    r[i] = __builtin_bit_cast(
+        float, __builtin_amdgcn_readlane(__builtin_bit_cast(int, v), 16 * i));
+  return op(op(r[0], r[1]), op(r[2], r[3]));
+}
+struct MaxOp {
+  __device__ __forceinline__ float operator()(float a, float b) const { return fmaxf(a, b); }
+};
+struct SumOp {
+  __device__ __forceinline__ float operator()(float a, float b) const { return a + b; }
+};
+
+// LDS traffic of the block is complete; loads from memory may still be on their way.
+__device__ __forceinline__ void lds_barrier() {
+  wait_lgkmcnt0();
+  block_barrier();
+}
+
+// Eight values as they lie in memory.
+template <bool F32>
+struct Raw8 {
+  eu32x4 w[F32 ? 2 : 1];
+};
+template <bool F32>
+__device__ __forceinline__ void load_raw8(const void* p, int64_t i, int n, Raw8<F32>& r) {
+  if (n >= 8) {
+    const char* q = static_cast<const char*>(p) + i * (F32 ? 4 : 2);
+    r.w[0] = load_any<eu32x4>(q);
+    if constexpr (F32) r.w[1] = load_any<eu32x4>(q + 16);
+    return;
   }
-  const float m = st.m == -INFINITY ? 0.f : st.m;
+  float v[8];
+  load8<F32>(p, i, n, v);
+  if constexpr (F32) {
 #pragma unroll
-  for (int k = 0; k < 8; ++k) {
-    if (k < n) {
-      const float d = x[k] - m;
-      const float e = __builtin_amdgcn_exp2f(d * kLog2e);
-      st.s += e;
-      st.u += e * fmaxf(d, kMostNegative);
+    for (int k = 0; k < 8; ++k) r.w[k >> 2][k & 3] = __builtin_bit_cast(uint32_t, v[k]);
+  } else {
+    r.w[0] = pack8(v);
+  }
+}
+template <bool F32>
+__device__ __forceinline__ void unpack_raw8(const Raw8<F32>& r, float (&v)[8]) {
+  if constexpr (F32) {
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+      const uint32_t word = r.w[k >> 2][k & 3];  // a bit cast of a vector's element takes its first
+      v[k] = __builtin_bit_cast(float, word);
     }
+  } else {
+    unpack8(r.w[0], v);
   }
 }
 
-// Block (row, slice): see the head of the file. LIST: there are listed biases.
-template <int HIST, bool LIST, bool IN32, bool OUT32>
-__global__ void __launch_bounds__(kProcThreads) process_kernel(ProcArgs a) {
+// x where bit k of `bits` is set, else `other`.
+__device__ __forceinline__ float select_bit(uint32_t bits, int k, float x, float other) {
+  const uint32_t m = (uint32_t)((int)(bits << (31 - k)) >> 31);
+  return __builtin_bit_cast(float, (m & __builtin_bit_cast(uint32_t, x)) |
+                                       (~m & __builtin_bit_cast(uint32_t, other)));
+}
+
+// The penalties of the eight ids from v on of the slice.
+template <int HIST, bool WIDE>
+__device__ __forceinline__ void proc_penalise(const uint32_t* count, int v, const ProcScale& sc,
+                                              float (&x)[8]) {
 #pragma clang fp contract(off)
-  extern __shared__ uint32_t sh[];
-  __shared__ ProcState wave_state[kProcThreads / 64];
-  __shared__ int wave_invalid[kProcThreads / 64];
-  const int64_t slice = blockIdx.x % (uint32_t)a.slices;
-  const int64_t row = a.row0 + blockIdx.x / (uint32_t)a.slices;
-  const int64_t lo = slice * a.slice;
-  const int n = (int)(a.V - lo < a.slice ? a.V - lo : a.slice);
-  const int tid = threadIdx.x;
-  const ProcRow r = proc_row(a, row);
-  const ProcScale sc = proc_scale(a, row);
-  uint32_t* count = sh;
-  const int words = HIST == HIST_COUNT ? a.slice : (HIST == HIST_SEEN ? a.slice / 32 : 0);
-  float* sum = reinterpret_cast<float*>(sh + words);
-  uint32_t* tag = sh + words + a.slice;
-  if constexpr (HIST != HIST_NONE || LIST) {
-    const int clear = words + (LIST ? a.slice : 0);
-    for (int i = tid; i < clear; i += kProcThreads) sh[i] = 0;
-    __syncthreads();
-    int invalid = 0;
-    if constexpr (HIST != HIST_NONE) invalid = proc_history_slice<HIST>(a, r, lo, n, count);
-    if constexpr (LIST)
-      if (tid < 64) invalid += proc_bias_slice(a, r, lo, n, sum, tag);
-    if (slice == 0) {
-      for (int d = 32; d > 0; d >>= 1) invalid += __shfl_down(invalid, d, 64);
-      if ((tid & 63) == 0) wave_invalid[tid >> 6] = invalid;
+  if constexpr (HIST == HIST_SEEN) {
+    const uint32_t bits = (count[v >> 5] >> (v & 31)) & 0xFFu;
+    if (bits != 0) {
+#pragma unroll
+      for (int k = 0; k < 8; ++k)
+        if ((bits >> k) & 1) x[k] = x[k] * (x[k] > 0.f ? sc.inv_r : sc.r);
     }
-    __syncthreads();
-  }
-  if (slice == 0 && tid == 0) {
-    int invalid = r.bad ? 1 : 0;
-    if constexpr (HIST != HIST_NONE || LIST)
-      for (int w = 0; w < kProcThreads / 64; ++w) invalid += wave_invalid[w];
-    a.invalid[row] = invalid;
-  }
-  ProcState st{-INFINITY, 0.f, 0.f, -1};
-  for (int v = tid * 8; v < n; v += kProcStep) {
-    const int left = n - v;
-    float x[8];
-    load8<IN32>(a.in, row * a.ld + lo + v, left, x);
-    if constexpr (HIST == HIST_COUNT) {
-      uint32_t c[8], any = 0;
+  } else if constexpr (HIST == HIST_COUNT) {
+    uint32_t c[8], any = 0;
+    if constexpr (WIDE) {
 #pragma unroll
       for (int k = 0; k < 8; ++k) {
         c[k] = count[v + k];
         any |= c[k];
       }
-      if (any != 0) {
+    } else {
+      const eu32x4 w = *reinterpret_cast<const eu32x4*>(count + (v >> 1));
+      any = w[0] | w[1] | w[2] | w[3];
 #pragma unroll
-        for (int k = 0; k < 8; ++k) {
-          const float times = (float)(c[k] & ~kSeenPrompt);
-          if (c[k] != 0) x[k] = x[k] * (x[k] > 0.f ? sc.inv_r : sc.r);
-          if (times > 0.f) x[k] = (x[k] - sc.frequency * times) - sc.presence;
-        }
-      }
-    } else if constexpr (HIST == HIST_SEEN) {
-      const uint32_t bits = (count[v >> 5] >> (v & 31)) & 0xFFu;
-      if (bits != 0) {
-#pragma unroll
-        for (int k = 0; k < 8; ++k)
-          if ((bits >> k) & 1) x[k] = x[k] * (x[k] > 0.f ? sc.inv_r : sc.r);
-      }
+      for (int k = 0; k < 8; ++k) c[k] = (w[k >> 1] >> (16 * (k & 1))) & 0xFFFFu;
     }
-    if (a.o.bias != nullptr) {
-      float b[8];
-      load8<true>(a.o.bias, row * a.o.bias_stride + lo + v, left, b);
-#pragma unroll
-      for (int k = 0; k < 8; ++k) x[k] = x[k] + b[k];
-    }
-    if constexpr (LIST) {
-#pragma unroll
-      for (int k = 0; k < 8; ++k) x[k] = x[k] + sum[v + k];
-    }
-    const uint32_t allowed = mask_bits(a, row, lo + v);
+    if (any == 0) return;
+    const uint32_t flag = WIDE ? kSeenPromptWide : kSeenPrompt;
 #pragma unroll
     for (int k = 0; k < 8; ++k) {
-      x[k] = x[k] * sc.inv_t;
-      x[k] = (allowed >> k) & 1 ? x[k] : -INFINITY;
-      if (r.bad) x[k] = NAN;
-    }
-    store8<OUT32>(a.out, row * a.ld_out + lo + v, left, x);
-    // The statistics are those of the values as they are returned.
-    if constexpr (!OUT32) unpack8(pack8(x), x);
-    proc_accumulate(st, x, left, (int)lo + v);
-  }
-  if (!r.bad && st.s != st.s) {
-    // A NaN among this thread's values (or infinity - infinity): find it.
-    for (int v = tid * 8; v < n; v += kProcStep) {
-      float x[8];
-      load8<OUT32>(a.out, row * a.ld_out + lo + v, n - v, x);
-      for (int k = 0; k < 8 && v + k < n; ++k)
-        if (x[k] != x[k] && st.m == st.m) {
-          st.m = NAN;
-          st.id = (int)lo + v + k;
-        }
+      const float times = (float)(c[k] & ~flag);
+      if (c[k] != 0) x[k] = x[k] * (x[k] > 0.f ? sc.inv_r : sc.r);
+      if (times > 0.f) x[k] = (x[k] - sc.frequency * times) - sc.presence;
     }
   }
-  if (r.bad) st = ProcState{NAN, NAN, NAN, -1};
-  st = proc_wave_merge(st);
-  if ((tid & 63) == 0) wave_state[tid >> 6] = st;
-  __syncthreads();
+}
+
+// LDS words of a slice: counts, sums of the listed biases, tags.
+__host__ __device__ constexpr int proc_count_words(int hist, int slice) {
+  return hist == HIST_COUNT ? slice / 2 : (hist == HIST_SEEN ? slice / 32 : 0);
+}
+__host__ __device__ constexpr int proc_lds_words(int hist, bool list, int slice) {
+  return proc_count_words(hist, slice) + (list ? slice + kProcTags : 0);
+}
+
+__device__ __forceinline__ void lds_clear(uint32_t* p, int words) {  // a multiple of 4
+  for (int i = threadIdx.x * 4; i < words; i += 4 * kProcThreads)
+    *reinterpret_cast<eu32x4*>(p + i) = eu32x4{0, 0, 0, 0};
+}
+
+// Block (row, slice): see the head of the file. LIST: there are listed biases. A slice
+// has STEPS steps of eight ids a thread.
+template <int HIST, bool LIST, int STEPS, bool IN32, bool OUT32>
+__global__ void __launch_bounds__(kProcThreads, STEPS == 4 ? 5 : 1) process_kernel(ProcArgs a) {
+#pragma clang fp contract(off)
+  constexpr int kSlice = STEPS * kProcStep, kWaves = kProcThreads / 64;
+  __shared__ __attribute__((aligned(16))) uint32_t sh[proc_lds_words(HIST, LIST, kSlice) + 4];
+  __shared__ float wave_max[kWaves], wave_s[kWaves], wave_u[kWaves];
+  __shared__ int wave_invalid[kWaves], first_id, first_nan;
+  const int64_t slice = blockIdx.x % (uint32_t)a.slices;
+  const int64_t row = a.row0 + blockIdx.x / (uint32_t)a.slices;
+  const int64_t lo = slice * kSlice;
+  const int n = (int)(a.V - lo < kSlice ? a.V - lo : kSlice);
+  const int tid = threadIdx.x;
+  Raw8<IN32> raw[STEPS];
+  uint32_t allowed[STEPS];
+#pragma unroll
+  for (int j = 0; j < STEPS; ++j) {
+    const int v = j * kProcStep + tid * 8;
+    if (v < n) {
+      load_raw8<IN32>(a.in, row * a.ld + lo + v, n - v, raw[j]);
+      allowed[j] = mask_bits(a, row, lo + v);
+    }
+  }
+  const ProcRow r = proc_row(a, row);
+  const ProcScale sc = proc_scale(a, row);
+  uint32_t* count = sh;
+  float* sum = reinterpret_cast<float*>(sh + proc_count_words(HIST, kSlice));
+  const bool wide = HIST == HIST_COUNT && r.end - r.begin > kLongHistory;
   if (tid == 0) {
-    for (int w = 1; w < kProcThreads / 64; ++w) st = proc_merge(st, wave_state[w]);
-    a.parts[row * a.slices + slice] = make_float4(st.m, st.s, st.u, __int_as_float(st.id));
+    first_id = 0x7FFFFFFF;
+    first_nan = 0x7FFFFFFF;
+  }
+  int invalid = 0;
+  if constexpr (HIST != HIST_NONE || LIST) {
+    lds_clear(sh, proc_count_words(HIST, kSlice) + (LIST ? kSlice : 0));
+    lds_barrier();
+    if constexpr (HIST != HIST_NONE)
+      if (!wide) invalid = proc_history_slice<HIST, false>(a, r, lo, n, count);
+    if constexpr (LIST)
+      if (tid < 64)
+        invalid += proc_bias_slice(a, r, lo, n, sum,
+                                   sh + proc_count_words(HIST, kSlice) + kSlice);
+  }
+  lds_barrier();
+  float x[STEPS][8];
+#pragma unroll
+  for (int j = 0; j < STEPS; ++j) {
+    const int v = j * kProcStep + tid * 8;
+    if (v < n) {
+      unpack_raw8<IN32>(raw[j], x[j]);
+      if (!wide) proc_penalise<HIST, false>(count, v, sc, x[j]);
+    }
+  }
+  if constexpr (HIST == HIST_COUNT) {
+    // Half the slice at a time has room for counts of 32 bits.
+    for (int half = 0; wide && half < 2; ++half) {
+      lds_barrier();
+      lds_clear(count, kSlice / 2);
+      lds_barrier();
+      const int from = half * (kSlice / 2);
+      const int ids = n - from < kSlice / 2 ? n - from : kSlice / 2;
+      const int found = proc_history_slice<HIST, true>(a, r, lo + from, ids, count);
+      if (half == 0) invalid += found;
+      lds_barrier();
+#pragma unroll
+      for (int j = 0; j < STEPS; ++j) {
+        const int v = j * kProcStep + tid * 8 - from;
+        if (v >= 0 && v < ids) proc_penalise<HIST, true>(count, v, sc, x[j]);
+      }
+    }
+  }
+  float top = -INFINITY;
+#pragma unroll
+  for (int j = 0; j < STEPS; ++j) {
+    const int v = j * kProcStep + tid * 8, left = n - v;
+    if (left > 0) {
+      if (a.o.bias != nullptr) {
+        float b[8];
+        load8<true>(a.o.bias, row * a.o.bias_stride + lo + v, left, b);
+#pragma unroll
+        for (int k = 0; k < 8; ++k) x[j][k] = x[j][k] + b[k];
+      }
+      if constexpr (LIST) {
+#pragma unroll
+        for (int k = 0; k < 8; ++k) x[j][k] = x[j][k] + sum[v + k];
+      }
+#pragma unroll
+      for (int k = 0; k < 8; ++k)
+        x[j][k] = select_bit(allowed[j], k, x[j][k] * sc.inv_t, -INFINITY);
+      if (r.bad) {
+#pragma unroll
+        for (int k = 0; k < 8; ++k) x[j][k] = NAN;
+      }
+      store8<OUT32>(a.out, row * a.ld_out + lo + v, left, x[j]);
+      // The statistics are those of the values as they are returned.
+      if constexpr (!OUT32) unpack8(pack8(x[j]), x[j]);
+      if (left < 8) {
+#pragma unroll
+        for (int k = 0; k < 8; ++k)
+          if (k >= left) x[j][k] = -INFINITY;
+      }
+    } else {
+#pragma unroll
+      for (int k = 0; k < 8; ++k) x[j][k] = -INFINITY;
+    }
+#pragma unroll
+    for (int k = 0; k < 8; ++k) top = fmaxf(top, x[j][k]);
+  }
+  const float wmax = wave_all(top, MaxOp{});
+  if constexpr (HIST != HIST_NONE || LIST) {
+    if (slice == 0)
+      for (int d = 32; d > 0; d >>= 1) invalid += __shfl_down(invalid, d, 64);
+  }
+  if ((tid & 63) == 0) {
+    wave_max[tid >> 6] = wmax;
+    wave_invalid[tid >> 6] = invalid;
+  }
+  lds_barrier();
+  float m = wave_max[0];
+#pragma unroll
+  for (int w = 1; w < kWaves; ++w) m = fmaxf(m, wave_max[w]);
+  // Nothing is allowed: every term is exp(-inf).
+  const float base = m == -INFINITY ? 0.f : m;
+  float s = 0.f, u = 0.f;
+#pragma unroll
+  for (int j = 0; j < STEPS; ++j)
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+      const float d = x[j][k] - base;
+      const float e = __builtin_amdgcn_exp2f(d * kLog2e);
+      s = s + e;
+      u = __builtin_fmaf(e, fmaxf(d, kMostNegative), u);
+    }
+  if (top == m && m != -INFINITY) {
+    int id = 0x7FFFFFFF;
+#pragma unroll
+    for (int j = STEPS - 1; j >= 0; --j)
+#pragma unroll
+      for (int k = 7; k >= 0; --k)
+        if (x[j][k] == m) id = (int)lo + j * kProcStep + tid * 8 + k;
+    atomicMin(&first_id, id);
+  }
+  if (s != s) {
+    // A NaN among the thread's values, or infinity - infinity.
+#pragma unroll
+    for (int j = STEPS - 1; j >= 0; --j)
+#pragma unroll
+      for (int k = 7; k >= 0; --k)
+        if (x[j][k] != x[j][k]) atomicMin(&first_nan, (int)lo + j * kProcStep + tid * 8 + k);
+  }
+  s = wave_all(s, SumOp{});
+  u = wave_all(u, SumOp{});
+  if ((tid & 63) == 0) {
+    wave_s[tid >> 6] = s;
+    wave_u[tid >> 6] = u;
+  }
+  lds_barrier();
+  if (tid == 0) {
+#pragma unroll
+    for (int w = 1; w < kWaves; ++w) {
+      s += wave_s[w];
+      u += wave_u[w];
+      invalid += wave_invalid[w];
+    }
+    int id = m == -INFINITY ? -1 : first_id;
+    if (first_nan != 0x7FFFFFFF) {
+      m = NAN;
+      id = r.bad ? -1 : first_nan;
+    }
+    a.parts[row * a.slices + slice] = make_float4(m, s, u, __int_as_float(id));
+    if (slice == 0) a.invalid[row] = invalid + (r.bad ? 1 : 0);
   }
 }
 
@@ -431,7 +609,7 @@ __global__ void __launch_bounds__(kProcThreads) process_grad_kernel(ProcArgs a) 
   if constexpr (SEEN) {
     for (int i = tid; i < a.slice / 32; i += kProcThreads) sh[i] = 0;
     __syncthreads();
-    invalid = proc_history_slice<HIST_SEEN>(a, r, lo, n, sh);
+    invalid = proc_history_slice<HIST_SEEN, false>(a, r, lo, n, sh);
   }
   if (slice == 0) {
     for (int d = 32; d > 0; d >>= 1) invalid += __shfl_down(invalid, d, 64);

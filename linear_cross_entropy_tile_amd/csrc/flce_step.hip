@@ -27,19 +27,30 @@ void launch_logits(const LogitsArgs& a, bool f32, dim3 grid, hipStream_t st) {
 
 // ---- processing of logits ----------------------------------------------------------
 
-template <int HIST, bool LIST>
-void launch_process(const ProcArgs& a, unsigned grid, hipStream_t st) {
-  const size_t words = HIST == HIST_COUNT ? a.slice : (HIST == HIST_SEEN ? a.slice / 32 : 0);
-  const size_t lds = 4 * (words + (LIST ? 2 * (size_t)a.slice : 0));
+template <int HIST, bool LIST, int STEPS>
+void launch_process_types(const ProcArgs& a, unsigned grid, hipStream_t st) {
   const bool i = a.o.logits_dtype == FLCE_GRAD_F32, o = a.o.out_dtype == FLCE_GRAD_F32;
   if (i && o)
-    process_kernel<HIST, LIST, true, true><<<grid, kProcThreads, lds, st>>>(a);
+    process_kernel<HIST, LIST, STEPS, true, true><<<grid, kProcThreads, 0, st>>>(a);
   else if (i)
-    process_kernel<HIST, LIST, true, false><<<grid, kProcThreads, lds, st>>>(a);
+    process_kernel<HIST, LIST, STEPS, true, false><<<grid, kProcThreads, 0, st>>>(a);
   else if (o)
-    process_kernel<HIST, LIST, false, true><<<grid, kProcThreads, lds, st>>>(a);
+    process_kernel<HIST, LIST, STEPS, false, true><<<grid, kProcThreads, 0, st>>>(a);
   else
-    process_kernel<HIST, LIST, false, false><<<grid, kProcThreads, lds, st>>>(a);
+    process_kernel<HIST, LIST, STEPS, false, false><<<grid, kProcThreads, 0, st>>>(a);
+}
+template <int HIST, bool LIST>
+void launch_process(const ProcArgs& a, unsigned grid, hipStream_t st) {
+  if (a.slice == kProcStep) {
+    launch_process_types<HIST, LIST, 1>(a, grid, st);
+  } else if (a.slice == kProcSteps * kProcStep) {
+    launch_process_types<HIST, LIST, kProcSteps>(a, grid, st);
+  } else if constexpr (HIST != HIST_NONE && !LIST) {
+    if (a.o.out_dtype == FLCE_GRAD_F32)
+      process_kernel<HIST, LIST, kProcStepsHistory, false, true><<<grid, kProcThreads, 0, st>>>(a);
+    else
+      process_kernel<HIST, LIST, kProcStepsHistory, false, false><<<grid, kProcThreads, 0, st>>>(a);
+  }
 }
 
 template <bool SEEN, bool STATS>
@@ -165,7 +176,7 @@ flce_status_t flce_logits(const void* hidden, const void* weight, const float* b
 
 flce_status_t flce_process_workspace_size(int64_t N, int64_t V, size_t* bytes) {
   if (N < 0 || N > kMaxN || V < 1 || V > kMaxV) return FLCE_ERR_BAD_SHAPE;
-  if (bytes) *bytes = make_proc_plan(N, V, true).total;
+  if (bytes) *bytes = make_proc_plan(N, V, kProcSteps).total;
   return FLCE_OK;
 }
 
@@ -184,7 +195,9 @@ flce_status_t flce_process_logits(const void* logits, int64_t ld, int64_t N, int
   if (N > 0 && logits == out && (opt->logits_dtype != opt->out_dtype || ld != ld_out))
     return FLCE_ERR_BAD_OPTION;
   const bool list = opt->bias_offsets != nullptr;
-  const ProcPlan p = make_proc_plan(N, V, list);
+  const int hist = proc_history(*opt, false);
+  const bool far = hist != HIST_NONE && !list && opt->logits_dtype == FLCE_GRAD_BF16;
+  const ProcPlan p = make_proc_plan(N, V, far ? kProcStepsHistory : kProcSteps);
   if (workspace_bytes < p.total) return FLCE_ERR_WORKSPACE_TOO_SMALL;
   hipStream_t st = static_cast<hipStream_t>(stream);
   ProcArgs a = process_args(N, V, *opt, p, workspace);
@@ -195,7 +208,6 @@ flce_status_t flce_process_logits(const void* logits, int64_t ld, int64_t N, int
   a.lse = lse;
   a.entropy = entropy;
   a.greedy = greedy;
-  const int hist = proc_history(*opt, false);
   FLCE_TRY(over_rows(a, K_PROCESS, st, [&](const ProcArgs& b, unsigned grid) {
     switch (hist * 2 + (list ? 1 : 0)) {
       case 0: launch_process<HIST_NONE, false>(b, grid, st); break;
@@ -235,7 +247,7 @@ flce_status_t flce_process_logits_backward(const flce_process_grads_t* grads, co
   if (N > 0 && g.grad_out == grad_logits &&
       (opt->logits_dtype != opt->out_dtype || g.ld_grad_out != ld_grad))
     return FLCE_ERR_BAD_OPTION;
-  const ProcPlan p = make_proc_plan(N, V, false);
+  const ProcPlan p = make_proc_plan(N, V, kProcSteps);
   if (workspace_bytes < p.total) return FLCE_ERR_WORKSPACE_TOO_SMALL;
   hipStream_t st = static_cast<hipStream_t>(stream);
   ProcArgs a = process_args(N, V, *opt, p, workspace);

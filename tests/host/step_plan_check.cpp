@@ -45,15 +45,15 @@ static void check_logits_plan(int64_t N, int64_t H, int64_t V) {
 }
 
 static void check_proc_plan(int64_t N, int64_t V) {
-  const size_t promised = make_proc_plan(N, V, true).total;
-  for (int list = 0; list < 2; ++list) {
-    const ProcPlan p = make_proc_plan(N, V, list != 0);
-    CHECK(p.slice % kProcStep == 0 && p.slices >= 1 && p.slices * p.slice >= V);
+  const size_t promised = make_proc_plan(N, V, kProcSteps).total;
+  for (int most : {kProcSteps, kProcStepsHistory}) {
+    const ProcPlan p = make_proc_plan(N, V, most);
+    CHECK(p.slices >= 1 && p.slices * p.slice >= V);
     CHECK((p.slices - 1) * p.slice < V && p.slices <= kMaxGrid);
-    // Counts, sums and tags of a slice.
-    CHECK(4 * (size_t)p.slice * (list ? 3 : 1) + 1024 <= 65536);
+    // One of the kernel's slices.
+    CHECK(p.slice == kProcStep || p.slice == most * kProcStep);
     CHECK(p.parts % 16 == 0 && p.parts + 16 * (size_t)N * p.slices <= p.invalid);
-    CHECK(p.invalid + 4 * (size_t)N <= p.total && p.total <= promised);
+    CHECK(p.invalid + 4 * (size_t)N <= p.total && p.total == promised);
   }
 }
 
