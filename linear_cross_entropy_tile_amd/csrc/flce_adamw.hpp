@@ -50,17 +50,29 @@ __device__ __forceinline__ int table_find(const First& first, int count, int b) 
   return lo;
 }
 
+// Four loads a thread are in flight.
 template <bool F32>
 __device__ __forceinline__ double norm_chunk_sum(const void* p, int64_t i0, int64_t i1) {
-  double s = 0.0;
-  for (int64_t i = i0 + threadIdx.x * 8; i < i1; i += 8 * kNormThreads) {
+  constexpr int U = 4, kStride = 8 * kNormThreads;
+  double s[U] = {0.0, 0.0, 0.0, 0.0};
+  int64_t i = i0 + threadIdx.x * 8;
+  for (; i + (U - 1) * kStride + 8 <= i1; i += U * kStride) {
+    float v[U][8];
+#pragma unroll
+    for (int u = 0; u < U; ++u) load8<F32>(p, i + u * kStride, 8, v[u]);
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+#pragma unroll
+      for (int k = 0; k < 8; ++k) s[u] += (double)v[u][k] * (double)v[u][k];
+  }
+  for (; i < i1; i += kStride) {
     const int64_t left = i1 - i;
     float v[8];
     load8<F32>(p, i, left < 8 ? (int)left : 8, v);
 #pragma unroll
-    for (int k = 0; k < 8; ++k) s += (double)v[k] * (double)v[k];
+    for (int k = 0; k < 8; ++k) s[0] += (double)v[k] * (double)v[k];
   }
-  return s;
+  return (s[0] + s[1]) + (s[2] + s[3]);
 }
 
 template <int WAVES>
@@ -188,15 +200,16 @@ struct AdamArgs {
   const AdamCoef* coef;
 };
 
-// Random bits of value i of a tensor of key k: 16 for the weight, 16 for each moment.
+// Random bits of value i of a tensor of key k: 16 for the weight; in `moments` the
+// upper 16 for the first and the lower 16 for the second.
 struct AdamBits {
-  uint32_t p, m, v;
+  uint32_t p, moments;
 };
 __device__ __forceinline__ AdamBits adam_bits(uint32_t key, uint32_t i) {
   const uint32_t h = hash32(i ^ key);
   uint32_t g = (h ^ 0x6A09E667u) * 0x9E3779B1u;
   g ^= g >> 16;
-  return {h >> 16, g >> 16, g & 0xFFFFu};
+  return {h >> 16, g};
 }
 
 // fp32 bits of x rounded to bf16, up with the probability of the part cut off.
@@ -206,36 +219,47 @@ __device__ __forceinline__ float bf16_stochastic(float x, uint32_t bits) {
   return (b & 0x7F800000u) == 0x7F800000u ? x : __builtin_bit_cast(float, up);
 }
 
-// The value of the e4m3 code next below or above y (|y| <= 448), up with the
-// probability of the part cut off.
-__device__ __forceinline__ float e4m3_stochastic(float y, uint32_t bits) {
-  const float a = fabsf(y);
-  const float large = __builtin_bit_cast(
-      float, (__builtin_bit_cast(uint32_t, a) + (bits << 4)) & 0xFFF00000u);
-  const float small = floorf(a * 512.f + (float)bits * 0x1p-16f) * 0x1p-9f;
-  return copysignf(a >= 0x1p-6f ? large : small, y);
-}
-
-// EXACT: the root rounded correctly. 8-bit states keep the root, whose last bit can
-// decide a code and with it a block's scale.
-template <bool EXACT>
-__device__ __forceinline__ void adam_value(const AdamCoef& c, float g, float& p, float& m,
-                                           float& v, float& r) {
+// The gradient scaled, and both moments.
+__device__ __forceinline__ void adam_moments(const AdamCoef& c, float g, float& m, float& v) {
 #pragma clang fp contract(off)
   g = g * c.scale;
   m = m * c.b1 + g * c.a1;
   v = v * c.b2 + (g * g) * c.a2;
-  // Otherwise, and for the quotient, the hardware's approximations (1 ulp each): the
-  // update is far below the weight.
-  if constexpr (EXACT) {
-    r = sqrtf(v);
-  } else {
-    // The instruction flushes denormals, which a scale of 2^32 takes out of them.
-    const bool tiny = v < 0x1p-96f;
-    r = __builtin_amdgcn_sqrtf(tiny ? v * 0x1p32f : v);
-    r = tiny ? r * 0x1p-16f : r;
+}
+// The weight, from the root r of the second moment. The quotient's reciprocal is the
+// hardware's (1 ulp): the update is far below the weight.
+__device__ __forceinline__ float adam_weight(const AdamCoef& c, float p, float m, float r) {
+#pragma clang fp contract(off)
+  return p * c.keep - c.rise * (m * __builtin_amdgcn_rcpf(r * c.root + c.eps));
+}
+
+// Root within 1 ulp. The instruction flushes denormals, which a scale of 2^32 takes out
+// of them.
+__device__ __forceinline__ float root_near(float v) {
+  const bool tiny = v < 0x1p-96f;
+  const float r = __builtin_amdgcn_sqrtf(tiny ? v * 0x1p32f : v);
+  return tiny ? r * 0x1p-16f : r;
+}
+// Roots rounded to the nearest: the last bit of a root that is kept in 8 bits can decide
+// a code, and with it a block's scale. One Newton step from the reciprocal root on x and
+// on 1 / (2 x), then the remainder, in 11 instruction slots a value against sqrtf's 20
+// (equal to it for every mantissa); values that it does not hold for (0, below 2^-96, infinities) take sqrtf.
+__device__ __forceinline__ void roots16(const float (&v)[16], float (&r)[16]) {
+  bool odd = false;
+#pragma unroll
+  for (int k = 0; k < 16; ++k) {
+    const float y = __builtin_amdgcn_rsqf(v[k]);
+    float x = v[k] * y, h = 0.5f * y;
+    const float e = __builtin_fmaf(-h, x, 0.5f);
+    x = __builtin_fmaf(x, e, x);
+    h = __builtin_fmaf(h, e, h);
+    r[k] = __builtin_fmaf(__builtin_fmaf(-x, x, v[k]), h, x);
+    odd = odd || !(v[k] >= 0x1p-96f && v[k] < INFINITY);
   }
-  p = p * c.keep - c.rise * (m * __builtin_amdgcn_rcpf(r * c.root + c.eps));
+  if (odd) {
+#pragma unroll
+    for (int k = 0; k < 16; ++k) r[k] = sqrtf(v[k]);
+  }
 }
 
 // W values of an update with fp32 states, from element i on (n of them).
@@ -252,8 +276,8 @@ __device__ __forceinline__ void adam_f32(const AdamEntry& e, const AdamCoef& c, 
   load8<true>(e.v, i, n, v);
 #pragma unroll
   for (int k = 0; k < 8; ++k) {
-    float r;
-    adam_value<false>(c, g[k], p[k], m[k], v[k], r);
+    adam_moments(c, g[k], m[k], v[k]);
+    p[k] = adam_weight(c, p[k], m[k], root_near(v[k]));
   }
   store8<true>(e.m, i, n, m);
   store8<true>(e.v, i, n, v);
@@ -330,7 +354,9 @@ __device__ __forceinline__ float row16_max(float v) {
 constexpr float kTinyBlock = 0x1p-100f;
 
 // Codes of 16 values whose block of 256 lies in the row of 16 lanes; returns the
-// block's scale. POSITIVE: values >= 0, of which those above 0 get a code above 0.
+// block's scale. POSITIVE: values >= 0, of which those above 0 get a code above 0. SR:
+// stochastic rounding by the upper 16 of `bits` (the others 0), which the conversion adds
+// to the part that it cuts off.
 template <bool SR, bool POSITIVE>
 __device__ __forceinline__ float encode16(const float (&x)[16], const uint32_t (&bits)[16],
                                           uint32_t (&w)[4]) {
@@ -346,13 +372,20 @@ __device__ __forceinline__ float encode16(const float (&x)[16], const uint32_t (
     float y[4];
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
-      const float exact = x[4 * q + k] * up;
-      y[k] = exact;
-      if constexpr (SR) y[k] = e4m3_stochastic(exact, bits[4 * q + k]);
-      if (POSITIVE && exact > 0.f) y[k] = fmaxf(y[k], 0x1p-9f);
+      y[k] = x[4 * q + k] * up;
+      if constexpr (POSITIVE) y[k] = y[k] > 0.f ? fmaxf(y[k], 0x1p-9f) : y[k];
     }
-    int word = __builtin_amdgcn_cvt_pk_fp8_f32(y[0], y[1], 0, false);
-    w[q] = (uint32_t)__builtin_amdgcn_cvt_pk_fp8_f32(y[2], y[3], word, true);
+    int word = 0;
+    if constexpr (SR) {
+      word = __builtin_amdgcn_cvt_sr_fp8_f32(y[0], (int)bits[4 * q], word, 0);
+      word = __builtin_amdgcn_cvt_sr_fp8_f32(y[1], (int)bits[4 * q + 1], word, 1);
+      word = __builtin_amdgcn_cvt_sr_fp8_f32(y[2], (int)bits[4 * q + 2], word, 2);
+      word = __builtin_amdgcn_cvt_sr_fp8_f32(y[3], (int)bits[4 * q + 3], word, 3);
+    } else {
+      word = __builtin_amdgcn_cvt_pk_fp8_f32(y[0], y[1], word, false);
+      word = __builtin_amdgcn_cvt_pk_fp8_f32(y[2], y[3], word, true);
+    }
+    w[q] = (uint32_t)word;
   }
   return live ? top * (1.f / 448.f) : 0.f;
 }
@@ -373,6 +406,7 @@ __device__ __forceinline__ void decode16(const uint32_t (&w)[4], float (&x)[16])
 template <bool P32, bool G32, bool MASTER, bool SR>
 __device__ __forceinline__ void adam_8bit(const AdamEntry& e, const AdamCoef& c, uint32_t key,
                                           int64_t i, int n) {
+#pragma clang fp contract(off)
   float p[16], g[16], m[16], v[16];
   uint32_t mw[4], vw[4], mb[16], vb[16];
   if constexpr (MASTER)
@@ -389,22 +423,26 @@ __device__ __forceinline__ void adam_8bit(const AdamEntry& e, const AdamCoef& c,
   const uint32_t k0 = SR ? hash32(key ^ (uint32_t)((uint64_t)i >> 32)) : 0;
 #pragma unroll
   for (int k = 0; k < 16; ++k) {
-#pragma clang fp contract(off)
     const float q = v[k] * vs;
-    float mk = m[k] * ms, vk = q * q, r;
-    adam_value<true>(c, g[k], p[k], mk, vk, r);
-    m[k] = mk;
-    v[k] = r;
+    m[k] = m[k] * ms;
+    v[k] = q * q;
+    adam_moments(c, g[k], m[k], v[k]);
+  }
+  float r[16];
+  roots16(v, r);
+#pragma unroll
+  for (int k = 0; k < 16; ++k) {
+    p[k] = adam_weight(c, p[k], m[k], r[k]);
     if constexpr (SR) {
       const AdamBits b = adam_bits(k0, (uint32_t)i + k);
-      mb[k] = b.m;
-      vb[k] = b.v;
+      mb[k] = b.moments & 0xFFFF0000u;
+      vb[k] = b.moments << 16;
       if constexpr (!P32 && !MASTER) p[k] = bf16_stochastic(p[k], b.p);
     }
   }
   // Lanes and values past the end: a gradient, weight and moments of 0 give 0.
   const float ms1 = encode16<SR, false>(m, mb, mw);
-  const float vs1 = encode16<SR, true>(v, vb, vw);
+  const float vs1 = encode16<SR, true>(r, vb, vw);
   if (n <= 0) return;
   store_codes(e.m, i, n, mw);
   store_codes(e.v, i, n, vw);
