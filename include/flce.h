@@ -712,8 +712,8 @@ enum { FLCE_STATE_F32 = 0, FLCE_STATE_8BIT = 1 };
 enum { FLCE_ROUND_NEAREST = 0, FLCE_ROUND_STOCHASTIC = 1 };
 
 /* The tensors of an update: host arrays of `count` entries. Tensor i has sizes[i]
- * values, its pointers are device pointers aligned to their elements; sizes of 0 are
- * passed over. With FLCE_STATE_8BIT the states are e4m3 codes (OCP: the largest is 448)
+ * values, its pointers are device pointers aligned to their elements, to memory of its
+ * own; sizes of 0 are passed over. With FLCE_STATE_8BIT the states are e4m3 codes (OCP: the largest is 448)
  * in blocks of 256 values from the tensor's start on, and exp_avg_scales and
  * exp_avg_sq_scales (fp32, one a block) what a code is multiplied by; exp_avg_sqs then
  * holds the root of the second moment. */
@@ -752,7 +752,8 @@ size_t flce_adamw_workspace_size(void);
  *   g = s grad,  m = beta1 m + (1 - beta1) g,  v = beta2 v + (1 - beta2) g^2,
  *   p = (1 - lr weight_decay) p - lr / (1 - beta1^t) m / (sqrt(v) / sqrt(1 - beta2^t) + eps).
  * If s is not finite (an overflow in the backward), nothing is changed, step among
- * it. In 8-bit states a block's scale is its largest magnitude a times 1 / 448 and
+ * it (without a grad_scale, a gradient that is not finite makes its weight and states
+ * NaN, in 8 bits its block's states). In 8-bit states a block's scale is its largest magnitude a times 1 / 448 and
  * its codes are those of the values times 448 (1 / a) (all 0 if a is below 2^-100), in
  * fp32; a second moment above 0 has a code above 0.
  * Stochastic rounding goes up with the probability of the part cut off, by 16 bits

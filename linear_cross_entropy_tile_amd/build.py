@@ -56,8 +56,9 @@ C_CHECK_DIR = os.path.join(ROOT, "tests", "c_abi")
 
 def build_c_check(verbose: bool = False, name: str = "flce_c_check") -> str:
     """Compiles a plain-C99 program that drives the C ABI (a GPU test runs it;
-    flce_c_check: the head, flce_ops_check: the operators beside it) against
-    the in-tree library, with gcc: the header must be valid C."""
+    flce_c_check: the head, flce_ops_check: the operators beside it,
+    flce_step_check: those at the ends of a training step) against the in-tree
+    library, with gcc: the header must be valid C."""
     rocm = os.environ.get("ROCM_PATH", "/opt/rocm")
     exe = os.path.join(C_CHECK_DIR, name)
     cmd = ["gcc", "-std=c99", "-O2", "-Wall", "-Werror", "-D__HIP_PLATFORM_AMD__",
@@ -79,3 +80,4 @@ if __name__ == "__main__":
     print(build(verbose=True))
     print(build_c_check(verbose=True))
     print(build_c_check(verbose=True, name="flce_ops_check"))
+    print(build_c_check(verbose=True, name="flce_step_check"))

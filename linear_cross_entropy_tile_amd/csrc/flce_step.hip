@@ -41,16 +41,10 @@ void launch_process_types(const ProcArgs& a, unsigned grid, hipStream_t st) {
 }
 template <int HIST, bool LIST>
 void launch_process(const ProcArgs& a, unsigned grid, hipStream_t st) {
-  if (a.slice == kProcStep) {
+  if (a.slice == kProcStep)
     launch_process_types<HIST, LIST, 1>(a, grid, st);
-  } else if (a.slice == kProcSteps * kProcStep) {
+  else
     launch_process_types<HIST, LIST, kProcSteps>(a, grid, st);
-  } else if constexpr (HIST != HIST_NONE && !LIST) {
-    if (a.o.out_dtype == FLCE_GRAD_F32)
-      process_kernel<HIST, LIST, kProcStepsHistory, false, true><<<grid, kProcThreads, 0, st>>>(a);
-    else
-      process_kernel<HIST, LIST, kProcStepsHistory, false, false><<<grid, kProcThreads, 0, st>>>(a);
-  }
 }
 
 template <bool SEEN, bool STATS>
@@ -176,7 +170,7 @@ flce_status_t flce_logits(const void* hidden, const void* weight, const float* b
 
 flce_status_t flce_process_workspace_size(int64_t N, int64_t V, size_t* bytes) {
   if (N < 0 || N > kMaxN || V < 1 || V > kMaxV) return FLCE_ERR_BAD_SHAPE;
-  if (bytes) *bytes = make_proc_plan(N, V, kProcSteps).total;
+  if (bytes) *bytes = make_proc_plan(N, V).total;
   return FLCE_OK;
 }
 
@@ -196,8 +190,7 @@ flce_status_t flce_process_logits(const void* logits, int64_t ld, int64_t N, int
     return FLCE_ERR_BAD_OPTION;
   const bool list = opt->bias_offsets != nullptr;
   const int hist = proc_history(*opt, false);
-  const bool far = hist != HIST_NONE && !list && opt->logits_dtype == FLCE_GRAD_BF16;
-  const ProcPlan p = make_proc_plan(N, V, far ? kProcStepsHistory : kProcSteps);
+  const ProcPlan p = make_proc_plan(N, V);
   if (workspace_bytes < p.total) return FLCE_ERR_WORKSPACE_TOO_SMALL;
   hipStream_t st = static_cast<hipStream_t>(stream);
   ProcArgs a = process_args(N, V, *opt, p, workspace);
@@ -247,7 +240,7 @@ flce_status_t flce_process_logits_backward(const flce_process_grads_t* grads, co
   if (N > 0 && g.grad_out == grad_logits &&
       (opt->logits_dtype != opt->out_dtype || g.ld_grad_out != ld_grad))
     return FLCE_ERR_BAD_OPTION;
-  const ProcPlan p = make_proc_plan(N, V, kProcSteps);
+  const ProcPlan p = make_proc_plan(N, V);
   if (workspace_bytes < p.total) return FLCE_ERR_WORKSPACE_TOO_SMALL;
   hipStream_t st = static_cast<hipStream_t>(stream);
   ProcArgs a = process_args(N, V, *opt, p, workspace);

@@ -96,30 +96,24 @@ struct ProcPlan {
   size_t parts, invalid, total;
 };
 
-// Steps of a slice: two, or four for bf16 logits with a history, which every slice of a
-// row reads again (512 rows of 152064 bf16 logits with histories of 1000 to 2048
-// tokens: 96 us against 102; fp32 ones, with twice the registers, take 73 us against 61
-// at 256 rows of 128256); one where that leaves the GPU less than 1024 blocks (four a
-// CU).
-constexpr int kProcSteps = 2, kProcStepsHistory = 4;
-inline int proc_steps(int64_t N, int64_t V, int most) {
-  return N * ceil_div(V, (int64_t)most * kProcStep) < 1024 ? 1 : most;
+// Steps of a slice: two, or one where that leaves the GPU less than 1024 blocks (four a
+// CU). Four (half the readings of a row's history, but twice the registers) are no
+// faster: 512 rows of 152064 bf16 logits with histories of 1000 to 2048 tokens take 89
+// us with either.
+constexpr int kProcSteps = 2;
+inline int proc_steps(int64_t N, int64_t V) {
+  return N * ceil_div(V, (int64_t)kProcSteps * kProcStep) < 1024 ? 1 : kProcSteps;
 }
 
 // Workspace: header, the softmax state and first largest id of every slice
-// [N, slices], the invalid tokens of every row [N]. Its size is that of slices of
-// kProcSteps or one step, whatever `most` is.
-inline ProcPlan make_proc_plan(int64_t N, int64_t V, int most) {
+// [N, slices], the invalid tokens of every row [N].
+inline ProcPlan make_proc_plan(int64_t N, int64_t V) {
   ProcPlan p{};
-  p.slice = proc_steps(N, V, most) * kProcStep;
+  p.slice = proc_steps(N, V) * kProcStep;
   p.slices = ceil_div(V, p.slice);
-  int64_t room = ceil_div(V, (int64_t)proc_steps(N, V, kProcSteps) * kProcStep);
-  if (room < p.slices) room = p.slices;
-  const int64_t longest = ceil_div(V, (int64_t)proc_steps(N, V, kProcStepsHistory) * kProcStep);
-  if (room < longest) room = longest;
   size_t off = kHeaderBytes;
   p.parts = off;
-  off = align_up(off + 16 * (size_t)N * (size_t)room);
+  off = align_up(off + 16 * (size_t)N * (size_t)p.slices);
   p.invalid = off;
   off = align_up(off + 4 * (size_t)N);
   p.total = off;

@@ -45,6 +45,13 @@ __device__ __forceinline__ void store_any(void* p, const T& v) {
   __builtin_memcpy(p, &v, sizeof(T));
 }
 
+// The same past the caches (nontemporal), for outputs larger than those.
+template <class T>
+__device__ __forceinline__ void stream_any(void* p, const T& v) {
+  typedef T loose __attribute__((aligned(2)));
+  __builtin_nontemporal_store(v, static_cast<loose*>(p));
+}
+
 // Eight consecutive values of an array of bf16 or fp32 from element i on, at any
 // address; the first `n` of them where n < 8 (the others read as 0 or stay).
 template <bool F32>
@@ -81,13 +88,19 @@ __device__ __forceinline__ void store1(void* p, int64_t i, float v) {
   else
     static_cast<uint16_t*>(p)[i] = (uint16_t)bf16_pair(v, 0.f);
 }
-template <bool F32>
+template <bool F32, bool STREAM = false>
 __device__ __forceinline__ void store8(void* p, int64_t i, int n, const float (&v)[8]) {
   if constexpr (F32) {
     float* q = static_cast<float*>(p) + i;
     if (n >= 8) {
-      store_any(q, ef32x4{v[0], v[1], v[2], v[3]});
-      store_any(q + 4, ef32x4{v[4], v[5], v[6], v[7]});
+      const ef32x4 a{v[0], v[1], v[2], v[3]}, b{v[4], v[5], v[6], v[7]};
+      if constexpr (STREAM) {
+        stream_any(q, a);
+        stream_any(q + 4, b);
+      } else {
+        store_any(q, a);
+        store_any(q + 4, b);
+      }
       return;
     }
 #pragma unroll
@@ -97,7 +110,10 @@ __device__ __forceinline__ void store8(void* p, int64_t i, int n, const float (&
     uint16_t* q = static_cast<uint16_t*>(p) + i;
     const eu32x4 w = pack8(v);
     if (n >= 8) {
-      store_any(q, w);
+      if constexpr (STREAM)
+        stream_any(q, w);
+      else
+        store_any(q, w);
       return;
     }
 #pragma unroll

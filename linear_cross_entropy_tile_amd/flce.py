@@ -1266,6 +1266,13 @@ def _torch_dtype(code):
     return torch.float32 if code == FLCE_GRAD_F32 else torch.bfloat16
 
 
+def _written(tensors) -> None:
+    """Tells autograd that a call has written to these tensors: a graph that saved
+    one of them refuses its backward."""
+    torch = _torch()
+    torch.autograd.graph.increment_version([t for t in tensors if not t.is_inference()])
+
+
 def _out_rows(out, N, V, dtype, dev, name="out"):
     """(out or a new [N,V] tensor, row stride)."""
     torch = _torch()
@@ -1299,10 +1306,13 @@ def logits(hidden, weight, bias=None, softcap: float = 0.0, out_dtype: str = "f3
     if bias is not None:
         _check_vector(bias, torch.float32, V, dev.index, "bias")
     odt = _choice(_GRAD_DTYPES, out_dtype, "out_dtype")
+    given = out is not None
     out, ld = _out_rows(out, N, V, _torch_dtype(odt), dev)
     workspace = _workspace(workspace, _logits_bytes(N, H, V), dev)
     _call(dev, "flce_logits", hidden.data_ptr(), weight.data_ptr(), _ptr(bias), N, H, V,
           float(softcap), odt, out.data_ptr(), ld, workspace.data_ptr(), workspace.numel())
+    if given:
+        _written([out])
     return {"logits": out, "workspace": workspace}
 
 
@@ -1434,6 +1444,7 @@ def process_logits(logits, out_dtype=None, out=None, workspace=None, **options) 
     torch = _torch()
     N, V, ld, opt = _process_options(logits, out_dtype, **options)
     dev = logits.device
+    given = out is not None
     out, ld_out = _out_rows(out, N, V, _torch_dtype(opt.out_dtype), dev)
     workspace = _workspace(workspace, _process_bytes(N, V), dev)
     stats = torch.empty((2, N), dtype=torch.float32, device=dev)
@@ -1442,6 +1453,8 @@ def process_logits(logits, out_dtype=None, out=None, workspace=None, **options) 
     _call(dev, "flce_process_logits", logits.data_ptr(), ld, N, V, opt, out.data_ptr(), ld_out,
           lse.data_ptr(), entropy.data_ptr(), greedy.data_ptr(), workspace.data_ptr(),
           workspace.numel())
+    if given:
+        _written([out])
     return {"logits": out, "lse": lse, "entropy": entropy, "greedy": greedy,
             "workspace": workspace}
 
@@ -1482,10 +1495,13 @@ def process_logits_backward(grad_out, logits, processed=None, lse=None, entropy=
         raise ValueError("grad_lse and grad_entropy need processed and lse")
     if grad_entropy is not None and entropy is None:
         raise ValueError("grad_entropy needs entropy")
+    given = out is not None
     out, ld_grad = _out_rows(out, N, V, logits.dtype, dev)
     workspace = _workspace(workspace, _process_bytes(N, V), dev)
     _call(dev, "flce_process_logits_backward", g, logits.data_ptr(), ld, N, V, opt,
           out.data_ptr(), ld_grad, workspace.data_ptr(), workspace.numel())
+    if given:
+        _written([out])
     return out
 
 
@@ -1601,7 +1617,7 @@ def adamw_step(params, grads, state, lr=1e-3, beta1: float = 0.9, beta2: float =
     """One AdamW step over a list of tensors, in place (flce_adamw_step).
 
     params and grads: dense bf16 or fp32 tensors of the same sizes, the types in
-    any mixture; state: of ``adamw_state``, updated in place, its step raised by
+    any mixture, no parameter twice; state: of ``adamw_state``, updated in place, its step raised by
     one. lr: a number, or fp32 [1] on the device (a captured step then follows
     it). grad_scale: fp32 [1] that the gradients are multiplied by, e.g.
     ``grad_norm``'s scale; if it is not finite, nothing is changed. Under
@@ -1638,6 +1654,10 @@ def adamw_step(params, grads, state, lr=1e-3, beta1: float = 0.9, beta2: float =
                                  for t, p in zip(master, params)):
             raise ValueError("state master: fp32 parameters have no copy")
         lists[3] = array.array("Q", [0 if t is None else t.data_ptr() for t in master])
+    for a, name in ((lists[1], "params"), (lists[4], "state exp_avg"), (lists[5], "state exp_avg_sq")):
+        # Two of a list at one address would be updated at once. (No values, no address.)
+        if len(set(a)) < len(a) - max(0, sizes.count(0) - 1):
+            raise ValueError(f"{name}: the same tensor twice")
     step = state["step"]
     _check_vector(step, torch.int64, 1, dev.index, "state step")
     lr_device = None
@@ -1653,6 +1673,7 @@ def adamw_step(params, grads, state, lr=1e-3, beta1: float = 0.9, beta2: float =
     workspace = _workspace(workspace, _ADAMW_BYTES, dev)
     _call(dev, "flce_adamw_step", table, opt, _ptr(lr_device), _ptr(grad_scale),
           step.data_ptr(), workspace.data_ptr(), workspace.numel())
+    _written(params)
 
 
 _ADAMW_BYTES = 512  # flce_adamw_workspace_size()

@@ -315,6 +315,20 @@ def test_denormal_gradients_without_eps():
         assert abs(q[0][0].item() - 0.75) < 0.25 * 1e-3
 
 
+def test_a_step_between_forward_and_backward_is_noticed():
+    """Autograd sees the update: a graph that saved the weight refuses its backward."""
+    w = torch.ones(50, device=DEV, requires_grad=True)
+    loss = (w * w).sum()
+    state = flce.adamw_state([w])
+    with torch.no_grad():
+        flce.adamw_step([w], [torch.ones(50, device=DEV)], state)
+    with pytest.raises(RuntimeError, match="modified by an inplace operation"):
+        loss.backward()
+    with torch.inference_mode():
+        p = [torch.ones(50, device=DEV)]
+        flce.adamw_step(p, [torch.ones(50, device=DEV)], flce.adamw_state(p))
+
+
 def test_refusals():
     p = [torch.ones(300, device=DEV), torch.ones(4, device=DEV, dtype=torch.bfloat16)]
     g = [t.clone() for t in p]
@@ -325,7 +339,10 @@ def test_refusals():
            dict(params=[t.half() for t in p]), dict(grads=g[:1]), dict(grads=[g[0][:299], g[1]]),
            dict(grads=[torch.ones(300, 2, device=DEV)[:, 0], g[1]]),
            dict(grad_scale=torch.ones(2, device=DEV)), dict(lr=torch.ones(1, device=DEV).double()),
-           dict(rounding="up"), dict(state={**st, "exp_avg": s8["exp_avg"]}),
+           dict(rounding="up"), dict(params=[p[0], p[0][:4]]),
+           dict(params=[p[0], p[0]], grads=[g[0], g[0]]),
+           dict(state={**st, "exp_avg": [st["exp_avg"][0], st["exp_avg"][0][:4]]}),
+           dict(state={**st, "exp_avg": s8["exp_avg"]}),
            dict(state={**st, "exp_avg_sq": st["exp_avg"][:1]}),
            dict(state={**st, "step": torch.zeros(1, device=DEV)}),
            dict(state={**s8, "exp_avg_scale": [t[:1] for t in s8["exp_avg_scale"]]}),
