@@ -14,11 +14,14 @@
 // be aligned, so any vocabulary is read in place.
 //
 // With many rows the matrix units bound it, and the head's block tile of 256 columns
-// by 256 tokens takes it (logits_tile_kernel).
+// by 256 tokens takes it (logits_tile_kernel), or, where rows of the weight are not
+// aligned, logits_wide_kernel. make_logits_plan says which and why.
 #pragma once
 
 #include <hip/hip_runtime.h>
 #include <stdint.h>
+
+#include <type_traits>
 
 #include "flce_gemm.hpp"
 #include "flce_step_plan.hpp"
@@ -52,6 +55,12 @@ __device__ __forceinline__ float soft_cap(float z, float c, float inv_c) {
   const float far = copysignf((1.f - t) * __builtin_amdgcn_rcpf(1.f + t), x);
   const float near = x * (1.f + q * (q * (2.f / 15.f) - 1.f / 3.f));
   return c * (fabsf(x) < 0.04f ? near : far);
+}
+
+// LDS traffic of the block is complete; loads from memory may still be on their way.
+__device__ __forceinline__ void lds_barrier() {
+  wait_lgkmcnt0();
+  block_barrier();
 }
 
 // Bias and cap of the eight (n) columns from col on.
@@ -269,6 +278,156 @@ __global__ void __launch_bounds__(256) logits_sum_kernel(LogitsArgs a, int split
   }
   logits_finish(a, col, n, z);
   store8<OUT32>(a.out, t * a.ld_out + col, n, z);
+}
+
+// Up to 64 WM tokens at once for more than 64 of them, in any vocabulary of 128 ids or
+// more. The waves share the strip's weight rows, of which each thread brings 128 / WM
+// bytes a step to LDS, some steps ahead in registers and one in LDS; wave w takes the
+// tokens 64 w .. 64 w + 63 of the pass, reads the strip's eight rows of its lanes from
+// LDS and goes on like logits_kernel. One barrier a step. With one wave a SIMD and 254
+// registers the wait for LDS before the products is what bounds it: 200 tokens of hidden
+// size 4096 and 50257 ids take 192 us (430 TFLOP/s, 2.4 TB/s), 1024 take 650 us (648
+// TFLOP/s).
+template <int WM, bool OUT32>
+__global__ void __launch_bounds__(64 * WM, 2) logits_wide_kernel(LogitsArgs a) {
+  constexpr int kPieces = 8 / WM;           // 16-byte pieces a thread and step
+  constexpr int kAhead = 8 / kPieces;       // steps in registers
+  __shared__ __attribute__((aligned(16))) char sh[2][32 * 2 * kLogitStrip];
+  const int tid = threadIdx.x, lane = tid & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int c = lane & 15, g = lane >> 4;
+  const int group = (int)blockIdx.x / (8 * a.passes), in = (int)blockIdx.x % (8 * a.passes);
+  const int64_t v0 = (int64_t)(group * 8 + (in & 7)) * kLogitStrip;
+  if (v0 >= a.V) return;
+  // The last strip starts where it ends with the vocabulary; ids below v0 are not stored
+  // again.
+  const int64_t base = v0 < a.V - kLogitStrip ? v0 : a.V - kLogitStrip;
+  const int64_t t0 = (int64_t)(in >> 3) * (64 * WM) + 64 * wave;
+  const bool idle = t0 >= a.N;
+  const int whole = (int)(a.H / 32);  // steps
+  const uint16_t* strip = a.weight + base;
+
+  uint32_t hoff[4];  // bytes, at most 2^31; rows past the last token read the first one's
+#pragma unroll
+  for (int m = 0; m < 4; ++m) {
+    const int64_t t = t0 + 16 * m + c;
+    hoff[m] = (uint32_t)(2 * ((t < a.N ? t : 0) * a.H + 8 * g));
+  }
+  lf32x4 acc[4][8];
+#pragma unroll
+  for (int m = 0; m < 4; ++m)
+#pragma unroll
+    for (int j = 0; j < 8; ++j) acc[m][j] = lf32x4{0.f, 0.f, 0.f, 0.f};
+
+  // Piece p of thread tid: row (p * 64 WM + tid) / 16 of the step, columns 8 (tid % 16).
+  const uint32_t poff = (uint32_t)(2 * ((tid >> 4) * a.V + 8 * (tid & 15)));
+  auto fetch = [&](int step, eu32x4 (&r)[kPieces]) {
+#pragma unroll
+    for (int p = 0; p < kPieces; ++p)
+      r[p] = load_any<eu32x4>(reinterpret_cast<const char*>(
+                                  strip + (32 * (int64_t)step + p * (4 * WM)) * a.V) + poff);
+  };
+  auto put = [&](int buffer, const eu32x4 (&r)[kPieces]) {
+#pragma unroll
+    for (int p = 0; p < kPieces; ++p)
+      *reinterpret_cast<eu32x4*>(&sh[buffer][(p * (64 * WM) + tid) * 16]) = r[p];
+  };
+  auto hidden_step = [&](int step, eu32x4 (&h)[4]) {
+    const char* src = reinterpret_cast<const char*>(a.hidden + 32 * (int64_t)step);
+#pragma unroll
+    for (int m = 0; m < 4; ++m) h[m] = *reinterpret_cast<const eu32x4*>(src + hoff[m]);
+  };
+  auto multiply = [&](int buffer, const eu32x4 (&h)[4]) {
+    WeightStep w;
+    const char* src = &sh[buffer][(8 * g * 16 + c) * 16];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) w.w[i] = *reinterpret_cast<const eu32x4*>(src + i * 256);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      const lbf16x8 x = weight_column(w, j);
+#pragma unroll
+      for (int m = 0; m < 4; ++m)
+        acc[m][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
+            x, __builtin_bit_cast(lbf16x8, h[m]), acc[m][j], 0, 0, 0);
+    }
+  };
+  if (whole > 0) {
+    // Steps past the last whole one are fetched as that one, for nothing: without a
+    // branch around them the loads' waits stay exact.
+    const int end = whole - 1;
+    eu32x4 ahead[kAhead][kPieces], h[2][4];
+#pragma unroll
+    for (int s = 0; s < kAhead; ++s) fetch(s < end ? s : end, ahead[s]);
+    hidden_step(0, h[0]);
+    put(0, ahead[0]);
+    lds_barrier();
+    // S: the step's number modulo four, so that registers and buffers are known.
+    auto one = [&](int step, auto S) {
+      constexpr int s = decltype(S)::value;
+      fetch(step + kAhead < end ? step + kAhead : end, ahead[s % kAhead]);
+      hidden_step(step + 1 < end ? step + 1 : end, h[(s + 1) & 1]);
+      __builtin_amdgcn_sched_barrier(0);
+      multiply(s & 1, h[s & 1]);
+      __builtin_amdgcn_sched_barrier(0);
+      put((s + 1) & 1, ahead[(s + 1) % kAhead]);
+      lds_barrier();
+    };
+    int step = 0;
+    for (; step + 4 <= whole; step += 4) {
+      one(step, std::integral_constant<int, 0>{});
+      one(step + 1, std::integral_constant<int, 1>{});
+      one(step + 2, std::integral_constant<int, 2>{});
+      one(step + 3, std::integral_constant<int, 3>{});
+    }
+    if (step < whole) one(step, std::integral_constant<int, 0>{});
+    if (step + 1 < whole) one(step + 1, std::integral_constant<int, 1>{});
+    if (step + 2 < whole) one(step + 2, std::integral_constant<int, 2>{});
+  }
+  if (32 * (int64_t)whole < a.H) {
+    // What is left of the hidden dimension, in groups of eight.
+    const int64_t k = 32 * (int64_t)whole;
+    eu32x4 r[kPieces], h[4];
+#pragma unroll
+    for (int p = 0; p < kPieces; ++p) {
+      r[p] = eu32x4{0, 0, 0, 0};
+      if (k + p * (4 * WM) + (tid >> 4) < a.H)
+        r[p] = load_any<eu32x4>(
+            reinterpret_cast<const char*>(strip + (k + p * (4 * WM)) * a.V) + poff);
+    }
+#pragma unroll
+    for (int m = 0; m < 4; ++m) {
+      h[m] = eu32x4{0, 0, 0, 0};
+      if (k + 8 * g < a.H)
+        h[m] = *reinterpret_cast<const eu32x4*>(reinterpret_cast<const char*>(a.hidden + k) +
+                                                hoff[m]);
+    }
+    put(0, r);
+    lds_barrier();
+    multiply(0, h);
+  }
+  if (idle) return;
+#pragma unroll
+  for (int m = 0; m < 4; ++m) {
+    const int64_t t = t0 + 16 * m + c;
+    if (t >= a.N) continue;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int64_t col = base + 8 * (4 * g + i);
+      if (col + 8 <= v0) continue;
+      float z[8];
+#pragma unroll
+      for (int j = 0; j < 8; ++j) z[j] = acc[m][j][i];
+      logits_finish(a, col, 8, z);
+      const int skip = v0 > col ? (int)(v0 - col) : 0;
+      if (skip == 0) {
+        store8<OUT32>(a.out, t * a.ld_out + col, 8, z);
+      } else {
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+          if (j >= skip) store1<OUT32>(a.out, t * a.ld_out + col + j, z[j]);
+      }
+    }
+  }
 }
 
 // The hidden rows as the tile's B operand: strips of 256 tokens (zeros past the last

@@ -18,6 +18,7 @@
 #include <stdint.h>
 
 #include "flce_gemm.hpp"
+#include "flce_logits.hpp"
 #include "flce_step_plan.hpp"
 #include "flce_vector.hpp"
 
@@ -258,12 +259,6 @@ struct MaxOp {
 struct SumOp {
   __device__ __forceinline__ float operator()(float a, float b) const { return a + b; }
 };
-
-// LDS traffic of the block is complete; loads from memory may still be on their way.
-__device__ __forceinline__ void lds_barrier() {
-  wait_lgkmcnt0();
-  block_barrier();
-}
 
 // Eight values as they lie in memory.
 template <bool F32>

@@ -127,6 +127,18 @@ flce_status_t flce_logits(const void* hidden, const void* weight, const float* b
   a.ld_out = ld_out;
   const bool f32 = out_dtype == FLCE_GRAD_F32;
   hipStream_t st = static_cast<hipStream_t>(stream);
+  if (p.wide > 0) {
+    a.passes = p.passes;
+    const unsigned grid = (unsigned)(ceil_div(p.strips, 8) * 8 * p.passes);
+    return launch(K_LOGITS, st, [&] {
+      switch (p.wide * 2 + (f32 ? 1 : 0)) {
+        case 4: logits_wide_kernel<2, false><<<grid, 128, 0, st>>>(a); break;
+        case 5: logits_wide_kernel<2, true><<<grid, 128, 0, st>>>(a); break;
+        case 8: logits_wide_kernel<4, false><<<grid, 256, 0, st>>>(a); break;
+        default: logits_wide_kernel<4, true><<<grid, 256, 0, st>>>(a); break;
+      }
+    });
+  }
   if (p.mt == 0) {
     a.image = reinterpret_cast<uint16_t*>(wsp(workspace, p.image));
     a.hkb = p.hkb;

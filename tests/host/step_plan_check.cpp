@@ -24,6 +24,12 @@ static void check_logits_plan(int64_t N, int64_t H, int64_t V) {
   const LogitsPlan p = make_logits_plan(N, H, V);
   CHECK(p.total >= kHeaderBytes && p.total % kAlign == 0);
   if (N == 0) return;
+  if (p.wide > 0) {
+    CHECK((p.wide == 2 || p.wide == 4) && V >= kLogitStrip && p.strips * kLogitStrip >= V);
+    CHECK((int64_t)p.passes * p.wide * 64 >= N);
+    CHECK((p.strips + 7) / 8 * 8 * p.passes * p.wide * 64 < ((int64_t)1 << 32));
+    return;
+  }
   if (p.mt == 0) {
     CHECK(V % 8 == 0);
     CHECK((int64_t)p.hkb * kBK >= H && (int64_t)p.vt * kTile >= V && (int64_t)p.tb * kTile >= N);
