@@ -431,20 +431,29 @@ __global__ void __launch_bounds__(64 * WM, 2) logits_wide_kernel(LogitsArgs a) {
 }
 
 // The hidden rows as the tile's B operand: strips of 256 tokens (zeros past the last
-// one), K blocks of 32. A block fills 8 consecutive K blocks of one strip.
+// one), K blocks of 32. A block fills two consecutive K blocks of one strip with all of
+// its loads at once.
+constexpr int kPackBlocks = 2;
 __global__ void __launch_bounds__(256) logits_pack_kernel(LogitsArgs a) {
+  constexpr int kPieces = kPackBlocks * 4;  // 16 bytes of a row
   const int strip = blockIdx.y;
-#pragma unroll 4
-  for (int p = 0; p < 32; ++p) {
-    const int i = p * 256 + threadIdx.x;
-    const int r = i >> 5, kb = blockIdx.x * 8 + ((i >> 2) & 7), c = i & 3;
+  eu32x4 v[kPieces];
+#pragma unroll
+  for (int p = 0; p < kPieces; ++p) {
+    const int i = p * 256 + threadIdx.x, r = i / kPieces, c = i % kPieces;
+    const int64_t row = (int64_t)strip * kTile + r;
+    const int64_t k = (int64_t)blockIdx.x * kPackBlocks * kBK + c * 8;
+    v[p] = eu32x4{0, 0, 0, 0};
+    if (row < a.N && k < a.H) v[p] = *reinterpret_cast<const eu32x4*>(a.hidden + row * a.H + k);
+  }
+#pragma unroll
+  for (int p = 0; p < kPieces; ++p) {
+    const int i = p * 256 + threadIdx.x, r = i / kPieces, c = i % kPieces;
+    const int kb = blockIdx.x * kPackBlocks + (c >> 2);
     if (kb >= a.hkb) continue;
-    const int64_t row = (int64_t)strip * kTile + r, k = (int64_t)kb * kBK + c * 8;
-    eu32x4 v{0, 0, 0, 0};
-    if (row < a.N && k < a.H) v = *reinterpret_cast<const eu32x4*>(a.hidden + row * a.H + k);
     char* block = reinterpret_cast<char*>(a.image) +
                   ((int64_t)strip * a.hkb + kb) * (int64_t)kBlockBytes;
-    *reinterpret_cast<eu32x4*>(block + blk_byte(r, c * 8)) = v;
+    *reinterpret_cast<eu32x4*>(block + blk_byte(r, (c & 3) * 8)) = v[p];
   }
 }
 

@@ -144,7 +144,7 @@ flce_status_t flce_logits(const void* hidden, const void* weight, const float* b
     a.hkb = p.hkb;
     a.VT = p.vt;
     a.TB = p.tb;
-    const dim3 pack((unsigned)ceil_div(p.hkb, 8), (unsigned)p.tb);
+    const dim3 pack((unsigned)ceil_div(p.hkb, kPackBlocks), (unsigned)p.tb);
     FLCE_TRY(launch(K_LOGITS, st, [&] { logits_pack_kernel<<<pack, 256, 0, st>>>(a); }));
     return launch(K_LOGITS, st, [&] {
       const unsigned grid = (unsigned)(p.vt * p.tb);
