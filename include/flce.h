@@ -586,7 +586,7 @@ flce_status_t flce_logits_workspace_size(int64_t N, int64_t H, int64_t V, size_t
 /* hidden device bf16 [N,H], weight device bf16 [H,V], both 16-byte aligned (H a
  * multiple of 8, V any size); bias device fp32 [V] or NULL; out device [N,V] of
  * out_dtype (FLCE_GRAD_BF16 or FLCE_GRAD_F32), row i from element i * ld_out on
- * (ld_out >= V), aligned to its elements. */
+ * (ld_out >= V), aligned to its elements. The call has no status to read. */
 flce_status_t flce_logits(const void* hidden, const void* weight, const float* bias, int64_t N,
                           int64_t H, int64_t V, float softcap, int out_dtype, void* out,
                           int64_t ld_out, void* workspace, size_t workspace_bytes, void* stream);
@@ -713,10 +713,10 @@ enum { FLCE_ROUND_NEAREST = 0, FLCE_ROUND_STOCHASTIC = 1 };
 
 /* The tensors of an update: host arrays of `count` entries. Tensor i has sizes[i]
  * values, its pointers are device pointers aligned to their elements, to memory of its
- * own; sizes of 0 are passed over. With FLCE_STATE_8BIT the states are e4m3 codes (OCP: the largest is 448)
- * in blocks of 256 values from the tensor's start on, and exp_avg_scales and
- * exp_avg_sq_scales (fp32, one a block) what a code is multiplied by; exp_avg_sqs then
- * holds the root of the second moment. */
+ * own; sizes of 0 are passed over. With FLCE_STATE_8BIT the states are e4m3 codes (OCP:
+ * the largest is 448) in blocks of 256 values from the tensor's start on, and
+ * exp_avg_scales and exp_avg_sq_scales (fp32, one a block) what a code is multiplied by;
+ * exp_avg_sqs then holds the root of the second moment. */
 typedef struct flce_adamw_list {
   int64_t count;
   const int64_t* sizes;
@@ -753,9 +753,9 @@ size_t flce_adamw_workspace_size(void);
  *   p = (1 - lr weight_decay) p - lr / (1 - beta1^t) m / (sqrt(v) / sqrt(1 - beta2^t) + eps).
  * If s is not finite (an overflow in the backward), nothing is changed, step among
  * it (without a grad_scale, a gradient that is not finite makes its weight and states
- * NaN, in 8 bits its block's states). In 8-bit states a block's scale is its largest magnitude a times 1 / 448 and
- * its codes are those of the values times 448 (1 / a) (all 0 if a is below 2^-100), in
- * fp32; a second moment above 0 has a code above 0.
+ * NaN, in 8 bits its block's states). In 8-bit states a block's scale is its largest
+ * magnitude a times 1 / 448 and its codes are those of the values times 448 (1 / a) (all
+ * 0 if a is below 2^-100), in fp32; a second moment above 0 has a code above 0.
  * Stochastic rounding goes up with the probability of the part cut off, by 16 bits
  * of a hash of the seed, t, the tensor's index and the value's. */
 flce_status_t flce_adamw_step(const flce_adamw_list_t* list, const flce_adamw_options_t* opt,
@@ -764,8 +764,8 @@ flce_status_t flce_adamw_step(const flce_adamw_list_t* list, const flce_adamw_op
 
 /* Reads the status word that the last call with this workspace left, after
  * synchronising `stream`. *invalid_labels (may be NULL) receives the number of
- * labels (embedding, processing of logits: tokens) that were neither ignore_index nor in [0, V), or of
- * bad sequence offsets (losses); returns FLCE_ERR_INVALID_LABEL if that number is
+ * labels (embedding, processing of logits: tokens) that were neither ignore_index nor in
+ * [0, V), or of bad sequence offsets (losses, processing of logits); returns FLCE_ERR_INVALID_LABEL if that number is
  * not 0, else FLCE_OK. */
 flce_status_t flce_get_status(const void* workspace, int64_t* invalid_labels, void* stream);
 

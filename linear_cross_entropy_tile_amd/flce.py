@@ -1617,8 +1617,8 @@ def adamw_step(params, grads, state, lr=1e-3, beta1: float = 0.9, beta2: float =
     """One AdamW step over a list of tensors, in place (flce_adamw_step).
 
     params and grads: dense bf16 or fp32 tensors of the same sizes, the types in
-    any mixture, no parameter twice; state: of ``adamw_state``, updated in place, its step raised by
-    one. lr: a number, or fp32 [1] on the device (a captured step then follows
+    any mixture; state: of ``adamw_state``, updated in place, its step raised by
+    one; no two tensors of params and state share memory. lr: a number, or fp32 [1] on the device (a captured step then follows
     it). grad_scale: fp32 [1] that the gradients are multiplied by, e.g.
     ``grad_norm``'s scale; if it is not finite, nothing is changed. Under
     rounding "stochastic" bf16 parameters without a master copy and 8-bit states
@@ -1654,10 +1654,14 @@ def adamw_step(params, grads, state, lr=1e-3, beta1: float = 0.9, beta2: float =
                                  for t, p in zip(master, params)):
             raise ValueError("state master: fp32 parameters have no copy")
         lists[3] = array.array("Q", [0 if t is None else t.data_ptr() for t in master])
-    for a, name in ((lists[1], "params"), (lists[4], "state exp_avg"), (lists[5], "state exp_avg_sq")):
-        # Two of a list at one address would be updated at once. (No values, no address.)
-        if len(set(a)) < len(a) - max(0, sizes.count(0) - 1):
-            raise ValueError(f"{name}: the same tensor twice")
+    # Two of the written tensors at one address would be updated at once. (No values, no
+    # address.)
+    written = array.array("Q")
+    for a in (lists[1], *lists[3:8]):
+        if a is not None:
+            written += a
+    if len(set(written)) < len(written) - max(0, written.count(0) - 1):
+        raise ValueError("params and state: the same tensor twice")
     step = state["step"]
     _check_vector(step, torch.int64, 1, dev.index, "state step")
     lr_device = None
