@@ -10,7 +10,12 @@
 // in 8 bits take 16 values a lane, so that the 256 values that share a scale lie in a
 // row of 16 lanes and their largest magnitude takes four exchanges within it.
 //
-// What bounds them: the bytes; with 8-bit states also the instructions.
+// What bounds them: the bytes; with 8-bit states also the instructions. A bf16 weight of
+// 590 M values with fp32 states takes 2.44 ms (22 bytes a value, 5.3 TB/s), with 8-bit
+// ones 1.2 ms (10 bytes, 4.9 TB/s), 356 M values in 97 tensors with fp32 copies 1.88 ms
+// (28 bytes, 5.3 TB/s).
+// The norm of 590 M bf16 values takes 250 us (4.7 TB/s), bound by the float64 products:
+// more or smaller chunks, or two loads in flight instead of four, are slower.
 #pragma once
 
 #include <hip/hip_runtime.h>
@@ -243,7 +248,8 @@ __device__ __forceinline__ float root_near(float v) {
 // Roots rounded to the nearest: the last bit of a root that is kept in 8 bits can decide
 // a code, and with it a block's scale. One Newton step from the reciprocal root on x and
 // on 1 / (2 x), then the remainder, in 11 instruction slots a value against sqrtf's 20
-// (equal to it for every mantissa); values that it does not hold for (0, below 2^-96, infinities) take sqrtf.
+// (equal to it for every mantissa); values that it does not hold for (0, below 2^-96,
+// infinities) take sqrtf.
 __device__ __forceinline__ void roots16(const float (&v)[16], float (&r)[16]) {
   bool odd = false;
 #pragma unroll

@@ -9,9 +9,11 @@ Two layers, both argument marshalling only:
   status raises ``FlceError``.
 * ``forward`` / ``backward`` / ``forward_backward`` (the fused call, for
   upstream gradients known before the forward), the embedding
-  (``embedding``, ``embedding_backward``) and the losses between the head's
+  (``embedding``, ``embedding_backward``), the losses between the head's
   forward and its backward (``policy_loss``, ``preference_loss``, each with
-  ``_backward`` and ``_forward_backward``): take torch CUDA tensors, check
+  ``_backward`` and ``_forward_backward``), what sampling needs (``logits``,
+  ``process_logits``, ``process_logits_backward``) and the update
+  (``grad_norm``, ``adamw_state``, ``adamw_step``): take torch CUDA tensors, check
   dtypes and layouts, allocate outputs and the workspace with torch (so
   torch's caching allocator owns all memory), and call the C entry points on
   torch's current stream. No arithmetic of the operators happens here.
