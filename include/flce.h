@@ -640,9 +640,9 @@ typedef struct flce_process_options {
   const float* bias_values;
   int64_t bias_count;
   const int64_t* bias_offsets;    /* [N+1], within [0, bias_count] and not decreasing */
-  const int32_t* allowed;         /* device bits: id v of a row is allowed if bit v % 32 of word v / 32
-                                   * is set; one row for all (allowed_stride 0) or rows of
-                                   * allowed_stride words; NULL: all allowed */
+  const int32_t* allowed;         /* device bits: id v of a row is allowed if bit v % 32 of
+                                   * word v / 32 is set; one row for all (allowed_stride 0) or
+                                   * rows of allowed_stride words; NULL: all allowed */
   int64_t allowed_stride;
   int logits_dtype, out_dtype;    /* FLCE_GRAD_BF16 or FLCE_GRAD_F32 */
 } flce_process_options_t;
@@ -765,8 +765,8 @@ flce_status_t flce_adamw_step(const flce_adamw_list_t* list, const flce_adamw_op
 /* Reads the status word that the last call with this workspace left, after
  * synchronising `stream`. *invalid_labels (may be NULL) receives the number of
  * labels (embedding, processing of logits: tokens) that were neither ignore_index nor in
- * [0, V), or of bad sequence offsets (losses, processing of logits); returns FLCE_ERR_INVALID_LABEL if that number is
- * not 0, else FLCE_OK. */
+ * [0, V), or of bad sequence offsets (losses, processing of logits); returns
+ * FLCE_ERR_INVALID_LABEL if that number is not 0, else FLCE_OK. */
 flce_status_t flce_get_status(const void* workspace, int64_t* invalid_labels, void* stream);
 
 /* Static English text for a status code. */

@@ -117,7 +117,8 @@ __device__ __forceinline__ lbf16x8 weight_column(const WeightStep& s, int j) {
 // for other tokens are eight apart in number, so that they run on one XCD at about the
 // same time and all but the first find the strip in its L2.
 template <int MT, int W, bool OUT32>
-__global__ void __launch_bounds__(64 * W, MT >= 2 ? (MT >= 4 ? 2 : 3) : 4) logits_kernel(LogitsArgs a) {
+__global__ void __launch_bounds__(64 * W, MT >= 2 ? (MT >= 4 ? 2 : 3) : 4)
+logits_kernel(LogitsArgs a) {
   __shared__ float sh[W][8][4][64];
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6));
@@ -145,7 +146,8 @@ __global__ void __launch_bounds__(64 * W, MT >= 2 ? (MT >= 4 ? 2 : 3) : 4) logit
   auto hidden_step = [&](int64_t k, eu32x4 (&h)[MT]) {
 #pragma unroll
     for (int m = 0; m < MT; ++m)
-      h[m] = *reinterpret_cast<const eu32x4*>(reinterpret_cast<const char*>(a.hidden + k) + hoff[m]);
+      h[m] = *reinterpret_cast<const eu32x4*>(reinterpret_cast<const char*>(a.hidden + k) +
+                                              hoff[m]);
   };
   auto multiply = [&](WeightStep& s, const eu32x4 (&h)[MT]) {
     // Here and no earlier: the compiler would pair the words of a step in flight

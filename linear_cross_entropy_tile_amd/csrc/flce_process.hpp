@@ -5,17 +5,18 @@
 // A row's ids are cut into slices, a block each, of which a thread holds eight
 // consecutive ids a step in registers. The logits are asked for first; while they
 // come, the block counts the history's tokens that fall into its slice in LDS
-// (integer atomics: the order does not matter) and adds up the slice's listed biases
-// there in the list's order. The values are formed and stored, and from the block's
-// maximum m come s = sum exp(x - m) and u = sum exp(x - m) (x - m). The slices' states
-// are merged by a wave a row in a second launch. lse = m + ln s, entropy = ln s - u / s.
+// (integer atomics: the order does not matter) and then, once the penalties have been
+// applied, adds up the slice's listed biases there in the list's order. The values are
+// formed and stored, and from the block's maximum m come s = sum exp(x - m) and
+// u = sum exp(x - m) (x - m). The slices' states are merged by a wave a row in a second
+// launch. lse = m + ln s, entropy = ln s - u / s.
 //
 // 512 rows of 152064 bf16 logits take 57 us without a history (5.4 TB/s, bound by the
 // bytes) and 89 to 96 with up to 2048 tokens a row and a mask: then a block's chain of
 // offsets, tokens, counts and statistics shows, at eight blocks a CU. Sorting the
 // histories by slice in a launch before saves 5 us and costs 9. 64 rows of 128256 fp32
-// logits, up to 4096 tokens and 100 listed biases a row, take 24 us and 5 to 8 of the merge. The gradient of
-// 300 rows of 50257 fp32 takes 35 us (5.3 TB/s).
+// logits, up to 4096 tokens and 100 listed biases a row, take 24 us and 5 to 8 of the
+// merge. The gradient of 300 rows of 50257 fp32 takes 35 us (5.3 TB/s).
 //
 // Contraction of a product and a sum into one rounding is off: the value of a
 // logit is the header's sequence of fp32 operations, whatever the compiler picks.

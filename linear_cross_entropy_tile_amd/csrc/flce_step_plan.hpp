@@ -237,8 +237,9 @@ inline flce_status_t check_adamw(const flce_adamw_list_t* list, const flce_adamw
                       l.param_dtypes == nullptr || l.grad_dtypes == nullptr ||
                       (eight && (l.exp_avg_scales == nullptr || l.exp_avg_sq_scales == nullptr))))
     return FLCE_ERR_NULL_POINTER;
-  if (!std::isfinite(o->lr) || !std::isfinite((float)o->lr) || !(o->beta1 >= 0.0 && o->beta1 < 1.0) ||
-      !(o->beta2 >= 0.0 && o->beta2 < 1.0) || !(o->eps >= 0.0 && std::isfinite((float)o->eps)) ||
+  if (!std::isfinite(o->lr) || !std::isfinite((float)o->lr) ||
+      !(o->beta1 >= 0.0 && o->beta1 < 1.0) || !(o->beta2 >= 0.0 && o->beta2 < 1.0) ||
+      !(o->eps >= 0.0 && std::isfinite((float)o->eps)) ||
       !std::isfinite(o->weight_decay) || !std::isfinite((float)(o->lr * o->weight_decay)))
     return FLCE_ERR_BAD_OPTION;
   if (!eight && o->state_dtype != FLCE_STATE_F32) return FLCE_ERR_BAD_OPTION;

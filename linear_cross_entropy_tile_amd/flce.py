@@ -48,8 +48,8 @@ __all__ = [
     "policy_loss_backward", "policy_loss_forward_backward", "preference_loss",
     "preference_loss_backward", "preference_loss_forward_backward",
     "FLCE_STATE_F32", "FLCE_STATE_8BIT", "FLCE_ROUND_NEAREST", "FLCE_ROUND_STOCHASTIC",
-    "FlceProcessOptions", "FlceProcessGrads", "FlceAdamwList", "FlceAdamwOptions", "flce_logits_workspace_size",
-    "flce_logits", "flce_process_workspace_size", "flce_process_logits",
+    "FlceProcessOptions", "FlceProcessGrads", "FlceAdamwList", "FlceAdamwOptions",
+    "flce_logits_workspace_size", "flce_logits", "flce_process_workspace_size", "flce_process_logits",
     "flce_process_logits_backward", "flce_grad_norm_workspace_size", "flce_grad_norm",
     "flce_adamw_workspace_size", "flce_adamw_step", "logits", "process_logits",
     "process_logits_backward", "grad_norm", "adamw_state", "adamw_step",
@@ -1620,8 +1620,8 @@ def adamw_step(params, grads, state, lr=1e-3, beta1: float = 0.9, beta2: float =
 
     params and grads: dense bf16 or fp32 tensors of the same sizes, the types in
     any mixture; state: of ``adamw_state``, updated in place, its step raised by
-    one; no two tensors of params and state share memory. lr: a number, or fp32 [1] on the device (a captured step then follows
-    it). grad_scale: fp32 [1] that the gradients are multiplied by, e.g.
+    one; no two tensors of params and state share memory. lr: a number, or fp32
+    [1] on the device (a captured step then follows it). grad_scale: fp32 [1] that the gradients are multiplied by, e.g.
     ``grad_norm``'s scale; if it is not finite, nothing is changed. Under
     rounding "stochastic" bf16 parameters without a master copy and 8-bit states
     are rounded up with the probability of the part cut off, by a hash of seed,
