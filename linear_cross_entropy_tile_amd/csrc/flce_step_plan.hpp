@@ -147,6 +147,29 @@ inline int proc_history(const flce_process_options_t& o, bool gradient) {
   return o.repetition != nullptr || o.repetition_penalty != 1.0 ? HIST_SEEN : HIST_NONE;
 }
 
+// Rows of longer histories are counted in 32 bits.
+constexpr int64_t kLongHistory = 0x7FFF;
+// Words by which ids of one listed bias wait for each other.
+constexpr int kProcTags = 256;
+// LDS words of a slice: counts, then in their place sums of the listed biases; tags.
+constexpr int proc_count_words(int hist, int slice) {
+  return hist == HIST_COUNT ? slice / 2 : (hist == HIST_SEEN ? slice / 32 : 0);
+}
+constexpr int proc_lds_words(int hist, bool list, int slice) {
+  return list ? slice + kProcTags : proc_count_words(hist, slice);
+}
+
+// A token's distance from id lo: its place among the n ids from there on if it is below
+// n. Any int64 may be a token; those before lo are far past every n.
+constexpr uint64_t proc_place(int64_t token, int64_t lo) {
+  return (uint64_t)token - (uint64_t)lo;
+}
+// A slice of n ids whose counts take 32 bits is counted in parts of `part` ids: the ids
+// of the one from `from` on, none where the slice ends before it.
+constexpr uint32_t proc_part(int n, int from, int part) {
+  return (uint32_t)(n <= from ? 0 : (n - from < part ? n - from : part));
+}
+
 inline flce_status_t check_process(int64_t N, int64_t V, const flce_process_options_t* o) {
   if (N < 0 || N > kMaxN || V < 1 || V > kMaxV) return FLCE_ERR_BAD_SHAPE;
   if (o == nullptr) return FLCE_ERR_NULL_POINTER;
