@@ -752,8 +752,10 @@ size_t flce_adamw_workspace_size(void);
  *   g = s grad,  m = beta1 m + (1 - beta1) g,  v = beta2 v + (1 - beta2) g^2,
  *   p = (1 - lr weight_decay) p - lr / (1 - beta1^t) m / (sqrt(v) / sqrt(1 - beta2^t) + eps).
  * If s is not finite (an overflow in the backward), nothing is changed, step among
- * it (without a grad_scale, a gradient that is not finite makes its weight and states
- * NaN, in 8 bits its block's states). In 8-bit states a block's scale is its largest
+ * it. Without a grad_scale, a gradient that is not finite makes its weight NaN and its
+ * states NaN or infinite; in 8 bits all states of its block are NaN then: a NaN or an
+ * infinity (the square of a gradient above 2^64 is one) makes the block's scale infinite
+ * and every code 0 or NaN. In 8-bit states a block's scale is otherwise its largest
  * magnitude a times 1 / 448 and its codes are those of the values times 448 (1 / a) (all
  * 0 if a is below 2^-100), in fp32; a second moment above 0 has a code above 0.
  * Stochastic rounding goes up with the probability of the part cut off, by 16 bits

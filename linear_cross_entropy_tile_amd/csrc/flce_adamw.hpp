@@ -249,9 +249,10 @@ __device__ __forceinline__ float root_near(float v) {
 // a code, and with it a block's scale. One Newton step from the reciprocal root on x and
 // on 1 / (2 x), then the remainder, in 11 instruction slots a value against sqrtf's 20
 // (equal to it for every mantissa); values that it does not hold for (0, below 2^-96,
-// infinities) take sqrtf.
-__device__ __forceinline__ void roots16(const float (&v)[16], float (&r)[16]) {
+// infinities, NaN) take sqrtf. Returns infinity if there is a NaN, else 0.
+__device__ __forceinline__ float roots16(const float (&v)[16], float (&r)[16]) {
   bool odd = false;
+  float sum = 0.f;
 #pragma unroll
   for (int k = 0; k < 16; ++k) {
     const float y = __builtin_amdgcn_rsqf(v[k]);
@@ -265,7 +266,10 @@ __device__ __forceinline__ void roots16(const float (&v)[16], float (&r)[16]) {
   if (odd) {
 #pragma unroll
     for (int k = 0; k < 16; ++k) r[k] = sqrtf(v[k]);
+#pragma unroll
+    for (int k = 0; k < 16; ++k) sum += r[k];
   }
+  return sum != sum ? INFINITY : 0.f;
 }
 
 // W values of an update with fp32 states, from element i on (n of them).
@@ -362,12 +366,13 @@ constexpr float kTinyBlock = 0x1p-100f;
 // Codes of 16 values whose block of 256 lies in the row of 16 lanes; returns the
 // block's scale. POSITIVE: values >= 0, of which those above 0 get a code above 0. SR:
 // stochastic rounding by the upper 16 of `bits` (the others 0), which the conversion adds
-// to the part that it cuts off.
+// to the part that it cuts off. top: 0, or infinity if the lane has a NaN, which the
+// maximum passes over: the block then reads as NaN, as it does with an infinity among its
+// values, whose scale is infinite and every code 0 or NaN.
 template <bool SR, bool POSITIVE>
-__device__ __forceinline__ float encode16(const float (&x)[16], const uint32_t (&bits)[16],
-                                          uint32_t (&w)[4]) {
+__device__ __forceinline__ float encode16(const float (&x)[16], float top,
+                                          const uint32_t (&bits)[16], uint32_t (&w)[4]) {
 #pragma clang fp contract(off)
-  float top = 0.f;
 #pragma unroll
   for (int k = 0; k < 16; ++k) top = fmaxf(top, fabsf(x[k]));
   top = row16_max(top);
@@ -434,8 +439,9 @@ __device__ __forceinline__ void adam_8bit(const AdamEntry& e, const AdamCoef& c,
     v[k] = q * q;
     adam_moments(c, g[k], m[k], v[k]);
   }
+  // A NaN of the gradient or of the states is one of the second moment too.
   float r[16];
-  roots16(v, r);
+  const float lost = roots16(v, r);
 #pragma unroll
   for (int k = 0; k < 16; ++k) {
     p[k] = adam_weight(c, p[k], m[k], r[k]);
@@ -447,8 +453,8 @@ __device__ __forceinline__ void adam_8bit(const AdamEntry& e, const AdamCoef& c,
     }
   }
   // Lanes and values past the end: a gradient, weight and moments of 0 give 0.
-  const float ms1 = encode16<SR, false>(m, mb, mw);
-  const float vs1 = encode16<SR, true>(r, vb, vw);
+  const float ms1 = encode16<SR, false>(m, lost, mb, mw);
+  const float vs1 = encode16<SR, true>(r, lost, vb, vw);
   if (n <= 0) return;
   store_codes(e.m, i, n, mw);
   store_codes(e.v, i, n, vw);
