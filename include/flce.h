@@ -623,15 +623,16 @@ typedef struct flce_process_options {
   int64_t tokens_size, tokens_stride;
   const int64_t* offsets;
   const int64_t* prompt_lengths;  /* [N], cut to the history; NULL: 0 */
-  /* Device fp32 [N], or NULL for the value of all rows below. */
+  /* Device fp32 [N] in the ranges of the values of all rows below (not checked), or NULL
+   * for those. */
   const float* repetition;
   const float* presence;
   const float* frequency;
   const float* temperatures;
-  double repetition_penalty;      /* > 0, 1: off */
+  double repetition_penalty;      /* > 0, 1: off; finite in fp32, as its reciprocal there */
   double presence_penalty;        /* 0: off */
   double frequency_penalty;       /* 0: off */
-  double temperature;             /* >= 0, 1: off */
+  double temperature;             /* 0, or like repetition_penalty; 1: off */
   const float* bias;              /* device fp32 [V] (bias_stride 0) or [N, bias_stride], or NULL */
   int64_t bias_stride;
   /* Listed biases: row i's are the pairs [bias_offsets[i], bias_offsets[i+1]) of the

@@ -170,13 +170,18 @@ constexpr uint32_t proc_part(int n, int from, int part) {
   return (uint32_t)(n <= from ? 0 : (n - from < part ? n - from : part));
 }
 
+// Above 0, and in fp32 still so and finite, as its reciprocal there is.
+inline bool fp32_divisor(double x) {
+  const float f = (float)x;
+  return f > 0.f && std::isfinite(f) && std::isfinite(1.f / f);
+}
 inline flce_status_t check_process(int64_t N, int64_t V, const flce_process_options_t* o) {
   if (N < 0 || N > kMaxN || V < 1 || V > kMaxV) return FLCE_ERR_BAD_SHAPE;
   if (o == nullptr) return FLCE_ERR_NULL_POINTER;
   if (!known_dtype(o->logits_dtype) || !known_dtype(o->out_dtype)) return FLCE_ERR_BAD_OPTION;
-  if (!(o->repetition_penalty > 0.0 && std::isfinite(o->repetition_penalty)) ||
-      !std::isfinite(o->presence_penalty) || !std::isfinite(o->frequency_penalty) ||
-      !(o->temperature >= 0.0 && std::isfinite(o->temperature)))
+  if (!fp32_divisor(o->repetition_penalty) || !std::isfinite(o->presence_penalty) ||
+      !std::isfinite(o->frequency_penalty) ||
+      !(o->temperature == 0.0 || fp32_divisor(o->temperature)))
     return FLCE_ERR_BAD_OPTION;
   const int64_t most = (int64_t)1 << 40;
   if (o->tokens_size < 0 || o->tokens_size > most || o->tokens_stride < 0 ||
