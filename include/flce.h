@@ -586,7 +586,8 @@ flce_status_t flce_logits_workspace_size(int64_t N, int64_t H, int64_t V, size_t
 /* hidden device bf16 [N,H], weight device bf16 [H,V], both 16-byte aligned (H a
  * multiple of 8, V any size); bias device fp32 [V] or NULL; out device [N,V] of
  * out_dtype (FLCE_GRAD_BF16 or FLCE_GRAD_F32), row i from element i * ld_out on
- * (ld_out >= V), aligned to its elements. The call has no status to read. */
+ * (ld_out >= V), aligned to its elements. softcap finite, as its reciprocal in fp32 if it
+ * is above 0. The call has no status to read. */
 flce_status_t flce_logits(const void* hidden, const void* weight, const float* bias, int64_t N,
                           int64_t H, int64_t V, float softcap, int out_dtype, void* out,
                           int64_t ld_out, void* workspace, size_t workspace_bytes, void* stream);

@@ -92,7 +92,8 @@ inline flce_status_t check_logits(int64_t N, int64_t H, int64_t V, float softcap
   const flce_status_t s = check_shape(N, H, V);
   if (s != FLCE_OK) return s;
   if (ld_out < V || ld_out > ((int64_t)1 << 40)) return FLCE_ERR_BAD_SHAPE;
-  if (!std::isfinite(softcap)) return FLCE_ERR_BAD_SOFTCAP;
+  if (!std::isfinite(softcap) || (softcap > 0.f && !std::isfinite(1.f / softcap)))
+    return FLCE_ERR_BAD_SOFTCAP;
   if (!known_dtype(out_dtype)) return FLCE_ERR_BAD_OPTION;
   return FLCE_OK;
 }

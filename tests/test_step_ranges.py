@@ -38,3 +38,11 @@ def test_divisors_of_logits(which, name, value, code):
 def test_a_temperature_of_zero_is_no_divisor(which):
     assert _process(which, temperature=0.0) == ACCEPTED
     assert _process(which, repetition_penalty=0.0) == BAD_OPTION
+
+
+@pytest.mark.parametrize("softcap,code", [
+    # Of 1e-40 the reciprocal is infinite in fp32, and a logit of 0 would be NaN.
+    (1e-40, 6), (2.0 ** -128, 6), (1e-44, 6), (2.0 ** -127, ACCEPTED), (1e-20, ACCEPTED),
+    (50.0, ACCEPTED), (3e38, ACCEPTED), (0.0, ACCEPTED), (-1e-40, ACCEPTED)])
+def test_tanh_cap_of_logits(softcap, code):
+    assert flce.lib().flce_logits(A, A, None, 4, 8, 10, softcap, 1, A, 10, A, 0, None) == code
