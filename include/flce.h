@@ -738,7 +738,8 @@ typedef struct flce_adamw_list {
 typedef struct flce_adamw_options {
   double lr;               /* finite */
   double beta1, beta2;     /* in [0, 1) */
-  double eps;              /* >= 0 */
+  double eps;              /* 0 or at least 2^-126 (with 0, a value whose gradients were all 0
+                            * becomes 0 / 0) */
   double weight_decay;     /* finite */
   int state_dtype;         /* FLCE_STATE_* */
   int rounding;            /* FLCE_ROUND_*: of bf16 weights without a master copy, and of codes */

@@ -269,6 +269,8 @@ inline flce_status_t check_adamw(const flce_adamw_list_t* list, const flce_adamw
   if (!std::isfinite(o->lr) || !std::isfinite((float)o->lr) ||
       !(o->beta1 >= 0.0 && o->beta1 < 1.0) || !(o->beta2 >= 0.0 && o->beta2 < 1.0) ||
       !(o->eps >= 0.0 && std::isfinite((float)o->eps)) ||
+      // The quotient's hardware reciprocal takes a denormal for 0.
+      (o->eps > 0.0 && (float)o->eps < 0x1p-126f) ||
       !std::isfinite(o->weight_decay) || !std::isfinite((float)(o->lr * o->weight_decay)))
     return FLCE_ERR_BAD_OPTION;
   if (!eight && o->state_dtype != FLCE_STATE_F32) return FLCE_ERR_BAD_OPTION;

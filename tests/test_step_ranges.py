@@ -46,3 +46,15 @@ def test_a_temperature_of_zero_is_no_divisor(which):
     (50.0, ACCEPTED), (3e38, ACCEPTED), (0.0, ACCEPTED), (-1e-40, ACCEPTED)])
 def test_tanh_cap_of_logits(softcap, code):
     assert flce.lib().flce_logits(A, A, None, 4, 8, 10, softcap, 1, A, 10, A, 0, None) == code
+
+
+@pytest.mark.parametrize("eps,code", [
+    # In fp32 these are 0 or denormals: a gradient of 0 would make its weight 0 / 0.
+    (1e-320, BAD_OPTION), (1e-50, BAD_OPTION), (1e-40, BAD_OPTION), (2.0 ** -127, BAD_OPTION),
+    (2.0 ** -126, ACCEPTED), (1e-30, ACCEPTED), (1e-8, ACCEPTED), (0.0, ACCEPTED)])
+def test_eps_of_adamw(eps, code):
+    o = flce.FlceAdamwOptions(1e-3, 0.9, 0.999, eps, 0.01, flce.FLCE_STATE_F32,
+                              flce.FLCE_ROUND_NEAREST, 0)
+    table = flce.FlceAdamwList()
+    assert flce.lib().flce_adamw_step(ctypes.byref(table), ctypes.byref(o), None, None, A, A, 0,
+                                      None) == code
