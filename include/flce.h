@@ -619,7 +619,8 @@ typedef struct flce_process_options {
    * [offsets[i], offsets[i+1]) of the tokens_size ones (offsets [N+1], within
    * [0, tokens_size] and not decreasing). Padded (tokens_stride > 0, N * tokens_stride
    * <= tokens_size): row i is the first offsets[i] tokens (in [0, tokens_stride]) from
-   * i * tokens_stride on (offsets [N]). Both NULL: no history. */
+   * i * tokens_stride on (offsets [N]). Both NULL: no history. A row has at most 2^31 - 1
+   * tokens; the offsets of a longer one are bad. */
   const int64_t* tokens;
   int64_t tokens_size, tokens_stride;
   const int64_t* offsets;

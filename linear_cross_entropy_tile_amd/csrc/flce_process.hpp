@@ -68,13 +68,14 @@ __device__ __forceinline__ ProcRow proc_row(const ProcArgs& a, int64_t row) {
   if (o.tokens != nullptr) {
     if (o.tokens_stride > 0) {
       const int64_t n = o.offsets[row];
-      r.bad = n < 0 || n > o.tokens_stride;
+      r.bad = n < 0 || n > o.tokens_stride || n > kMostHistory;
       r.begin = row * o.tokens_stride;
       r.end = r.begin + n;
     } else {
       r.begin = o.offsets[row];
       r.end = o.offsets[row + 1];
-      r.bad = r.begin < 0 || r.end < r.begin || r.end > o.tokens_size;
+      r.bad = r.begin < 0 || r.end < r.begin || r.end > o.tokens_size ||
+              r.end - r.begin > kMostHistory;
     }
     const int64_t p = o.prompt_lengths != nullptr ? o.prompt_lengths[row] : 0;
     r.generated = p <= 0 ? r.begin : (p < r.end - r.begin ? r.begin + p : r.end);

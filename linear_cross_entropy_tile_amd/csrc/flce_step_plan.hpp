@@ -148,8 +148,9 @@ inline int proc_history(const flce_process_options_t& o, bool gradient) {
   return o.repetition != nullptr || o.repetition_penalty != 1.0 ? HIST_SEEN : HIST_NONE;
 }
 
-// Rows of longer histories are counted in 32 bits.
-constexpr int64_t kLongHistory = 0x7FFF;
+// Rows of longer histories are counted in 32 bits, of which one is the prompt's; those that
+// are longer than a count are refused.
+constexpr int64_t kLongHistory = 0x7FFF, kMostHistory = 0x7FFFFFFF;
 // Words by which ids of one listed bias wait for each other.
 constexpr int kProcTags = 256;
 // LDS words of a slice: counts, then in their place sums of the listed biases; tags.

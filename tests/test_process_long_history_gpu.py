@@ -119,3 +119,22 @@ def test_what_lies_behind_the_vocabulary_changes_no_result():
     y = got["logits"].double()
     assert torch.equal(got["greedy"], y.argmax(1))
     assert (got["lse"].double() - torch.logsumexp(y, 1)).abs().max() < 2.0 ** -24 * 330
+
+
+def test_the_longest_row_and_a_longer_one():
+    """2^31 - 1 occurrences are counted; a row of one more is refused."""
+    most = (1 << 31) - 1
+    tok = torch.zeros(1, most + 1, dtype=torch.int64, device=DEV)
+    x = torch.ones(1, 3, device=DEV)
+    kw = dict(tokens=tok, frequency_penalty=2.0 ** -20)
+    out = flce.process_logits(x, lengths=torch.tensor([most], device=DEV), **kw)
+    # The count rounds to 2^31 in fp32.
+    assert out["logits"].tolist() == [[1.0 - 2048.0, 1.0, 1.0]] and out["greedy"].item() == 1
+    assert flce.flce_get_status(out["workspace"].data_ptr(), 0) == 0
+    packed = dict(tokens=tok[0], cu_seqlens=torch.tensor([0, most + 1], device=DEV))
+    for history in (dict(tokens=tok, lengths=torch.tensor([most + 1], device=DEV)), packed):
+        out = flce.process_logits(x, frequency_penalty=2.0 ** -20, **history)
+        grad = flce.process_logits_backward(x, x, frequency_penalty=2.0 ** -20, **history)
+        assert flce.flce_get_status(out["workspace"].data_ptr(), 0) == 1
+        assert torch.isnan(out["logits"]).all() and out["greedy"].item() == -1
+        assert torch.isnan(grad).all()
