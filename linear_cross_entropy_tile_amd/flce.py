@@ -1679,7 +1679,7 @@ def adamw_step(params, grads, state, lr=1e-3, beta1: float = 0.9, beta2: float =
     workspace = _workspace(workspace, _ADAMW_BYTES, dev)
     _call(dev, "flce_adamw_step", table, opt, _ptr(lr_device), _ptr(grad_scale),
           step.data_ptr(), workspace.data_ptr(), workspace.numel())
-    _written(params)
+    _written(params if master is None else [*params, *(t for t in master if t is not None)])
 
 
 _ADAMW_BYTES = 512  # flce_adamw_workspace_size()
