@@ -655,7 +655,7 @@ flce_status_t flce_process_workspace_size(int64_t N, int64_t V, size_t* bytes);
 
 /* logits device [N,V] of logits_dtype, row i from element i * ld on (ld >= V); out
  * likewise of out_dtype and ld_out (it may be logits itself, of the same type and
- * ld); lse and entropy device fp32 [N], greedy device int64 [N], each or NULL. All
+ * ld, and shares no memory with it otherwise); lse and entropy device fp32 [N], greedy device int64 [N], each or NULL. All
  * aligned to their elements. Tokens of a history (if there is a penalty) or of listed
  * biases that are neither ignore_index nor in [0, V) are passed over and counted in the
  * status word. A row whose offsets are bad (see above) counts there as one, and its
@@ -705,8 +705,9 @@ flce_status_t flce_grad_norm_workspace_size(const int64_t* sizes, int64_t count,
 
 /* norm (device fp32 [1]) = sqrt(sum of squares) over all values of the count tensors
  * (device, type dtypes[i], aligned to their elements), summed in float64 in a fixed
- * order. scale (device fp32 [1], or NULL) = min(1, max_norm / norm), 1 if max_norm is
- * 0, and NaN if the norm is not finite. */
+ * order. scale (device fp32 [1], or NULL) = min(1, max_norm / norm) of the float64 norm, 1
+ * if max_norm is 0, and NaN if a value is not finite. (Of finite values norm alone can
+ * be above fp32's range, and then is infinite.) */
 flce_status_t flce_grad_norm(const void* const* grads, const int64_t* sizes, const int* dtypes,
                              int64_t count, double max_norm, float* norm, float* scale,
                              void* workspace, size_t workspace_bytes, void* stream);
@@ -763,7 +764,8 @@ size_t flce_adamw_workspace_size(void);
  * magnitude a times 1 / 448 and its codes are those of the values times 448 (1 / a) (all
  * 0 if a is below 2^-100), in fp32; a second moment above 0 has a code above 0.
  * Stochastic rounding goes up with the probability of the part cut off, by 16 bits
- * of a hash of the seed, t, the tensor's index and the value's. */
+ * of a hash of the seed, t, the tensor's index and the value's: lists of a step that are
+ * updated by calls of their own take different seeds, or they draw the same bits. */
 flce_status_t flce_adamw_step(const flce_adamw_list_t* list, const flce_adamw_options_t* opt,
                               const float* lr_device, const float* grad_scale, int64_t* step,
                               void* workspace, size_t workspace_bytes, void* stream);

@@ -14,8 +14,9 @@
 // 590 M values with fp32 states takes 2.44 ms (22 bytes a value, 5.3 TB/s), with 8-bit
 // ones 1.2 ms (10 bytes, 4.9 TB/s), 356 M values in 97 tensors with fp32 copies 1.88 ms
 // (28 bytes, 5.3 TB/s).
-// The norm of 590 M bf16 values takes 250 us (4.7 TB/s), bound by the float64 products:
-// more or smaller chunks, or two loads in flight instead of four, are slower.
+// The norm of 590 M bf16 values takes 200 us by itself (5.9 TB/s) and 245 behind an update
+// that leaves its own values in the caches. The bytes bound it: sums in fp32 take the same
+// 200 us, and more or smaller chunks, or two loads in flight instead of four, more.
 #pragma once
 
 #include <hip/hip_runtime.h>

@@ -41,11 +41,11 @@ inline LogitsPlan make_logits_plan(int64_t N, int64_t H, int64_t V) {
   p.total = kHeaderBytes;
   if (N == 0) return p;
   p.strips = ceil_div(V, kLogitStrip);
-  // More than 64 tokens: larger tiles, unless the product gives the smaller ones less
-  // than 256 blocks, which then share out the hidden dimension too and are faster (H
-  // 4096, tiles and then small ones: 1000 ids x 128 tokens 81 and 18 us, 5000 x 256 86
-  // and 31 us; with more blocks 20000 x 128 92 and 83 us, 20000 x 256 99 and 107 us,
-  // 50264 x 200 127 and 222 us).
+  // More than 64 tokens: larger tiles, unless the product gives the smaller ones less than
+  // 256 blocks, which then share out the hidden dimension too and are faster (H 4096, tiles
+  // and then small ones: 1000 ids x 128 tokens 81 and 18 us, 5000 x 256 86 and 31 us). With
+  // more blocks it depends on how full the tiles are: 20000 x 128, half of each empty, 92
+  // and 83 us, 20000 x 256 99 and 107, 50264 x 200 127 and 222. All of them take tiles.
   const bool large = N > 64 && p.strips * ceil_div(N, 64) >= 256;
   if (large && V % 8 == 0) {
     p.hkb = (int)ceil_div(H, kBK);

@@ -45,7 +45,7 @@ __device__ __forceinline__ void store_any(void* p, const T& v) {
   __builtin_memcpy(p, &v, sizeof(T));
 }
 
-// The same past the caches (nontemporal), for outputs larger than those.
+// The same past the caches (nontemporal).
 template <class T>
 __device__ __forceinline__ void stream_any(void* p, const T& v) {
   typedef T loose __attribute__((aligned(2)));

@@ -1421,7 +1421,7 @@ def process_logits(logits, out_dtype=None, out=None, workspace=None, **options) 
 
     logits: bf16 or fp32 [N,V] (rows may lie apart), e.g. of ``logits``. The
     result has their type or out_dtype ("f32" | "bf16"); out may be logits
-    itself. In row i a logit x of id v becomes
+    itself, and shares no memory with it otherwise. In row i a logit x of id v becomes
       x / repetition if x > 0, else x * repetition   (v anywhere in the history)
       x - frequency * n - (presence if n)            (n: v's count past the prompt)
       x + bias[v] + the row's listed biases of v
@@ -1432,7 +1432,8 @@ def process_logits(logits, out_dtype=None, out=None, workspace=None, **options) 
     the log-probability with which token t is drawn.
 
     Options: the rows' histories as tokens (int64, packed) with cu_seqlens
-    (int64 [N+1]), or as tokens [N, L] with lengths (int64 [N]); prompt_lengths
+    (int64 [N+1]), or as tokens [N, L] with lengths (int64 [N], not looked at if
+    L is 0), at most 2**31 - 1 tokens a row; prompt_lengths
     (int64 [N], None for 0); repetition_penalty = 1, presence_penalty = 0,
     frequency_penalty = 0 and temperature = 1, numbers or fp32 [N]; bias (fp32
     [V] or [N,V]); bias_tokens (int64 [K]), bias_values (fp32 [K]) and
@@ -1561,8 +1562,8 @@ def _dtype_codes(ts, kinds):
 def grad_norm(grads, max_norm: float = 0.0, workspace=None) -> dict:
     """{"norm": fp32 [1], "scale": fp32 [1], "workspace"}: the 2-norm over all
     values of a list of dense bf16 or fp32 tensors (summed in float64), and the
-    factor min(1, max_norm / norm) that clips it (1 without max_norm, NaN if the
-    norm is not finite), for ``adamw_step``'s grad_scale. Both stay on the
+    factor min(1, max_norm / norm) that clips it (1 without max_norm, NaN if a
+    value is not finite), for ``adamw_step``'s grad_scale. Both stay on the
     device."""
     torch = _torch()
     dev, sizes, kinds = _tensors(grads, {torch.bfloat16, torch.float32}, "grads")
@@ -1621,11 +1622,14 @@ def adamw_step(params, grads, state, lr=1e-3, beta1: float = 0.9, beta2: float =
     params and grads: dense bf16 or fp32 tensors of the same sizes, the types in
     any mixture; state: of ``adamw_state``, updated in place, its step raised by
     one; no two tensors of params and state share memory. lr: a number, or fp32
-    [1] on the device (a captured step then follows it). grad_scale: fp32 [1] that the gradients are multiplied by, e.g.
-    ``grad_norm``'s scale; if it is not finite, nothing is changed. Under
-    rounding "stochastic" bf16 parameters without a master copy and 8-bit states
-    are rounded up with the probability of the part cut off, by a hash of seed,
-    the step, the tensor's place in the list and the value's in the tensor.
+    [1] on the device (a captured step then follows it). eps: 0 or at least
+    2**-126. grad_scale: fp32 [1] that the gradients are multiplied by, e.g.
+    ``grad_norm``'s scale; if it is not finite, nothing is changed (without one, a
+    gradient that is not finite makes its weight NaN and loses its states, in 8
+    bits those of its block of 256). Under rounding "stochastic" bf16 parameters
+    without a master copy and 8-bit states are rounded up with the probability of
+    the part cut off, by a hash of seed, the step, the tensor's place in the list
+    and the value's in the tensor (lists updated one by one take different seeds).
     """
     torch = _torch()
     f32 = torch.float32
