@@ -655,11 +655,11 @@ flce_status_t flce_process_workspace_size(int64_t N, int64_t V, size_t* bytes);
 
 /* logits device [N,V] of logits_dtype, row i from element i * ld on (ld >= V); out
  * likewise of out_dtype and ld_out (it may be logits itself, of the same type and
- * ld, and shares no memory with it otherwise); lse and entropy device fp32 [N], greedy device int64 [N], each or NULL. All
- * aligned to their elements. Tokens of a history (if there is a penalty) or of listed
- * biases that are neither ignore_index nor in [0, V) are passed over and counted in the
- * status word. A row whose offsets are bad (see above) counts there as one, and its
- * outputs are NaN and -1. */
+ * ld, and shares no memory with it otherwise); lse and entropy device fp32 [N], greedy
+ * device int64 [N], each or NULL. All aligned to their elements. Tokens of a history (if
+ * there is a penalty) or of listed biases that are neither ignore_index nor in [0, V) are
+ * passed over and counted in the status word. A row whose offsets are bad (see above)
+ * counts there as one, and its outputs are NaN and -1. */
 flce_status_t flce_process_logits(const void* logits, int64_t ld, int64_t N, int64_t V,
                                   const flce_process_options_t* opt, void* out, int64_t ld_out,
                                   float* lse, float* entropy, int64_t* greedy, void* workspace,
